@@ -18,6 +18,10 @@ Functions
 ``chunk_gated_delta_rule``
     The high-level call of the same listing, differentiable through
     ``torch.autograd``: ``(o, final_state)``.
+``gdr_step``, ``gdr_causal_conv_fwd`` / ``_bwd`` / ``_step``, ``gdr_ssm_scan_fwd``,
+``gdr_ssm_step``, ``gdr_rms_norm_fwd`` / ``_bwd``, ``causal_conv``, ``rms_norm``
+    The operators around the rule in a layer, and its form for one new token
+    (the ``layer`` module).
 
 Layouts: q, k [B, T, Hq, K]; v [B, T, Hv, V]; g, beta [B, T, Hv] fp32;
 initial_state [N, Hv, K, V] fp32; cu_seqlens [N + 1] int32 (packed, B = 1).
@@ -35,7 +39,9 @@ import torch
 __all__ = ["gdr_chunk_fwd", "gdr_chunk_fwd_noalloc", "gdr_chunk_bwd", "gdr_chunk_fwd_plan", "fwd_workspace_bytes",
            "bwd_workspace_bytes", "chunk_gated_delta_rule",
            "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd", "Options", "lib_path",
-           "load_library", "GdrError", "timing"]
+           "load_library", "GdrError", "timing",
+           "gdr_step", "gdr_causal_conv_fwd", "gdr_causal_conv_bwd", "gdr_causal_conv_step", "gdr_ssm_scan_fwd",
+           "gdr_ssm_step", "gdr_rms_norm_fwd", "gdr_rms_norm_bwd", "causal_conv", "rms_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -407,3 +413,7 @@ class timing:
             lib.gdr_timing_entry(i, ctypes.byref(name), ctypes.byref(ms), ctypes.byref(cnt))
             out[name.value.decode()] = (ms.value, cnt.value)
         return out
+
+
+from .layer import (causal_conv, gdr_causal_conv_bwd, gdr_causal_conv_fwd, gdr_causal_conv_step,  # noqa: E402
+                    gdr_rms_norm_bwd, gdr_rms_norm_fwd, gdr_ssm_scan_fwd, gdr_ssm_step, gdr_step, rms_norm)

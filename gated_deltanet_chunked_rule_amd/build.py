@@ -19,7 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdr.so")
-SOURCES = ["gdr_api.cpp", "gdr_timing.cpp", "gdr_fwd.hip", "gdr_bwd.hip", "gdr_grads.hip"]
+SOURCES = ["gdr_api.cpp", "gdr_timing.cpp", "gdr_fwd.hip", "gdr_bwd.hip", "gdr_grads.hip",
+           "gdr_layer_api.cpp", "gdr_conv.hip", "gdr_step.hip", "gdr_ssm.hip", "gdr_norm.hip"]
 PEAK_SOURCES = ["gdr_peaks.hip"]
 PEAK_LIB = os.path.join(HERE, "libgdr_peaks.so")
 ARCH = os.environ.get("GDR_OFFLOAD_ARCH", "gfx950")

@@ -14,6 +14,7 @@
 
 #include "../../include/gdr.h"
 #include "gdr_kernels.h"
+#include "gdr_layer.h"
 
 // Workspace of gdr_chunk_fwd_noalloc: device memory owned by the library, one
 // copy per device (each device that loads the library holds it until the
@@ -378,6 +379,18 @@ gdr_status scratch_of_current_device(void** out) {
 }
 
 }  // namespace
+
+namespace gdr {
+
+gdr_status set_error(gdr_status s, const char* msg) noexcept {
+  try {
+    t_err = msg;
+  } catch (...) {   // no memory for the message: the status still stands
+  }
+  return s;
+}
+
+}  // namespace gdr
 
 extern "C" {
 

@@ -1,0 +1,339 @@
+// gdr_norm.hip -- root-mean-square norm with the residual's addition, a gate
+// and an 8-bit output with scales; and its gradient.
+//
+//   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w silu(gate)
+//
+// Bound by memory: TPR lanes hold a whole row in registers (NV vectors of 8
+// values each), so every operand is read once and the row's sum needs no
+// second pass.  The sum is fp32 over the unrounded h.
+#include "gdr_layer.h"
+
+namespace gdr {
+
+typedef uint32_t u32x2_u1 __attribute__((ext_vector_type(2), aligned(1)));
+
+constexpr float kE4M3Max = 448.f;
+constexpr float kQuantTiny = 0x1p-100f;   // an all-zero group gets the scale kQuantTiny / 448
+
+// Sum over the TPR lanes of a row (a power of two, 16 to 1024), the same value
+// on every lane; rows of more than a wave meet in LDS.  Two values at once.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2]) {
+  a = row16_sum(a);
+  b = row16_sum(b);
+#pragma unroll
+  for (int m = 16; m < (TPR < 64 ? TPR : 64); m <<= 1) {
+    a += __shfl_xor(a, m);
+    b += __shfl_xor(b, m);
+  }
+  if constexpr (TPR > 64) {
+    const int w = threadIdx.x >> 6;
+    if (lane_id() == 0) {
+      lds[w][0] = a;
+      lds[w][1] = b;
+    }
+    __syncthreads();
+    const int first = (threadIdx.x / TPR) * (TPR / 64);
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) {
+      a += lds[first + i][0];
+      b += lds[first + i][1];
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
+#define GDR_MAX_STEP(C) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, C, 0xF, 0xF, true))
+  GDR_MAX_STEP(0xB1);
+  GDR_MAX_STEP(0x4E);
+  GDR_MAX_STEP(0x141);
+  GDR_MAX_STEP(0x140);
+#undef GDR_MAX_STEP
+  return v;
+}
+
+__device__ __forceinline__ long row_at(long row, int inner, long outer_stride, long inner_stride) {
+  if (inner == 1) return row * outer_stride;
+  const long o = row / inner;
+  return o * outer_stride + (row - o * inner) * inner_stride;
+}
+
+template <typename T, int TPR, int NV, bool QUANT>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p) {
+  constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+  __shared__ float red[NT / 64][2];
+  const int t = threadIdx.x & (TPR - 1);
+  const long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool live = row < p.rows;   // rows behind the last read row 0 and write nothing
+  const long rr = live ? row : 0;
+  const T* x = static_cast<const T*>(p.x) + row_at(rr, p.inner, p.xo, p.xi);
+  const T* res = p.residual ? static_cast<const T*>(p.residual) + row_at(rr, p.inner, p.ro, p.ri) : nullptr;
+  const T* gate = p.gate ? static_cast<const T*>(p.gate) + row_at(rr, p.inner, p.go, p.gi) : nullptr;
+  typename VecIO<T, 8>::raw raw[NV], rawr[NV], rawg[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int d = (v * TPR + t) * 8;
+    raw[v] = vec_raw<T, 8>(x + d, max(0, p.dim - d));
+    if (res) rawr[v] = vec_raw<T, 8>(res + d, max(0, p.dim - d));
+    if (gate) rawg[v] = vec_raw<T, 8>(gate + d, max(0, p.dim - d));
+  }
+  float h[NV][8], ss = 0.f, unused = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    VecIO<T, 8>::up(raw[v], h[v]);
+    if (res) {
+      float f[8];
+      VecIO<T, 8>::up(rawr[v], f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) h[v][c] += f[c];
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) ss = fmaf(h[v][c], h[v][c], ss);
+  }
+  row_sum2<TPR>(ss, unused, red);
+  const float r = 1.f / sqrtf(ss / (float)p.dim + p.eps);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+    if (p.h_out && live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.h_out) + row * p.dim + d, nd, h[v]);
+    float w[8], y[8];
+    vec_load<T, 8>(static_cast<const T*>(p.weight) + d, max(0, nd), w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) y[c] = h[v][c] * r * w[c];
+    if (gate) {
+      float g[8];
+      VecIO<T, 8>::up(rawg[v], g);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) y[c] *= g[c] * sigmoid_f(g[c]);
+    }
+    if constexpr (QUANT) {
+      // a group of 128 values is 16 lanes of 8; the largest magnitude is taken
+      // on the bits, where a NaN is above everything
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) m = max(m, c < nd ? (__builtin_bit_cast(uint32_t, y[c]) & 0x7fffffffu) : 0u);
+      m = max16_u32(m);
+      m = max(m, __builtin_bit_cast(uint32_t, kQuantTiny));
+      const float scale = __builtin_bit_cast(float, m) / kE4M3Max;
+      if (nd <= 0 || !live) continue;
+      // true division: the value that is rounded is y / scale to half an ulp
+      // (the kernel stays bound by memory), clamped so that the largest one
+      // cannot pass 448 (fminf and fmaxf would drop a NaN, these compares keep it)
+      int q[2] = {0, 0};
+      float f[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        f[c] = y[c] / scale;
+        f[c] = f[c] > kE4M3Max ? kE4M3Max : f[c] < -kE4M3Max ? -kE4M3Max : f[c];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);
+        q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], q[i], true);
+      }
+      uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.dim + d;
+      if (nd == 8) {
+        *reinterpret_cast<u32x2_u1*>(out) = u32x2_u1{(uint32_t)q[0], (uint32_t)q[1]};
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < nd) out[c] = (uint8_t)((uint32_t)q[c / 4] >> (8 * (c % 4)));
+      }
+      if ((t & 15) == 0) p.scales[row * ((p.dim + 127) / 128) + d / 128] = scale;
+    } else {
+      if (nd > 0 && live) vec_store<T, 8>(static_cast<T*>(p.y) + row * p.dim + d, nd, y);
+    }
+  }
+}
+
+// Gradient at h:  u = dy silu(gate) w,  dh = r (u - n mean(u n)) + d_res with
+// n = h r;  dw = sum of dy silu(gate) n over the rows;  dgate = dy n w silu'.
+// Persistent workgroups keep their rows' sums for dw in registers and leave
+// one partial row each; a second kernel adds those in order.
+template <typename T, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p) {
+  constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+  __shared__ float red[2][NT / 64][2];
+  __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NV * 8 : 1];
+  const int t = threadIdx.x & (TPR - 1), sub = threadIdx.x / TPR;
+  float dw[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) dw[v][c] = 0.f;
+  const float inv = 1.f / (float)p.dim;
+  int buf = 0;
+  // every thread of the workgroup makes the same number of steps (barriers)
+  for (long base = (long)blockIdx.x * RPB; base < p.rows; base += (long)gridDim.x * RPB, buf ^= 1) {
+    const long row = base + sub;
+    const bool live = row < p.rows;
+    const long rr = live ? row : 0;
+    const T* h = static_cast<const T*>(p.x) + row_at(rr, p.inner, p.xo, p.xi);
+    const T* dy = static_cast<const T*>(p.dy) + rr * p.dim;
+    const T* gate = p.gate ? static_cast<const T*>(p.gate) + row_at(rr, p.inner, p.go, p.gi) : nullptr;
+    const T* dres = p.dres ? static_cast<const T*>(p.dres) + rr * p.dim : nullptr;
+    typename VecIO<T, 8>::raw hr[NV], gr[NV], zr[NV], sr[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = (v * TPR + t) * 8, nd = max(0, p.dim - d);
+      hr[v] = vec_raw<T, 8>(h + d, nd);
+      gr[v] = vec_raw<T, 8>(dy + d, nd);
+      if (gate) zr[v] = vec_raw<T, 8>(gate + d, nd);
+      if (dres) sr[v] = vec_raw<T, 8>(dres + d, nd);
+    }
+    float ss = 0.f, su = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = (v * TPR + t) * 8;
+      float hf[8], g[8], w[8];
+      VecIO<T, 8>::up(hr[v], hf);
+      VecIO<T, 8>::up(gr[v], g);
+      vec_load<T, 8>(static_cast<const T*>(p.weight) + d, max(0, p.dim - d), w);
+      if (gate) {
+        float z[8];
+        VecIO<T, 8>::up(zr[v], z);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) g[c] *= z[c] * sigmoid_f(z[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        ss = fmaf(hf[c], hf[c], ss);
+        su = fmaf(g[c] * w[c], hf[c], su);
+      }
+    }
+    row_sum2<TPR>(ss, su, red[buf]);   // two buffers: the next step's sums do not meet this step's readers
+    const float r = 1.f / sqrtf(ss * inv + p.eps);
+    const float m = su * r * inv;      // mean(u n)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+      float hf[8], g[8], w[8], o[8];
+      VecIO<T, 8>::up(hr[v], hf);
+      VecIO<T, 8>::up(gr[v], g);
+      vec_load<T, 8>(static_cast<const T*>(p.weight) + d, max(0, nd), w);
+      if (gate) {
+        float z[8], dz[8];
+        VecIO<T, 8>::up(zr[v], z);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float s = sigmoid_f(z[c]);
+          dz[c] = g[c] * hf[c] * r * w[c] * (s * fmaf(z[c], 1.f - s, 1.f));
+          g[c] *= z[c] * s;
+        }
+        if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dgate) + row * p.dim + d, nd, dz);
+      }
+      float s[8];
+      if (dres) VecIO<T, 8>::up(sr[v], s);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float n = hf[c] * r;
+        o[c] = r * (g[c] * w[c] - n * m) + (dres ? s[c] : 0.f);
+        dw[v][c] += live ? g[c] * n : 0.f;
+      }
+      if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dh) + row * p.dim + d, nd, o);
+    }
+  }
+  float* part = p.part + (long)blockIdx.x * p.dim;
+  if constexpr (RPB > 1) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) fold[sub][(v * TPR + t) * 8 + c] = dw[v][c];
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.dim; d += NT) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < RPB; ++i) s += fold[i][d];
+      part[d] = s;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+      if (nd > 0) vec_store<float, 8>(part + d, nd, dw[v]);
+    }
+  }
+}
+
+// dw: the workgroups' partial rows, in 16 strands of every 16th that are then
+// added in order; 16 columns per workgroup keep many workgroups busy at the
+// usual widths.
+template <typename T>
+__global__ __launch_bounds__(256) void k_norm_dw(NormParams p) {
+  __shared__ float acc[16][17];
+  const int c = threadIdx.x & 15, strand = threadIdx.x >> 4;
+  const int d = blockIdx.x * 16 + c;
+  float s = 0.f;
+  if (d < p.dim)
+    for (int b = strand; b < p.blocks; b += 16) s += p.part[(long)b * p.dim + d];
+  acc[strand][c] = s;
+  __syncthreads();
+  if (strand != 0 || d >= p.dim) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += acc[i][c];
+  static_cast<T*>(p.dw)[d] = from_f<T>(s);
+}
+
+// Lanes per row and vectors per lane by the row's length.
+#define NORM_DISPATCH(CALL)                    \
+  if (p.dim <= 128) { CALL(16, 1); }           \
+  else if (p.dim <= 256) { CALL(32, 1); }      \
+  else if (p.dim <= 512) { CALL(64, 1); }      \
+  else if (p.dim <= 1024) { CALL(128, 1); }    \
+  else if (p.dim <= 2048) { CALL(256, 1); }    \
+  else if (p.dim <= 4096) { CALL(256, 2); }    \
+  else if (p.dim <= 8192) { CALL(512, 2); }    \
+  else { CALL(1024, 2); }
+
+template <typename T, bool QUANT>
+static hipError_t norm_fwd(const NormParams& p, hipStream_t st) {
+  timing_before("norm_fwd", st);
+#define CALL(TPR, NV)                                                                                              \
+  hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, QUANT>),                                                              \
+                     dim3((unsigned)((p.rows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))), \
+                     dim3(TPR < 256 ? 256 : TPR), 0, st, p)
+  NORM_DISPATCH(CALL);
+#undef CALL
+  const hipError_t e = hipGetLastError();
+  timing_after(st);
+  return e;
+}
+hipError_t launch_norm_fwd(DType dt, bool quant, const NormParams& p, hipStream_t st) {
+  if (dt == DType::BF16) return quant ? norm_fwd<bf16, true>(p, st) : norm_fwd<bf16, false>(p, st);
+  return quant ? norm_fwd<float, true>(p, st) : norm_fwd<float, false>(p, st);
+}
+
+// Workgroups of the backward: enough to fill the GPU's waves (8 workgroups of
+// 4 waves a compute unit), fewer where the rows end first.
+static int norm_rows_per_block(int dim) { return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 512 ? 4 : dim <= 1024 ? 2 : 1; }
+int norm_bwd_blocks(long rows, int dim) {
+  const long want = dim <= 4096 ? 4 * kComputeUnits : dim <= 8192 ? 2 * kComputeUnits : kComputeUnits;
+  const long most = (rows + norm_rows_per_block(dim) - 1) / norm_rows_per_block(dim);
+  return (int)(most < want ? most : want);
+}
+template <typename T>
+static hipError_t norm_bwd(const NormParams& p, hipStream_t st) {
+  hipError_t e = hipSuccess;
+  if (p.blocks > 0) {
+    timing_before("norm_bwd", st);
+#define CALL(TPR, NV) \
+  hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV>), dim3((unsigned)p.blocks), dim3(TPR < 256 ? 256 : TPR), 0, st, p)
+    NORM_DISPATCH(CALL);
+#undef CALL
+    e = hipGetLastError();
+    timing_after(st);
+    if (e != hipSuccess) return e;
+  }
+  timing_before("norm_dw", st);
+  hipLaunchKernelGGL(k_norm_dw<T>, dim3((unsigned)((p.dim + 15) / 16)), dim3(256), 0, st, p);
+  e = hipGetLastError();
+  timing_after(st);
+  return e;
+}
+hipError_t launch_norm_bwd(DType dt, const NormParams& p, hipStream_t st) {
+  return dt == DType::BF16 ? norm_bwd<bf16>(p, st) : norm_bwd<float>(p, st);
+}
+
+}  // namespace gdr

@@ -217,6 +217,154 @@ gdr_status gdr_chunk_bwd(const gdr_shape* shape, const gdr_options* opts,
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* gdr_last_error(void);
 
+/* ==== the operators around the rule in a linear-attention layer ============
+ * The short causal convolution in front of the mixer, the rule's form for one
+ * new token, the selective state space scan (the mixer's sibling without the
+ * delta term, for layers of that kind in one model), and the root-mean-square
+ * norm before and after the mixer.
+ *
+ * They share the conventions above, with these differences:
+ * Strides: an operand marked "strided" may be a slice of a wider row: its
+ *   token stride is given in elements (0: dense).  Tokens of a batch are
+ *   numbered b * T + t through one stride.
+ * Alignment: tensors need the alignment of their elements only, except where
+ *   16-byte rows are asked for (the scan and the steps).
+ * Sequences: cu_seqlens is read on the device only; no host copy is needed
+ *   and a captured graph may be replayed with other offsets.  It must be
+ *   non-decreasing; offsets are clamped to [0, T], so that no value of it can
+ *   make a kernel leave its buffers.  Tokens before cu_seqlens[0] or from
+ *   cu_seqlens[N] on belong to no sequence: their output rows (and input
+ *   gradients) are zero.  Empty sequences are allowed; their final state is
+ *   their initial state.
+ * State pools (the steps): state holds num_slots states; row r works on slot
+ *   slots[r] (slots NULL: slot r, rows <= num_slots), in place.  A row whose
+ *   slot is outside [0, num_slots), or was named by an earlier row of the same
+ *   call, is padding: its output row is zero and no state changes.
+ * Non-finite inputs propagate as in the formulas; in the scan one may also
+ *   reach the outputs of the same heads up to 63 tokens before it in its own
+ *   sequence (the products of a chunk multiply it with the zeros above the
+ *   diagonal).  It never reaches another sequence. */
+
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
+
+/* ---- short causal convolution ----------------------------------------------
+ *   z_t = bias + sum_{j < W} weight[:, j] * x_{t - W + 1 + j},  y_t = act(z_t)
+ * per channel; inputs before a sequence's first token are the rows of its
+ * initial state (zeros without one).  Sums are fp32. */
+typedef struct {
+  int32_t B, T;               /* as in gdr_shape */
+  int32_t D, W;               /* channels; taps, 2 to 4 */
+  int32_t num_seqs;           /* N in packed mode; ignored otherwise */
+  gdr_dtype dtype;            /* of x, weight, bias, states, y and the gradients */
+  gdr_activation activation;
+  int64_t x_stride;           /* elements between tokens of x (0: D) */
+} gdr_conv_shape;
+
+/*   x              [B, T, D], strided;  weight [D, W];  bias [D], nullable
+ *   initial_state  [N, W - 1, D], nullable: the W - 1 inputs before each sequence, oldest first
+ *   y              [B, T, D] dense
+ *   final_state    [N, W - 1, D], nullable: the last W - 1 inputs (reaching into the initial state) */
+gdr_status gdr_causal_conv_fwd(const gdr_conv_shape* shape, const void* x, const void* weight, const void* bias,
+                               const void* initial_state, const int32_t* cu_seqlens, void* y, void* final_state,
+                               void* stream);
+
+/* Bytes of device workspace gdr_causal_conv_bwd needs (0 on invalid arguments). */
+size_t gdr_causal_conv_bwd_workspace_size(const gdr_conv_shape* shape);
+
+/* Gradients of <y, dy> + <final_state, dht>.  dy dense; dht nullable.  dx is
+ * [B, T, D] dense; dw [D, W], db [D] (nullable) and dh0 [N, W - 1, D]
+ * (nullable) have the call's dtype, each rounded once from an fp32 sum that is
+ * added in a fixed order. */
+gdr_status gdr_causal_conv_bwd(const gdr_conv_shape* shape, const void* x, const void* weight, const void* bias,
+                               const void* initial_state, const int32_t* cu_seqlens, const void* dy,
+                               const void* dht, void* dx, void* dw, void* db, void* dh0, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* One new token per row: x [rows, D] strided, y [rows, D]; state
+ * [num_slots, W - 1, D] moves on by one input.  shape: B = rows, T = 1. */
+gdr_status gdr_causal_conv_step(const gdr_conv_shape* shape, const void* x, const void* weight, const void* bias,
+                                void* state, int32_t num_slots, const int32_t* slots, void* y, void* stream);
+
+/* ---- gated delta rule, one new token per row -------------------------------
+ *   S = exp(g) S;  S += k (beta (v - S^T k))^T;  o = scale S^T q
+ * shape: B = rows, T = 1; q, k [rows, Hq, K], v, o [rows, Hv, V], g, beta
+ * [rows, Hv] fp32; state [num_slots, Hv, K, V] fp32, in place.  bf16 and fp32,
+ * K = V in {32, 64, 128} for both.  q_stride, k_stride, v_stride: elements
+ * between rows (0: dense); rows and state must be 16-byte aligned. */
+gdr_status gdr_step(const gdr_shape* shape, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, const float* g, const float* beta, float scale, float* state,
+                    int32_t num_slots, const int32_t* slots, void* o, void* stream);
+
+/* ---- selective state space scan (inference) --------------------------------
+ *   d_t = dt_t + dt_bias, through softplus if dt_softplus
+ *   S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T,   y_t = S_t^T C_t + D x_t
+ * per head, with an fp32 [N, P] state; head h reads group h / (H / G) of B and
+ * C.  No gradient is offered. */
+typedef struct {
+  int32_t B, T;               /* as in gdr_shape */
+  int32_t H, G;               /* heads; groups of B and C (H % G == 0) */
+  int32_t P, N;               /* head dimension and state size: 32, 64 or 128 each */
+  int32_t num_seqs;           /* sequences in packed mode; ignored otherwise */
+  gdr_dtype dtype;            /* of x, dt, B, C and y */
+  int32_t dt_softplus;        /* 0 or 1 */
+  int64_t x_stride, dt_stride, b_stride, c_stride;  /* elements between tokens (0: dense) */
+} gdr_ssm_shape;
+
+/* Bytes of device workspace gdr_ssm_scan_fwd needs (0 on invalid arguments). */
+size_t gdr_ssm_scan_fwd_workspace_size(const gdr_ssm_shape* shape);
+
+/*   x [B, T, H, P], dt [B, T, H], B, C [B, T, G, N]: strided; the rows of x, B and C 16-byte aligned
+ *   A [H] fp32;  D, dt_bias [H] fp32, nullable
+ *   initial_state, final_state   [num_seqs or B, H, N, P] fp32, nullable
+ *   y [B, T, H, P] dense */
+gdr_status gdr_ssm_scan_fwd(const gdr_ssm_shape* shape, const void* x, const void* dt, const float* A,
+                            const void* B, const void* C, const float* D, const float* dt_bias,
+                            const float* initial_state, const int32_t* cu_seqlens, void* y, float* final_state,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* One new token per row (shape: B = rows, T = 1); state [num_slots, H, N, P]
+ * fp32, in place. */
+gdr_status gdr_ssm_step(const gdr_ssm_shape* shape, const void* x, const void* dt, const float* A, const void* B,
+                        const void* C, const float* D, const float* dt_bias, float* state, int32_t num_slots,
+                        const int32_t* slots, void* y, void* stream);
+
+/* ---- root-mean-square norm --------------------------------------------------
+ *   h = x (+ residual),  y = h / sqrt(mean(h^2) + eps) * weight (* gate sigmoid(gate))
+ * over rows of dim values (dim <= 16384), statistics in fp32.  Row r of a
+ * strided operand starts (r / inner) * outer_stride + (r % inner) * inner_stride
+ * elements behind its pointer (both strides 0: dense), so that [tokens, heads,
+ * dim] slices of a wider row can be given as they are. */
+typedef struct { int64_t outer, inner; } gdr_row_stride;
+typedef struct {
+  int64_t rows;
+  int32_t inner;              /* rows per outer step (heads), >= 1; rows % inner == 0 */
+  int32_t dim;
+  gdr_dtype dtype;            /* of x, residual, gate, weight, 16- or 32-bit outputs and gradients */
+  float eps;                  /* >= 0 */
+  int32_t quant;              /* 1: y in 8 bits (e4m3) with an fp32 scale for each 128 values of a row */
+  gdr_row_stride x_stride, residual_stride, gate_stride;
+} gdr_norm_shape;
+
+/*   y             [rows, dim] of the call's dtype, or with quant one byte per value:
+ *                 y = e4m3 value * scale, scale = max(max |y| of the group, 2^-100) / 448;
+ *                 the last group of a row may be short.  A group with a NaN is NaN.
+ *   scales        [rows, ceil(dim / 128)] fp32 (quant only)
+ *   residual_out  [rows, dim] dense: h rounded to the call's dtype; nullable without residual.
+ *                 It may be the residual or x itself where that is dense. */
+gdr_status gdr_rms_norm_fwd(const gdr_norm_shape* shape, const void* x, const void* residual, const void* gate,
+                            const void* weight, void* y, float* scales, void* residual_out, void* stream);
+
+/* Bytes of device workspace gdr_rms_norm_bwd needs (0 on invalid arguments). */
+size_t gdr_rms_norm_bwd_workspace_size(const gdr_norm_shape* shape);
+
+/* Gradients of <y, dy> + <h, d_res> at h (x_stride is its stride): dh [rows,
+ * dim] dense (the gradient of x and of residual), dw [dim] and dgate [rows,
+ * dim] dense (with a gate), in the call's dtype.  d_res nullable; dy and d_res
+ * dense; shape->quant and residual_stride are ignored.  dw is added in a fixed order. */
+gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const void* gate, const void* weight,
+                            const void* dy, const void* d_res, void* dh, void* dw, void* dgate, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* ---- kernel timing (diagnostics) ------------------------------------------
  * When enabled, every kernel the library enqueues is bracketed by a pair of
  * HIP events recorded on the launch stream.  gdr_timing_collect() waits for
