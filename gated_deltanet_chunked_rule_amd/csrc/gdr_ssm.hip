@@ -9,11 +9,11 @@
 // Every decay is the exponential of a difference of gam, so that strong gates
 // underflow to zero instead of dividing by it.
 //
-// A workgroup of 4 waves takes 128 channels (x columns of one group's heads)
-// and one segment of the token axis; a wave owns 32 of them, within one head,
-// with its [N, 32] block of the state in fp32 accumulators.  The scores C B^T
-// of a chunk are the same for every head of the group: the waves share their
-// computation and each applies its own head's decays.
+// A workgroup takes one segment of the token axis and 32 channels (x columns of
+// one group's heads) for each of its waves; a wave's channels lie within one
+// head, and it keeps their [N, 32] block of the state in fp32 accumulators.
+// The scores C B^T of a chunk are the same for every head of the group: the
+// waves share their computation and each applies its own head's decays.
 //
 // Long prompts are cut into segments that run side by side: a first pass
 // computes what each segment adds to the state and its decay, k_ssm_join
@@ -25,23 +25,27 @@
 namespace gdr {
 
 constexpr int SC = 64;        // chunk
-constexpr int SCOLS = 128;    // channels of a workgroup
 
-// A contraction block of 32: lane group q = lane / 16 holds the indices
-// 16 (e / 4) + 4 q + e % 4, e < 8, on both operands -- the order in which two
-// accumulator tiles, one above the other, hold their rows.
+// Staged tiles: SC rows of NCH 16-byte pieces, unpadded (they are filled by
+// direct global -> LDS copies); piece c of row r stands at c ^ ssm_swz(r),
+// which takes the low four bits of r only.
+template <typename T, int NCH>
+__device__ __forceinline__ int ssm_swz(int r) {
+  if constexpr (sizeof(T) == 4) return r & (NCH < 16 ? NCH - 1 : 15);
+  else return stage_swz<NCH>(r & 15);
+}
+
+// A contraction block of 32 indices.  Over the state (n): lane group
+// q = lane / 16 holds n = 8 q + e, e < 8, a contiguous piece of a row of B or
+// C; the two accumulator tiles of the block hold n = 8 q + 4 u + e % 4 in tile
+// u, so that their registers are the other operand as they stand.  Over the
+// tokens (j): lane group q holds j = 16 (e / 4) + 4 q + e % 4, the rows of two
+// score tiles, one above the other.
 template <typename T> struct Blk;
 template <> struct Blk<bf16> {
   typedef bf16x8 frag;
   static __device__ __forceinline__ f32x4 mma(frag a, frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  // the contraction runs along an LDS row
-  static __device__ __forceinline__ frag along(const bf16* row) { return ld_a2(row, 4 * (lane_id() >> 4)); }
-  // the contraction runs down the rows r0.., operand index = column
-  static __device__ __forceinline__ frag down(const bf16* m, int pitch, int r0, int c0) {
-    const int r = r0 + 4 * (lane_id() >> 4);
-    return cat4(tr4(m, pitch, r, c0), tr4(m, pitch, r + 16, c0));
   }
   static __device__ __forceinline__ frag acc(const f32x4& x, const f32x4& y) { return pack_b(x, y); }
   static __device__ __forceinline__ float get(const frag& f, int e) { return static_cast<float>(f[e]); }
@@ -53,80 +57,149 @@ template <> struct Blk<float> {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
     return c;
   }
-  static __device__ __forceinline__ frag along(const float* row) {
-    const float* p = row + 4 * (lane_id() >> 4);
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 16);
-    return frag{{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
-  }
-  static __device__ __forceinline__ frag down(const float* m, int pitch, int r0, int c0) {
-    const float* p = m + (r0 + 4 * (lane_id() >> 4)) * pitch + c0 + (lane_id() & 15);
-    frag f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = p[(16 * (e / 4) + e % 4) * pitch];
-    return f;
-  }
   static __device__ __forceinline__ frag acc(const f32x4& x, const f32x4& y) {
     return frag{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
   }
   static __device__ __forceinline__ float get(const frag& f, int e) { return f.v[e]; }
 };
 
-// 64 rows of COLS elements, global -> registers -> LDS; rows from `rows` on
-// and columns from `cols` on read as zero.
-template <typename T, int COLS>
-struct ChunkRegs {
-  static constexpr int VEC = 16 / (int)sizeof(T), VPR = COLS / VEC, NV = SC * VPR / 256;
-  static constexpr int PITCH = COLS + VEC;
-  uint4 v[NV];
-  __device__ __forceinline__ void load(const T* base, long stride, int rows, int cols) {
-    const rsrc_t r = make_rsrc_u(base, ((long)(rows - 1) * stride + cols) * (long)sizeof(T));
+// Operand reads from staged tiles.  A lane's byte address is its row's start
+// plus (constant of the block) ^ (constant of the lane), and constant row
+// steps that the instruction's offset holds: a few registers for all of them.
+template <typename T, int NB, int NX> struct Reader;
+template <int NB, int NX> struct Reader<bf16, NB, NX> {
+  int arow, ax, brow, bx, xrow, xx, srow, sx;
+  __device__ __forceinline__ Reader(int w) {
+    const int l = lane_id(), c = l & 15, q = l >> 4, r = 4 * q + (c >> 2), s = c & 3, wx = 64 * (w & 3);
+    arow = c * NB * 16;
+    ax = 16 * (q ^ ssm_swz<bf16, NB>(c));
+    brow = r * NB * 16;
+    bx = 16 * (s ^ ssm_swz<bf16, NB>(r));
+    xrow = r * NX * 16 + 8 * (s & 1);
+    xx = wx ^ (16 * ((s >> 1) ^ ssm_swz<bf16, NX>(r)));
+    srow = c * NX * 16 + 8 * (q & 1);
+    sx = wx ^ (16 * ((q >> 1) ^ ssm_swz<bf16, NX>(c)));
+  }
+  // n along row 16 it + c
+  __device__ __forceinline__ bf16x8 along(const bf16* t, int it, int kb) const {
+    return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(t) + arow + ((64 * kb) ^ ax) + it * 256 * NB);
+  }
+  static __device__ __forceinline__ bf16x8 tr(const char* a, int step) {
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    return cat4(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)a), __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(a + step)));
+  }
+  // tokens of block jb down the columns 32 kb + 8 (c / 4) + 4 u + c % 4
+  __device__ __forceinline__ bf16x8 down_b(const bf16* t, int jb, int kb, int u) const {
+    return tr(reinterpret_cast<const char*>(t) + brow + ((64 * kb) ^ bx) + 8 * u + jb * 512 * NB, 256 * NB);
+  }
+  // and down this wave's columns 16 pt + c
+  __device__ __forceinline__ bf16x8 down_x(const bf16* t, int jb, int pt) const {
+    return tr(reinterpret_cast<const char*>(t) + xrow + ((32 * pt) ^ xx) + jb * 512 * NX, 256 * NX);
+  }
+  // columns 16 pt + 4 q .. + 3 of row 16 it + c
+  __device__ __forceinline__ f32x4 at(const bf16* t, int it, int pt) const {
+    const bf16x4 v = *reinterpret_cast<const bf16x4*>(reinterpret_cast<const char*>(t) + srow + ((32 * pt) ^ sx) + it * 256 * NX);
+    return f32x4{static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]), static_cast<float>(v[3])};
+  }
+};
+template <int NB, int NX> struct Reader<float, NB, NX> {
+  typedef Blk<float>::frag frag;
+  int arow, ax, brow, bx, xx, xrow, srow, sx;
+  __device__ __forceinline__ Reader(int w) {
+    const int l = lane_id(), c = l & 15, q = l >> 4, wx = 128 * (w & 3);
+    arow = c * NB * 16;
+    ax = 16 * ((2 * q) ^ ssm_swz<float, NB>(c));
+    brow = 4 * q * NB * 16 + 4 * (c & 3);
+    bx = 16 * ((2 * (c >> 2)) ^ ssm_swz<float, NB>(4 * q));
+    xrow = 4 * q * NX * 16 + 4 * (c & 3);
+    xx = wx ^ (16 * ((c >> 2) ^ ssm_swz<float, NX>(4 * q)));
+    srow = c * NX * 16;
+    sx = wx ^ (16 * (q ^ ssm_swz<float, NX>(c)));
+  }
+  __device__ __forceinline__ frag along(const float* t, int it, int kb) const {
+    const char* p = reinterpret_cast<const char*>(t) + arow + it * 256 * NB;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(p + ((128 * kb) ^ ax)), hi = *reinterpret_cast<const f32x4*>(p + ((128 * kb + 16) ^ ax));
+    return Blk<float>::acc(lo, hi);
+  }
+  // row 4 q + 16 (e / 4) + e % 4 of a block: its swizzle is that of 4 q, ^ e % 4
+  static __device__ __forceinline__ frag rows(const char* p, int x, int pitch) {
+    frag f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = *reinterpret_cast<const float*>(p + (x ^ (16 * (e % 4))) + (16 * (e / 4) + e % 4) * pitch);
+    return f;
+  }
+  __device__ __forceinline__ frag down_b(const float* t, int jb, int kb, int u) const {
+    return rows(reinterpret_cast<const char*>(t) + brow + jb * 512 * NB, (128 * kb + 16 * u) ^ bx, NB * 16);
+  }
+  __device__ __forceinline__ frag down_x(const float* t, int jb, int pt) const {
+    return rows(reinterpret_cast<const char*>(t) + xrow + jb * 512 * NX, (64 * pt) ^ xx, NX * 16);
+  }
+  __device__ __forceinline__ f32x4 at(const float* t, int it, int pt) const {
+    return *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(t) + srow + ((64 * pt) ^ sx) + it * 256 * NX);
+  }
+};
+
+// One wave's share of a tile's copy: blocks w, w + NW, ... of 64 pieces.
+// Offsets are per lane and the same for every chunk; columns from `cols` on
+// point behind any buffer and read as zero, as do rows behind the descriptor.
+template <typename T, int NCH, int NW>
+struct TileCopy {
+  static constexpr int VEC = 16 / (int)sizeof(T), BLOCKS = SC * NCH / 64, NV = (BLOCKS + NW - 1) / NW;
+  uint32_t off[NV];
+  __device__ __forceinline__ void plan(long stride, int cols) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int idx = (int)threadIdx.x + 256 * i, row = idx / VPR, c = (idx % VPR) * VEC;
-      const uint32_t off = (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(T);
-      v[i] = buf_load16(r, (row < rows && c < cols) ? off : 0x80000000u);
+      const int p = 64 * (wave_id() + NW * i) + lane_id(), r = p / NCH, c = (p % NCH) ^ ssm_swz<T, NCH>(r);
+      off[i] = c * VEC < cols ? (uint32_t)(r * (int)stride + c * VEC) * (uint32_t)sizeof(T) : 0x80000000u;
     }
   }
-  __device__ __forceinline__ void store(T* lds) const {
+  __device__ __forceinline__ void issue(T* lds, const T* base, long stride, int rows, int cols) const {
+    const i32x4v rs = rsrc_words(base, ((long)(rows - 1) * stride + cols) * (long)sizeof(T));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int idx = (int)threadIdx.x + 256 * i;
-      *reinterpret_cast<uint4*>(lds + (idx / VPR) * PITCH + (idx % VPR) * VEC) = v[i];
+      const int blk = wave_id() + NW * i;
+      if (BLOCKS % NW == 0 || blk < BLOCKS) lds_copy16(rs, off[i], lds_addr(lds + 64 * blk * VEC));
     }
   }
 };
 
-template <typename T, int ND, bool OUT>
+template <typename T, int ND, int NW, bool OUT>
 struct SsmLds {
-  static constexpr int PB = ChunkRegs<T, ND>::PITCH, PX = ChunkRegs<T, SCOLS>::PITCH;
-  T b[SC * PB];
-  T c[OUT ? SC * PB : 4];
-  T x[SC * PX];
+  static constexpr int VEC = 16 / (int)sizeof(T);
+  static constexpr int NB = ND / VEC, NX = 128 / VEC;              // pieces of a row of B or C, of x (128 channels)
+  static constexpr int XT = NW / 4;                                // x tiles of 128 channels
+  static constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;              // fp32 fills the LDS with one
+  T b[NBUF][SC * ND];
+  T x[NBUF][XT][SC * 128];
+  T c[OUT ? NBUF : 1][OUT ? SC * ND : 8];
   f32x4 score[OUT ? 10 * 64 : 1];   // tiles (jt <= it) of B C^T, by lane
   // per wave, its head's tokens: gam as a float (and its remainder, fp32), d,
-  // e^gam, and the weight of the token in the chunk's end state
-  float gam[4][SC], rem[sizeof(T) == 4 ? 4 : 1][SC], d[4][SC], eg[4][SC], wt[4][SC];
+  // e^gam, and two weights: of the token at its 16-token tile's end, and in
+  // the chunk's end state
+  float gam[OUT ? NW : 1][SC], rem[OUT && sizeof(T) == 4 ? NW : 1][SC], d[OUT ? NW : 1][SC], eg[OUT ? NW : 1][SC];
+  float ut[OUT ? NW : 1][SC], wt[NW][SC];
   int32_t cu[kCuLds];
 };
 
-template <typename T, int ND, bool OUT>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p, int total) {
+template <typename T, int ND, int NW, bool OUT>
+__global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   typedef Blk<T> K;
   typedef typename K::frag frag;
-  constexpr int NT = ND / 16, NK = ND / 32;
-  __shared__ __align__(16) SsmLds<T, ND, OUT> lds;
-  constexpr int PB = lds.PB, PX = lds.PX;
+  typedef SsmLds<T, ND, NW, OUT> Lds;
+  constexpr int NK = ND / 32, NB = Lds::NB, NX = Lds::NX, COLS = 32 * NW;
+  constexpr bool F32 = sizeof(T) == 4;
+  __shared__ __align__(16) Lds lds;
   // workgroups of one segment share B and C: keep them on one XCD
   const int id = xcd_remap(blockIdx.x, total);
   if (id >= total) return;
   const SeqFinder sf = seq_finder(p.s, lds.cu);
   const int hp = p.H / p.G * p.P;                       // channels of a group
-  const int per_group = (hp + SCOLS - 1) / SCOLS;
+  const int per_group = (hp + COLS - 1) / COLS;
   const int seg = id / p.wgs, wi = id - seg * p.wgs;
-  const int g = wi / per_group, col0 = (wi - g * per_group) * SCOLS;
-  const int cols = min(SCOLS, hp - col0);
+  const int g = wi / per_group, col0 = (wi - g * per_group) * COLS;
+  const int cols = min(COLS, hp - col0);
   const int w = wave_id(), l = lane_id(), c = l & 15, q = l >> 4;
-  const bool live = 32 * w < cols;                      // waves without channels still help with tiles and scores
+  const bool live = 32 * w < cols;                      // waves without channels still help with copies and scores
   const int chan0 = g * hp + col0;                      // the workgroup's first channel
   const int chan = chan0 + (live ? 32 * w : 0);
   const int head = chan / p.P, pc = chan - head * p.P;
@@ -140,25 +213,26 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p
   const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
   const float skip = OUT && p.D ? p.D[head] : 0.f;
 
-  f32x4 h[NT][2];
+  // element e of tile h[kb][u][pt]: state row 32 kb + 8 q + 4 u + e, column 16 pt + c
+  f32x4 h[NK][2][2];
   auto state_at = [&](const float* s) { return s + (long)head * sstride + pc; };
-  // accumulator element e of tile (nt, pt): state row 16 nt + 4 q + e, column 16 pt + c
-  auto load_state = [&](const float* s) {
+  auto each_state = [&](auto f) __attribute__((always_inline)) {
+    // made here each time (the asm hides that it is always the same): 64
+    // addresses kept over the chunk loop would spill the state itself
+    int at0 = 8 * q * p.P + c;
+    asm volatile("" : "+v"(at0));
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[nt][pt][e] = s ? s[(long)(16 * nt + 4 * q + e) * p.P + 16 * pt + c] : 0.f;
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[kb][u][pt][e] = f(h[kb][u][pt][e], at0 + (32 * kb + 4 * u + e) * p.P + 16 * pt);
   };
-  auto store_state = [&](float* s) {
-    if (!live) return;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[(long)(16 * nt + 4 * q + e) * p.P + 16 * pt + c] = h[nt][pt][e];
+  auto load_state = [&](const float* s) __attribute__((always_inline)) { each_state([&](float, int at) __attribute__((always_inline)) { return s ? s[at] : 0.f; }); };
+  auto store_state = [&](float* s) __attribute__((always_inline)) {
+    if (live) each_state([&](float v, int at) __attribute__((always_inline)) { s[at] = v; return v; });
   };
 
   if (seg >= p.segs) {   // final states of empty sequences
@@ -171,26 +245,32 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p
 
   const int seg0 = seg * p.seg, seg1 = min(seg0 + p.seg, p.s.Ttot);
   float total_gam = 0.f;
+  const Reader<T, NB, NX> rd(w);
+  TileCopy<T, NB, NW> cb, cc;
+  TileCopy<T, NX, NW> cx[Lds::XT];
+  cb.plan(p.b_stride, ND);
+  if constexpr (OUT) cc.plan(p.c_stride, ND);
+#pragma unroll
+  for (int i = 0; i < Lds::XT; ++i) cx[i].plan(p.x_stride, cols - 128 * i);
 
   // One run of tokens [t0, t1) of a sequence, from the state in h.
-  auto run = [&](int t0, int t1) {
-    ChunkRegs<T, ND> rb, rc;
-    ChunkRegs<T, SCOLS> rx;
-    float rdt;
-    auto fetch = [&](int t) {
+  auto run = [&](int t0, int t1) __attribute__((always_inline)) {
+    float rdt = 0.f;
+    auto copy = [&](int t, int buf) __attribute__((always_inline)) {
       const int len = min(SC, t1 - t);
-      rb.load(Bp + (long)t * p.b_stride, p.b_stride, len, ND);
-      if constexpr (OUT) rc.load(Cp + (long)t * p.c_stride, p.c_stride, len, ND);
-      rx.load(x + (long)t * p.x_stride + chan0, p.x_stride, len, cols);
-      rdt = l < len ? to_f(dt[(long)(t + l) * p.dt_stride + head]) : 0.f;
+      cb.issue(lds.b[buf], Bp + (long)t * p.b_stride, p.b_stride, len, ND);
+      if constexpr (OUT) cc.issue(lds.c[buf], Cp + (long)t * p.c_stride, p.c_stride, len, ND);
+#pragma unroll
+      for (int i = 0; i < Lds::XT; ++i)
+        cx[i].issue(lds.x[buf][i], x + (long)t * p.x_stride + chan0 + 128 * i, p.x_stride, len, max(cols - 128 * i, 0));
     };
-    fetch(t0);
+    auto load_dt = [&](int t) { rdt = t + l < t1 ? to_f(dt[(long)(t + l) * p.dt_stride + head]) : 0.f; };
+    lds_barrier();   // the tiles of the run before are no longer read
+    load_dt(t0);
+    if constexpr (Lds::NBUF == 2) copy(t0, 0);
+    int buf = 0;
     for (int t = t0; t < t1; t += SC) {
       const int len = min(SC, t1 - t);
-      lds_barrier();   // the tiles of the chunk before are no longer read
-      rb.store(lds.b);
-      if constexpr (OUT) rc.store(lds.c);
-      rx.store(lds.x);
       float d = rdt + bias;
       if (p.softplus) d = softplus_f(d);
       if (l >= len) d = 0.f;
@@ -202,99 +282,124 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p
         if (l >= m) gam += o;
       }
       const double gend = __shfl(gam, 63);   // tokens behind the last have d = 0
-      lds.gam[w][l] = (float)gam;
-      if constexpr (sizeof(T) == 4) lds.rem[w][l] = (float)(gam - (double)(float)gam);
-      lds.d[w][l] = d;
-      if constexpr (OUT) lds.eg[w][l] = exp_f((float)gam);
+      if constexpr (OUT) {
+        lds.gam[w][l] = (float)gam;
+        if constexpr (F32) lds.rem[w][l] = (float)(gam - (double)(float)gam);
+        lds.d[w][l] = d;
+        lds.eg[w][l] = exp_f((float)gam);
+        lds.ut[w][l] = exp_f((float)(__shfl(gam, l | 15) - gam)) * d;
+      }
       lds.wt[w][l] = exp_f((float)(gend - gam)) * d;
       total_gam += (float)gend;
-      lds_barrier();
-      if (t + SC < t1) fetch(t + SC);
-
+      if constexpr (Lds::NBUF == 1) {
+        lds_barrier();
+        copy(t, 0);
+      }
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies have landed
+      lds_barrier();                        // everyone's have, and the other buffer is no longer read
+      if (t + SC < t1) {
+        load_dt(t + SC);
+        if constexpr (Lds::NBUF == 2) copy(t + SC, buf ^ 1);
+      }
+      const T* tb = lds.b[buf];
+      const T* tc = lds.c[OUT ? buf : 0];
+      const T* tx = lds.x[buf][w / 4];
       frag xf[2][2];   // x^T: columns 16 pt.., tokens 32 jb..
 #pragma unroll
       for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-        for (int jb = 0; jb < 2; ++jb) xf[pt][jb] = K::down(lds.x, PX, 32 * jb, 32 * w + 16 * pt);
+        for (int jb = 0; jb < 2; ++jb) xf[pt][jb] = rd.down_x(tx, jb, pt);
+
       if constexpr (OUT) {
         // scores, transposed: tile (jt, it) holds B_j . C_i, rows j, columns i
+        for (int idx = w; idx < 10; idx += NW) {
+          const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
+          f32x4 s = zero4();
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int idx = w + 4 * k;
-          if (idx < 10) {
-            const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
-            f32x4 s = zero4();
+          for (int kb = 0; kb < NK; ++kb)
+            s = K::mma(rd.along(tb, jt, kb), rd.along(tc, it, kb), s);
+          lds.score[idx * 64 + l] = s;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // y^T, rows = channels, columns = tokens: first e^{gam_i} h^T C_i
+        f32x4 acc[4][2];
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb)
-              s = K::mma(K::along(lds.b + (16 * jt + c) * PB + 32 * kb), K::along(lds.c + (16 * it + c) * PB + 32 * kb), s);
-            lds.score[idx * 64 + l] = s;
+        for (int it = 0; it < 4; ++it) acc[it][0] = acc[it][1] = zero4();
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+          const frag h0 = K::acc(h[kb][0][0], h[kb][1][0]), h1 = K::acc(h[kb][0][1], h[kb][1][1]);
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const frag cf = rd.along(tc, it, kb);
+            acc[it][0] = K::mma(h0, cf, acc[it][0]);
+            acc[it][1] = K::mma(h1, cf, acc[it][1]);
           }
+          __builtin_amdgcn_sched_barrier(0);   // one block's operands at a time in registers
         }
         lds_barrier();
-        frag hf[2][NK];
+        // then the tokens of the chunk up to i.  Tiles left of the diagonal
+        // take e^{gam_i - gam_j} as two factors at the end of tile jt, both
+        // at most 1, which saves three quarters of their exponentials.
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-          for (int kb = 0; kb < NK; ++kb) hf[pt][kb] = K::acc(h[2 * kb][pt], h[2 * kb + 1][pt]);
-        // rolled: unrolled, the four tiles' operands do not fit the registers
-#pragma unroll 1
         for (int it = 0; it < 4; ++it) {
+          if (16 * it >= len) break;
           const int i = 16 * it + c;
-          f32x4 acc[2] = {zero4(), zero4()};
-#pragma unroll
-          for (int kb = 0; kb < NK; ++kb) {
-            const frag cf = K::along(lds.c + i * PB + 32 * kb);
-            acc[0] = K::mma(hf[0][kb], cf, acc[0]);
-            acc[1] = K::mma(hf[1][kb], cf, acc[1]);
-          }
           const float gi = lds.gam[w][i], ei = lds.eg[w][i];
-          const float ri = sizeof(T) == 4 ? lds.rem[sizeof(T) == 4 ? w : 0][i] : 0.f;
+          const float ri = F32 ? lds.rem[F32 ? w : 0][i] : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            acc[0][e] *= ei;
-            acc[1][e] *= ei;
+            acc[it][0][e] *= ei;
+            acc[it][1][e] *= ei;
           }
 #pragma unroll
-          for (int jb = 0; jb < 2; ++jb) {
-            if (2 * jb > it) break;
-            f32x4 pt2[2];
+          for (int jb = 0; 2 * jb <= it; ++jb) {
+            f32x4 pm[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int jt = 2 * jb + k;
-              pt2[k] = zero4();
-              if (jt <= it) {
-                const f32x4 s = lds.score[(it * (it + 1) / 2 + jt) * 64 + l];
+              pm[k] = zero4();
+              if (jt > it) continue;
+              const f32x4 s = lds.score[(it * (it + 1) / 2 + jt) * 64 + l];
+              if (jt < it) {
+                const f32x4 uj = *reinterpret_cast<const f32x4*>(&lds.ut[w][16 * jt + 4 * q]);
+                float df = gi - lds.gam[w][16 * jt + 15];
+                if constexpr (F32) df += ri - lds.rem[w][16 * jt + 15];
+                const float f = exp_f(df);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pm[k][e] = s[e] * (uj[e] * f);
+              } else {
                 const f32x4 gj = *reinterpret_cast<const f32x4*>(&lds.gam[w][16 * jt + 4 * q]);
                 const f32x4 dj = *reinterpret_cast<const f32x4*>(&lds.d[w][16 * jt + 4 * q]);
-                f32x4 df;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) df[e] = gi - gj[e];
-                if constexpr (sizeof(T) == 4) {
-                  const f32x4 rj = *reinterpret_cast<const f32x4*>(&lds.rem[w][16 * jt + 4 * q]);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) df[e] += ri - rj[e];
-                }
+                f32x4 rj = zero4();
+                if constexpr (F32) rj = *reinterpret_cast<const f32x4*>(&lds.rem[w][16 * jt + 4 * q]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const float v = s[e] * (exp_f(df[e]) * dj[e]);
-                  pt2[k][e] = (jt < it || 4 * q + e <= c) ? v : 0.f;
+                  float df = gi - gj[e];
+                  if constexpr (F32) df += ri - rj[e];
+                  const float v = s[e] * (exp_f(df) * dj[e]);
+                  pm[k][e] = 4 * q + e <= c ? v : 0.f;
                 }
               }
             }
-            const frag pf = K::acc(pt2[0], pt2[1]);
-            acc[0] = K::mma(xf[0][jb], pf, acc[0]);
-            acc[1] = K::mma(xf[1][jb], pf, acc[1]);
+            const frag pf = K::acc(pm[0], pm[1]);
+            acc[it][0] = K::mma(xf[0][jb], pf, acc[it][0]);
+            acc[it][1] = K::mma(xf[1][jb], pf, acc[it][1]);
           }
           if (live && i < len) {
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt) {
-              float xv[4], o[4];
-              vec_load<T, 4>(lds.x + i * PX + 32 * w + 16 * pt + 4 * q, 4, xv);
+              float o[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = p.D ? fmaf(skip, xv[e], acc[pt][e]) : acc[pt][e];
+              for (int e = 0; e < 4; ++e) o[e] = acc[it][pt][e];
+              if (p.D) {
+                const f32x4 xv = rd.at(tx, it, pt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(skip, xv[e], o[e]);
+              }
               vec_store<T, 4>(y + (long)(t + i) * HP + chan + 16 * pt + 4 * q, 4, o);
             }
           }
+          __builtin_amdgcn_sched_barrier(0);   // and one tile's
         }
       }
 
@@ -304,16 +409,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p
       // 2^-8, two 2^-16); B and x are bf16 as they are.
       const float en = exp_f((float)gend);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[nt][pt][e] *= en;
+          for (int pt = 0; pt < 2; ++pt) h[kb][u][pt] *= en;
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb) {
+        if (32 * jb >= len) break;
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds.wt[w][32 * jb + 4 * q]);
         const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds.wt[w][32 * jb + 16 + 4 * q]);
-        constexpr int TERMS = sizeof(T) == 2 ? 3 : 1;
+        constexpr int TERMS = F32 ? 1 : 3;
         frag wx[TERMS][2];
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt) {
@@ -335,14 +441,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const frag bf = K::down(lds.b, PB, 32 * jb, 16 * nt);
+        for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int u = 0; u < 2; ++u) {
+            const frag bf = rd.down_b(tb, jb, kb, u);
 #pragma unroll
-            for (int k = 0; k < TERMS; ++k) h[nt][pt] = K::mma(bf, wx[k][pt], h[nt][pt]);
-        }
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+              for (int k = 0; k < TERMS; ++k) h[kb][u][pt] = K::mma(bf, wx[k][pt], h[kb][u][pt]);
+            if (u == 1) __builtin_amdgcn_sched_barrier(0);
+          }
       }
+      if constexpr (Lds::NBUF == 2) buf ^= 1;
     }
   };
 
@@ -365,7 +475,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_ssm(SsmParams p
       const int stop = min(end, seg1);
       if (n < 0) {
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        for (long i = threadIdx.x; i < (long)(stop - t) * (cols / 4); i += 256) {
+        for (long i = threadIdx.x; i < (long)(stop - t) * (cols / 4); i += 64 * NW) {
           const long r = i / (cols / 4);
           vec_store<T, 4>(y + (t + r) * HP + chan0 + 4 * (i - r * (cols / 4)), 4, zero);
         }
@@ -411,15 +521,20 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmParams p) {
   }
 }
 
-// Segments: enough workgroups for two (bf16) or one (fp32, by its LDS) on
-// every compute unit, but not under 256 tokens, where the two further
-// launches cost more than they save.
+// Waves of a workgroup: 8 (256 channels share the tiles of B and C), or 4
+// where a group has no more than 128 channels, and in fp32, whose tiles take
+// twice the LDS.
+static int ssm_waves(DType dt, const SsmParams& p) {
+  return dt == DType::BF16 && p.H / p.G * p.P > 128 ? 8 : 4;
+}
+
+// Segments: enough workgroups for every compute unit, but not under 256
+// tokens, where the two further launches cost more than they save.
 void ssm_plan(DType dt, SsmParams& p) {
-  const int hp = p.H / p.G * p.P;
-  p.wgs = p.G * ((hp + SCOLS - 1) / SCOLS);
-  const long want = (dt == DType::BF16 ? 2L : 1L) * kComputeUnits;
+  const int hp = p.H / p.G * p.P, cols = 32 * ssm_waves(dt, p);
+  p.wgs = p.G * ((hp + cols - 1) / cols);
   const long most = (p.s.Ttot + 255) / 256;
-  long segs = (want + p.wgs - 1) / p.wgs;
+  long segs = (kComputeUnits + p.wgs - 1) / p.wgs;
   segs = segs > most ? most : segs;
   segs = segs < 1 ? 1 : segs;
   const long tokens = (p.s.Ttot + segs - 1) / segs;
@@ -428,13 +543,13 @@ void ssm_plan(DType dt, SsmParams& p) {
   p.segs = (p.s.Ttot + p.seg - 1) / p.seg;
 }
 
-template <typename T, int ND>
+template <typename T, int ND, int NW>
 static hipError_t ssm_scan(const SsmParams& p, hipStream_t st) {
   hipError_t e = hipSuccess;
   if (p.segs > 1) {
     const int total = (p.segs - 1) * p.wgs;
     timing_before("ssm_states", st);
-    hipLaunchKernelGGL((k_ssm<T, ND, false>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(256), 0, st, p, total);
+    hipLaunchKernelGGL((k_ssm<T, ND, NW, false>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(64 * NW), 0, st, p, total);
     e = hipGetLastError();
     timing_after(st);
     if (e != hipSuccess) return e;
@@ -451,18 +566,19 @@ static hipError_t ssm_scan(const SsmParams& p, hipStream_t st) {
   const long total = (long)(p.segs + extra) * p.wgs;
   if (total == 0) return hipSuccess;
   timing_before("ssm_scan", st);
-  hipLaunchKernelGGL((k_ssm<T, ND, true>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(256), 0, st, p, (int)total);
+  hipLaunchKernelGGL((k_ssm<T, ND, NW, true>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(64 * NW), 0, st, p, (int)total);
   e = hipGetLastError();
   timing_after(st);
   return e;
 }
+template <typename T, int NW>
+static hipError_t ssm_scan_n(const SsmParams& p, hipStream_t st) {
+  if (p.N == 32) return ssm_scan<T, 32, NW>(p, st);
+  return p.N == 64 ? ssm_scan<T, 64, NW>(p, st) : ssm_scan<T, 128, NW>(p, st);
+}
 hipError_t launch_ssm_scan(DType dt, const SsmParams& p, hipStream_t st) {
-  if (dt == DType::BF16) {
-    if (p.N == 32) return ssm_scan<bf16, 32>(p, st);
-    return p.N == 64 ? ssm_scan<bf16, 64>(p, st) : ssm_scan<bf16, 128>(p, st);
-  }
-  if (p.N == 32) return ssm_scan<float, 32>(p, st);
-  return p.N == 64 ? ssm_scan<float, 64>(p, st) : ssm_scan<float, 128>(p, st);
+  if (dt != DType::BF16) return ssm_scan_n<float, 4>(p, st);
+  return ssm_waves(dt, p) == 8 ? ssm_scan_n<bf16, 8>(p, st) : ssm_scan_n<bf16, 4>(p, st);
 }
 
 }  // namespace gdr
