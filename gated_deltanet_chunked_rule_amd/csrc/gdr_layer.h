@@ -202,9 +202,15 @@ __device__ __forceinline__ void vec_store(T* p, int n, const float (&f)[VEC]) {
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 // 1 / (1 + e^-x), with the hardware's exp2 and reciprocal (one ulp each)
 __device__ __forceinline__ float sigmoid_f(float x) { return __builtin_amdgcn_rcpf(1.f + exp_f(-x)); }
-// log(1 + e^x); above 20 it equals x in fp32.  log1pf keeps small steps exact
-// to fp32 where e^x is far below 1.
-__device__ __forceinline__ float softplus_f(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+// log(1 + e^x); above 20 it equals x in fp32.  With u = e^x and w = 1 + u
+// rounded, log(w) u / (w - 1) takes back the rounding of w (the correction of
+// Goldberg's "What every computer scientist should know about floating-point
+// arithmetic", theorem 4), so that small steps keep their relative accuracy.
+__device__ __forceinline__ float softplus_f(float x) {
+  const float u = exp_f(x), w = 1.f + u, d = w - 1.f;
+  const float v = d == 0.f ? u : __builtin_amdgcn_logf(w) * 0.6931471805599453f * (u * __builtin_amdgcn_rcpf(d));
+  return x > 20.f ? x : v;
+}
 
 // Tables of offsets: staged in LDS up to kCuLds sequences.
 constexpr int kCuLds = 1024;

@@ -261,7 +261,7 @@ gdr_status gdr_ssm_scan_fwd(const gdr_ssm_shape* shape, const void* x, const voi
   gdr::SsmParams p = ssm_params(shape, cu_seqlens);
   if (!workspace || workspace_bytes < ssm_bytes(p))
     return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_ssm_scan_fwd_workspace_size)");
-  if (((long)p.segs + p.s.N) * p.wgs > kMaxThreads / 256) return unsupported("too many sequences times heads");
+  if (((long)p.segs + 8) * p.wgs > kMaxThreads / 512) return unsupported("too many sequences times heads");
   p.x = x; p.dt = dt; p.A = A; p.B = B; p.C = C; p.D = D; p.bias = dt_bias; p.h0 = initial_state;
   p.y = y; p.ht = final_state;
   p.seg_state = static_cast<float*>(workspace);

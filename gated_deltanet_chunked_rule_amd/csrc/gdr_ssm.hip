@@ -47,8 +47,18 @@ template <> struct Blk<bf16> {
   static __device__ __forceinline__ f32x4 mma(frag a, frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ frag acc(const f32x4& x, const f32x4& y) { return pack_b(x, y); }
-  static __device__ __forceinline__ float get(const frag& f, int e) { return static_cast<float>(f[e]); }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), bf16x2));
+  }
+  static __device__ __forceinline__ frag acc(const f32x4& x, const f32x4& y) {
+    return __builtin_bit_cast(frag, make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(y[0], y[1]), pair(y[2], y[3])));
+  }
+  static __device__ __forceinline__ float get(const frag& f, int e) {
+    const uint4 u = __builtin_bit_cast(uint4, f);
+    const uint32_t v = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
+    return __builtin_bit_cast(float, e & 1 ? v & 0xffff0000u : v << 16);
+  }
 };
 template <> struct Blk<float> {
   struct frag { float v[8]; };
@@ -68,7 +78,7 @@ template <> struct Blk<float> {
 // steps that the instruction's offset holds: a few registers for all of them.
 template <typename T, int NB, int NX> struct Reader;
 template <int NB, int NX> struct Reader<bf16, NB, NX> {
-  int arow, ax, brow, bx, xrow, xx, srow, sx;
+  int arow, ax, brow, bx, xrow, xx;
   __device__ __forceinline__ Reader(int w) {
     const int l = lane_id(), c = l & 15, q = l >> 4, r = 4 * q + (c >> 2), s = c & 3, wx = 64 * (w & 3);
     arow = c * NB * 16;
@@ -77,8 +87,6 @@ template <int NB, int NX> struct Reader<bf16, NB, NX> {
     bx = 16 * (s ^ ssm_swz<bf16, NB>(r));
     xrow = r * NX * 16 + 8 * (s & 1);
     xx = wx ^ (16 * ((s >> 1) ^ ssm_swz<bf16, NX>(r)));
-    srow = c * NX * 16 + 8 * (q & 1);
-    sx = wx ^ (16 * ((q >> 1) ^ ssm_swz<bf16, NX>(c)));
   }
   // n along row 16 it + c
   __device__ __forceinline__ bf16x8 along(const bf16* t, int it, int kb) const {
@@ -96,15 +104,10 @@ template <int NB, int NX> struct Reader<bf16, NB, NX> {
   __device__ __forceinline__ bf16x8 down_x(const bf16* t, int jb, int pt) const {
     return tr(reinterpret_cast<const char*>(t) + xrow + ((32 * pt) ^ xx) + jb * 512 * NX, 256 * NX);
   }
-  // columns 16 pt + 4 q .. + 3 of row 16 it + c
-  __device__ __forceinline__ f32x4 at(const bf16* t, int it, int pt) const {
-    const bf16x4 v = *reinterpret_cast<const bf16x4*>(reinterpret_cast<const char*>(t) + srow + ((32 * pt) ^ sx) + it * 256 * NX);
-    return f32x4{static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]), static_cast<float>(v[3])};
-  }
 };
 template <int NB, int NX> struct Reader<float, NB, NX> {
   typedef Blk<float>::frag frag;
-  int arow, ax, brow, bx, xx, xrow, srow, sx;
+  int arow, ax, brow, bx, xrow, xx;
   __device__ __forceinline__ Reader(int w) {
     const int l = lane_id(), c = l & 15, q = l >> 4, wx = 128 * (w & 3);
     arow = c * NB * 16;
@@ -113,8 +116,6 @@ template <int NB, int NX> struct Reader<float, NB, NX> {
     bx = 16 * ((2 * (c >> 2)) ^ ssm_swz<float, NB>(4 * q));
     xrow = 4 * q * NX * 16 + 4 * (c & 3);
     xx = wx ^ (16 * ((c >> 2) ^ ssm_swz<float, NX>(4 * q)));
-    srow = c * NX * 16;
-    sx = wx ^ (16 * (q ^ ssm_swz<float, NX>(c)));
   }
   __device__ __forceinline__ frag along(const float* t, int it, int kb) const {
     const char* p = reinterpret_cast<const char*>(t) + arow + it * 256 * NB;
@@ -133,9 +134,6 @@ template <int NB, int NX> struct Reader<float, NB, NX> {
   }
   __device__ __forceinline__ frag down_x(const float* t, int jb, int pt) const {
     return rows(reinterpret_cast<const char*>(t) + xrow + jb * 512 * NX, (64 * pt) ^ xx, NX * 16);
-  }
-  __device__ __forceinline__ f32x4 at(const float* t, int it, int pt) const {
-    return *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(t) + srow + ((64 * pt) ^ sx) + it * 256 * NX);
   }
 };
 
@@ -235,12 +233,20 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
     if (live) each_state([&](float v, int at) __attribute__((always_inline)) { s[at] = v; return v; });
   };
 
-  if (seg >= p.segs) {   // final states of empty sequences
-    const int n = seg - p.segs;
-    if (sf.at(n + 1) > sf.at(n)) return;
-    load_state(p.h0 ? state_at(p.h0 + n * (long)p.H * sstride) : nullptr);
-    store_state(const_cast<float*>(state_at(p.ht + n * (long)p.H * sstride)));
-    return;
+  if constexpr (OUT) {
+    // final states of empty sequences: the first segment's workgroups copy
+    // them (workgroups of their own would wait for a compute unit each)
+    if (seg == 0 && p.ht) {
+      for (int n0 = 0; n0 < p.s.N; n0 += 64) {
+        const int m = n0 + l;
+        uint64_t empty = __builtin_amdgcn_ballot_w64(m < p.s.N && sf.at(min(m, p.s.N - 1) + 1) <= sf.at(min(m, p.s.N - 1)));
+        for (; empty; empty &= empty - 1) {
+          const int n = n0 + __builtin_ctzll(empty);
+          load_state(p.h0 ? state_at(p.h0 + n * (long)p.H * sstride) : nullptr);
+          store_state(const_cast<float*>(state_at(p.ht + n * (long)p.H * sstride)));
+        }
+      }
+    }
   }
 
   const int seg0 = seg * p.seg, seg1 = min(seg0 + p.seg, p.s.Ttot);
@@ -377,7 +383,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
                   float df = gi - gj[e];
                   if constexpr (F32) df += ri - rj[e];
                   const float v = s[e] * (exp_f(df) * dj[e]);
-                  pm[k][e] = 4 * q + e <= c ? v : 0.f;
+                  // D x_i joins the product as the diagonal's part of it
+                  pm[k][e] = 4 * q + e < c ? v : 4 * q + e == c ? v + skip : 0.f;
                 }
               }
             }
@@ -388,14 +395,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
           if (live && i < len) {
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt) {
-              float o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = acc[it][pt][e];
-              if (p.D) {
-                const f32x4 xv = rd.at(tx, it, pt);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = fmaf(skip, xv[e], o[e]);
-              }
+              const float o[4] = {acc[it][pt][0], acc[it][pt][1], acc[it][pt][2], acc[it][pt][3]};
               vec_store<T, 4>(y + (long)(t + i) * HP + chan + 16 * pt + 4 * q, 4, o);
             }
           }
@@ -560,13 +560,11 @@ static hipError_t ssm_scan(const SsmParams& p, hipStream_t st) {
     timing_after(st);
     if (e != hipSuccess) return e;
   }
-  // sequences without tokens have no segment: their states are copied by
-  // workgroups of their own
-  const int extra = p.ht && (p.s.cu || p.s.T == 0) ? p.s.N : 0;
-  const long total = (long)(p.segs + extra) * p.wgs;
+  // without a token in any sequence, one segment's workgroups copy the states
+  const int total = (p.segs > 0 ? p.segs : p.ht ? 1 : 0) * p.wgs;
   if (total == 0) return hipSuccess;
   timing_before("ssm_scan", st);
-  hipLaunchKernelGGL((k_ssm<T, ND, NW, true>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(64 * NW), 0, st, p, (int)total);
+  hipLaunchKernelGGL((k_ssm<T, ND, NW, true>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(64 * NW), 0, st, p, total);
   e = hipGetLastError();
   timing_after(st);
   return e;
