@@ -87,13 +87,13 @@ gdr_status ssm_check(const gdr_ssm_shape* sh, bool packed) {
   if (sh->H % sh->G != 0) return invalid("H must be a multiple of G");
   if (sh->P != 32 && sh->P != 64 && sh->P != 128) return unsupported("P must be 32, 64 or 128");
   if (sh->N != 32 && sh->N != 64 && sh->N != 128) return unsupported("N must be 32, 64 or 128");
-  if (sh->H > 65536) return unsupported("H must be at most 65536");
+  // a chunk's 64 rows lie within 2 GiB
+  if ((long)sh->H * sh->P > (1 << 22) || (long)sh->G * sh->N > (1 << 22)) return unsupported("H * P and G * N must be at most 2^22");
   if (sh->dt_softplus != 0 && sh->dt_softplus != 1) return invalid("dt_softplus must be 0 or 1");
   const int64_t st[4] = {sh->x_stride, sh->b_stride, sh->c_stride, sh->dt_stride};
   const int64_t least[4] = {(int64_t)sh->H * sh->P, (int64_t)sh->G * sh->N, (int64_t)sh->G * sh->N, sh->H};
   for (int i = 0; i < 4; ++i) {
     if (st[i] != 0 && st[i] < least[i]) return invalid("a token stride is smaller than its row");
-    // a chunk's 64 rows lie within 2 GiB
     if (st[i] > (1 << 22)) return unsupported("a token stride is over 2^22 elements");
     if (i < 3 && st[i] * esize(sh->dtype) % 16 != 0) return invalid("rows of x, B and C must be 16-byte aligned");
   }

@@ -271,15 +271,12 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         cx[i].issue(lds.x[buf][i], x + (long)t * p.x_stride + chan0 + 128 * i, p.x_stride, len, max(cols - 128 * i, 0));
     };
     auto load_dt = [&](int t) { rdt = t + l < t1 ? to_f(dt[(long)(t + l) * p.dt_stride + head]) : 0.f; };
-    lds_barrier();   // the tiles of the run before are no longer read
-    load_dt(t0);
-    if constexpr (Lds::NBUF == 2) copy(t0, 0);
-    int buf = 0;
-    for (int t = t0; t < t1; t += SC) {
-      const int len = min(SC, t1 - t);
+    // The gates of a chunk, lane l its token l: made from dt one chunk ahead.
+    struct { float gam, rem, d, eg, ut, wt, end; } gt;
+    auto gates = [&](int t) __attribute__((always_inline)) {
       float d = rdt + bias;
       if (p.softplus) d = softplus_f(d);
-      if (l >= len) d = 0.f;
+      if (t + l >= t1) d = 0.f;
       // gam in 64 bits: a difference of two far sums keeps fp32's accuracy
       double gam = (double)d * (double)A;
 #pragma unroll
@@ -287,16 +284,34 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         const double o = __shfl_up(gam, m);
         if (l >= m) gam += o;
       }
-      const double gend = __shfl(gam, 63);   // tokens behind the last have d = 0
+      const double end = __shfl(gam, 63);   // tokens behind the last have d = 0
+      gt.d = d;
+      gt.end = (float)end;
+      gt.wt = exp_f((float)(end - gam)) * d;
       if constexpr (OUT) {
-        lds.gam[w][l] = (float)gam;
-        if constexpr (F32) lds.rem[w][l] = (float)(gam - (double)(float)gam);
-        lds.d[w][l] = d;
-        lds.eg[w][l] = exp_f((float)gam);
-        lds.ut[w][l] = exp_f((float)(__shfl(gam, l | 15) - gam)) * d;
+        gt.gam = (float)gam;
+        gt.rem = (float)(gam - (double)gt.gam);
+        gt.eg = exp_f(gt.gam);
+        gt.ut = exp_f((float)(__shfl(gam, l | 15) - gam)) * d;
       }
-      lds.wt[w][l] = exp_f((float)(gend - gam)) * d;
-      total_gam += (float)gend;
+    };
+    lds_barrier();   // the tiles of the run before are no longer read
+    load_dt(t0);
+    if constexpr (Lds::NBUF == 2) copy(t0, 0);
+    gates(t0);
+    int buf = 0;
+    for (int t = t0; t < t1; t += SC) {
+      const int len = min(SC, t1 - t);
+      const float gend = gt.end;
+      if constexpr (OUT) {
+        lds.gam[w][l] = gt.gam;
+        if constexpr (F32) lds.rem[w][l] = gt.rem;
+        lds.d[w][l] = gt.d;
+        lds.eg[w][l] = gt.eg;
+        lds.ut[w][l] = gt.ut;
+      }
+      lds.wt[w][l] = gt.wt;
+      total_gam += gend;
       if constexpr (Lds::NBUF == 1) {
         lds_barrier();
         copy(t, 0);
@@ -343,6 +358,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
           __builtin_amdgcn_sched_barrier(0);   // one block's operands at a time in registers
         }
         lds_barrier();
+        const rsrc_t yr = make_rsrc_u(y + (long)t * HP, (long)len * HP * (long)sizeof(T));
+        const uint32_t yoff = (uint32_t)((c * (int)HP + chan + 4 * q) * (int)sizeof(T));
         // then the tokens of the chunk up to i.  Tiles left of the diagonal
         // take e^{gam_i - gam_j} as two factors at the end of tile jt, both
         // at most 1, which saves three quarters of their exponentials.
@@ -392,11 +409,16 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
             acc[it][0] = K::mma(xf[0][jb], pf, acc[it][0]);
             acc[it][1] = K::mma(xf[1][jb], pf, acc[it][1]);
           }
-          if (live && i < len) {
+          // rows behind the chunk's last lie behind the descriptor
+          if (live) {
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt) {
-              const float o[4] = {acc[it][pt][0], acc[it][pt][1], acc[it][pt][2], acc[it][pt][3]};
-              vec_store<T, 4>(y + (long)(t + i) * HP + chan + 16 * pt + 4 * q, 4, o);
+              const uint32_t off = yoff + (uint32_t)((16 * it * (int)HP + 16 * pt) * (int)sizeof(T));
+              if constexpr (F32) {
+                buf_store16(yr, off, __builtin_bit_cast(uint4, acc[it][pt]));
+              } else {
+                buf_store8(yr, off, make_uint2(K::pair(acc[it][pt][0], acc[it][pt][1]), K::pair(acc[it][pt][2], acc[it][pt][3])));
+              }
             }
           }
           __builtin_amdgcn_sched_barrier(0);   // and one tile's
@@ -407,7 +429,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       // product w x is taken as three bf16 terms of 8 bits each, so that the
       // state is as exact as fp32 operands would make it (one term would leave
       // 2^-8, two 2^-16); B and x are bf16 as they are.
-      const float en = exp_f((float)gend);
+      if (t + SC < t1) gates(t + SC);
+      const float en = exp_f(gend);
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
@@ -441,16 +464,17 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
           }
         }
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb)
+        for (int kb = 0; kb < NK; ++kb) {
+          const frag b0 = rd.down_b(tb, jb, kb, 0), b1 = rd.down_b(tb, jb, kb, 1);
+          // term by term over the four tiles, so that no product waits for the one before
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const frag bf = rd.down_b(tb, jb, kb, u);
+          for (int k = 0; k < TERMS; ++k)
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-              for (int k = 0; k < TERMS; ++k) h[kb][u][pt] = K::mma(bf, wx[k][pt], h[kb][u][pt]);
-            if (u == 1) __builtin_amdgcn_sched_barrier(0);
-          }
+            for (int pt = 0; pt < 2; ++pt) {
+              h[kb][0][pt] = K::mma(b0, wx[k][pt], h[kb][0][pt]);
+              h[kb][1][pt] = K::mma(b1, wx[k][pt], h[kb][1][pt]);
+            }
+        }
       }
       if constexpr (Lds::NBUF == 2) buf ^= 1;
     }

@@ -73,7 +73,7 @@ def ssm_shape(B=1, T=8, H=4, G=2, P=64, N=128, seqs=1, dtype=0, softplus=1, xs=0
 @pytest.mark.parametrize("kw,rc,msg", [
     (dict(H=5), -1, "multiple of G"), (dict(G=0), -1, "positive"), (dict(P=16), -2, "P must be"), (dict(N=256), -2, "N must be"),
     (dict(softplus=2), -1, "dt_softplus"), (dict(xs=255), -1, "smaller"), (dict(xs=257), -1, "16-byte"), (dict(bs=264 - 4), -1, "16-byte"),
-    (dict(ds=3), -1, "smaller"), (dict(cs=1 << 23), -2, "2^22"), (dict(H=1 << 17), -2, "H must be"), (dict(dtype=2), -2, "dtype"),
+    (dict(ds=3), -1, "smaller"), (dict(cs=1 << 23), -2, "2^22"), (dict(H=1 << 17), -2, "2^22"), (dict(dtype=2), -2, "dtype"),
 ])
 def test_scan_refuses(kw, rc, msg):
     p = [fake(i) for i in range(12)]
