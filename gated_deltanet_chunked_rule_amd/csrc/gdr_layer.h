@@ -212,7 +212,7 @@ __device__ __forceinline__ float softplus_f(float x) {
   return x > 20.f ? x : v;
 }
 
-// Tables of offsets: staged in LDS up to kCuLds sequences.
+// Tables of offsets: staged in LDS below this many sequences.
 constexpr int kCuLds = 1024;
 struct SeqFinder {
   const int32_t* cu;   // global, or the staged copy
@@ -250,6 +250,7 @@ struct SeqFinder {
   }
 };
 // Every thread of the workgroup calls this (barrier inside).
+template <int STAGE = kCuLds>
 __device__ __forceinline__ SeqFinder seq_finder(const SeqRanges& s, int32_t* lds) {
   SeqFinder f;
   f.cu = s.cu;
@@ -257,7 +258,7 @@ __device__ __forceinline__ SeqFinder seq_finder(const SeqRanges& s, int32_t* lds
   f.T = s.T;
   f.Ttot = s.Ttot;
   f.packed = s.cu != nullptr;
-  if (s.cu && s.N < kCuLds) {
+  if (s.cu && s.N < STAGE) {
     for (int i = threadIdx.x; i <= s.N; i += blockDim.x) lds[i] = s.cu[i];
     __syncthreads();
     f.cu = lds;

@@ -9,11 +9,16 @@
 // Every decay is the exponential of a difference of gam, so that strong gates
 // underflow to zero instead of dividing by it.
 //
-// A workgroup takes one segment of the token axis and 32 channels (x columns of
-// one group's heads) for each of its waves; a wave's channels lie within one
-// head, and it keeps their [N, 32] block of the state in fp32 accumulators.
-// The scores C B^T of a chunk are the same for every head of the group: the
-// waves share their computation and each applies its own head's decays.
+// A workgroup takes one segment of the token axis and 16 channels (x columns of
+// one group's heads) for each of its waves, up to 256 channels in at most 4
+// heads; a wave keeps its [N, 16] block of the state in fp32 accumulators.
+// The scores C B^T of a chunk are the same for every head of the group: a
+// wave computes a 16 x 16 tile of them and leaves it in LDS with each head's
+// decays applied, so that nothing of it is computed twice; the gates of the
+// next chunk are made meanwhile by waves without a tile.  16 waves of 128
+// registers hide each other's latencies: 8 waves of 32 channels took 76 us
+// where these take SCAN_US (8192 tokens, 64 heads of 64, N = 128), 4 of 64
+// channels took 89.
 //
 // Long prompts are cut into segments that run side by side: a first pass
 // computes what each segment adds to the state and its decay, k_ssm_join
@@ -51,6 +56,9 @@ template <> struct Blk<bf16> {
     typedef float f2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), bf16x2));
   }
+  typedef uint2 quad;   // four values, as they stand in an operand
+  static __device__ __forceinline__ quad four(const f32x4& x) { return make_uint2(pair(x[0], x[1]), pair(x[2], x[3])); }
+  static __device__ __forceinline__ frag join(quad x, quad y) { return __builtin_bit_cast(frag, make_uint4(x.x, x.y, y.x, y.y)); }
   static __device__ __forceinline__ frag acc(const f32x4& x, const f32x4& y) {
     return __builtin_bit_cast(frag, make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(y[0], y[1]), pair(y[2], y[3])));
   }
@@ -67,6 +75,9 @@ template <> struct Blk<float> {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
     return c;
   }
+  typedef f32x4 quad;
+  static __device__ __forceinline__ quad four(const f32x4& x) { return x; }
+  static __device__ __forceinline__ frag join(const quad& x, const quad& y) { return acc(x, y); }
   static __device__ __forceinline__ frag acc(const f32x4& x, const f32x4& y) {
     return frag{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
   }
@@ -80,7 +91,7 @@ template <typename T, int NB, int NX> struct Reader;
 template <int NB, int NX> struct Reader<bf16, NB, NX> {
   int arow, ax, brow, bx, xrow, xx;
   __device__ __forceinline__ Reader(int w) {
-    const int l = lane_id(), c = l & 15, q = l >> 4, r = 4 * q + (c >> 2), s = c & 3, wx = 64 * (w & 3);
+    const int l = lane_id(), c = l & 15, q = l >> 4, r = 4 * q + (c >> 2), s = c & 3, wx = 32 * (w & 7);
     arow = c * NB * 16;
     ax = 16 * (q ^ ssm_swz<bf16, NB>(c));
     brow = r * NB * 16;
@@ -100,16 +111,16 @@ template <int NB, int NX> struct Reader<bf16, NB, NX> {
   __device__ __forceinline__ bf16x8 down_b(const bf16* t, int jb, int kb, int u) const {
     return tr(reinterpret_cast<const char*>(t) + brow + ((64 * kb) ^ bx) + 8 * u + jb * 512 * NB, 256 * NB);
   }
-  // and down this wave's columns 16 pt + c
-  __device__ __forceinline__ bf16x8 down_x(const bf16* t, int jb, int pt) const {
-    return tr(reinterpret_cast<const char*>(t) + xrow + ((32 * pt) ^ xx) + jb * 512 * NX, 256 * NX);
+  // and down this wave's 16 columns of x
+  __device__ __forceinline__ bf16x8 down_x(const bf16* t, int jb) const {
+    return tr(reinterpret_cast<const char*>(t) + xrow + xx + jb * 512 * NX, 256 * NX);
   }
 };
 template <int NB, int NX> struct Reader<float, NB, NX> {
   typedef Blk<float>::frag frag;
   int arow, ax, brow, bx, xrow, xx;
   __device__ __forceinline__ Reader(int w) {
-    const int l = lane_id(), c = l & 15, q = l >> 4, wx = 128 * (w & 3);
+    const int l = lane_id(), c = l & 15, q = l >> 4, wx = 64 * (w & 7);
     arow = c * NB * 16;
     ax = 16 * ((2 * q) ^ ssm_swz<float, NB>(c));
     brow = 4 * q * NB * 16 + 4 * (c & 3);
@@ -132,8 +143,8 @@ template <int NB, int NX> struct Reader<float, NB, NX> {
   __device__ __forceinline__ frag down_b(const float* t, int jb, int kb, int u) const {
     return rows(reinterpret_cast<const char*>(t) + brow + jb * 512 * NB, (128 * kb + 16 * u) ^ bx, NB * 16);
   }
-  __device__ __forceinline__ frag down_x(const float* t, int jb, int pt) const {
-    return rows(reinterpret_cast<const char*>(t) + xrow + jb * 512 * NX, (64 * pt) ^ xx, NX * 16);
+  __device__ __forceinline__ frag down_x(const float* t, int jb) const {
+    return rows(reinterpret_cast<const char*>(t) + xrow + jb * 512 * NX, xx, NX * 16);
   }
 };
 
@@ -161,22 +172,28 @@ struct TileCopy {
   }
 };
 
+constexpr int SHEADS = 4;       // heads of a workgroup, at most
+constexpr int SCU = 256;        // staged sequence offsets
+
 template <typename T, int ND, int NW, bool OUT>
 struct SsmLds {
   static constexpr int VEC = 16 / (int)sizeof(T);
   static constexpr int NB = ND / VEC, NX = 128 / VEC;              // pieces of a row of B or C, of x (128 channels)
-  static constexpr int XT = NW / 4;                                // x tiles of 128 channels
+  static constexpr int XT = NW / 8;                                // x tiles of 128 channels
   static constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;              // fp32 fills the LDS with one
+  static constexpr int REM = OUT && sizeof(T) == 4;
   T b[NBUF][SC * ND];
   T x[NBUF][XT][SC * 128];
   T c[OUT ? NBUF : 1][OUT ? SC * ND : 8];
-  f32x4 score[OUT ? 10 * 64 : 1];   // tiles (jt <= it) of B C^T, by lane
-  // per wave, its head's tokens: gam as a float (and its remainder, fp32), d,
-  // e^gam, and two weights: of the token at its 16-token tile's end, and in
-  // the chunk's end state
-  float gam[OUT ? NW : 1][SC], rem[OUT && sizeof(T) == 4 ? NW : 1][SC], d[OUT ? NW : 1][SC], eg[OUT ? NW : 1][SC];
-  float ut[OUT ? NW : 1][SC], wt[NW][SC];
-  int32_t cu[kCuLds];
+  // per head, tiles (jt <= it) of the decayed scores, by lane: rows j, columns i
+  typename Blk<T>::quad score[OUT ? SHEADS : 1][OUT ? 10 * 64 : 1];
+  // per head and token: gam as a float (and its remainder, fp32), d, e^gam,
+  // and two weights: at the end of the token's tile of 16, and in the chunk's
+  // end state.  Two buffers: the next chunk's are made during this one.
+  float gam[2][SHEADS][SC], wt[2][SHEADS][SC];
+  float d[2][OUT ? SHEADS : 1][OUT ? SC : 1], eg[2][OUT ? SHEADS : 1][OUT ? SC : 1], ut[2][OUT ? SHEADS : 1][OUT ? SC : 1];
+  float rem[2][REM ? SHEADS : 1][REM ? SC : 1];
+  int32_t cu[SCU];
 };
 
 template <typename T, int ND, int NW, bool OUT>
@@ -184,23 +201,24 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   typedef Blk<T> K;
   typedef typename K::frag frag;
   typedef SsmLds<T, ND, NW, OUT> Lds;
-  constexpr int NK = ND / 32, NB = Lds::NB, NX = Lds::NX, COLS = 32 * NW;
+  constexpr int NK = ND / 32, NB = Lds::NB, NX = Lds::NX, COLS = 16 * NW;
   constexpr bool F32 = sizeof(T) == 4;
   __shared__ __align__(16) Lds lds;
   // workgroups of one segment share B and C: keep them on one XCD
   const int id = xcd_remap(blockIdx.x, total);
   if (id >= total) return;
-  const SeqFinder sf = seq_finder(p.s, lds.cu);
+  const SeqFinder sf = seq_finder<SCU>(p.s, lds.cu);
   const int hp = p.H / p.G * p.P;                       // channels of a group
   const int per_group = (hp + COLS - 1) / COLS;
   const int seg = id / p.wgs, wi = id - seg * p.wgs;
   const int g = wi / per_group, col0 = (wi - g * per_group) * COLS;
   const int cols = min(COLS, hp - col0);
   const int w = wave_id(), l = lane_id(), c = l & 15, q = l >> 4;
-  const bool live = 32 * w < cols;                      // waves without channels still help with copies and scores
-  const int chan0 = g * hp + col0;                      // the workgroup's first channel
-  const int chan = chan0 + (live ? 32 * w : 0);
-  const int head = chan / p.P, pc = chan - head * p.P;
+  const bool live = 16 * w < cols;                      // waves without channels still help with copies, scores and gates
+  const int chan0 = g * hp + col0;                      // the workgroup's first channel: the first of a head
+  const int head0 = chan0 / p.P, heads = cols / p.P;
+  const int chan = chan0 + (live ? 16 * w : 0);
+  const int head = chan / p.P, hd = head - head0, pc = chan - head * p.P;
   const long sstride = (long)p.N * p.P;
   const T* x = static_cast<const T*>(p.x);
   const T* dt = static_cast<const T*>(p.dt);
@@ -208,14 +226,17 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   const T* Cp = static_cast<const T*>(p.C) + (long)g * ND;
   T* y = static_cast<T*>(p.y);
   const long HP = (long)p.H * p.P;
-  const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.f;
-  const float skip = OUT && p.D ? p.D[head] : 0.f;
+  // the last waves make the gates, one head each
+  const int ghd = NW - 1 - w;
+  const bool gater = ghd < heads;
+  const int ghead = head0 + (gater ? ghd : 0);
+  const float A = p.A[ghead], bias = p.bias ? p.bias[ghead] : 0.f;
 
-  // element e of tile h[kb][u][pt]: state row 32 kb + 8 q + 4 u + e, column 16 pt + c
-  f32x4 h[NK][2][2];
+  // element e of tile h[kb][u]: state row 32 kb + 8 q + 4 u + e, column c
+  f32x4 h[NK][2];
   auto state_at = [&](const float* s) { return s + (long)head * sstride + pc; };
   auto each_state = [&](auto f) __attribute__((always_inline)) {
-    // made here each time (the asm hides that it is always the same): 64
+    // made here each time (the asm hides that it is always the same): the
     // addresses kept over the chunk loop would spill the state itself
     int at0 = 8 * q * p.P + c;
     asm volatile("" : "+v"(at0));
@@ -224,11 +245,11 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[kb][u][pt][e] = f(h[kb][u][pt][e], at0 + (32 * kb + 4 * u + e) * p.P + 16 * pt);
+        for (int e = 0; e < 4; ++e) h[kb][u][e] = f(h[kb][u][e], at0 + (32 * kb + 4 * u + e) * p.P);
   };
-  auto load_state = [&](const float* s) __attribute__((always_inline)) { each_state([&](float, int at) __attribute__((always_inline)) { return s ? s[at] : 0.f; }); };
+  auto load_state = [&](const float* s) __attribute__((always_inline)) {
+    each_state([&](float, int at) __attribute__((always_inline)) { return s ? s[at] : 0.f; });
+  };
   auto store_state = [&](float* s) __attribute__((always_inline)) {
     if (live) each_state([&](float v, int at) __attribute__((always_inline)) { s[at] = v; return v; });
   };
@@ -270,10 +291,9 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       for (int i = 0; i < Lds::XT; ++i)
         cx[i].issue(lds.x[buf][i], x + (long)t * p.x_stride + chan0 + 128 * i, p.x_stride, len, max(cols - 128 * i, 0));
     };
-    auto load_dt = [&](int t) { rdt = t + l < t1 ? to_f(dt[(long)(t + l) * p.dt_stride + head]) : 0.f; };
-    // The gates of a chunk, lane l its token l: made from dt one chunk ahead.
-    struct { float gam, rem, d, eg, ut, wt, end; } gt;
-    auto gates = [&](int t) __attribute__((always_inline)) {
+    auto load_dt = [&](int t) { rdt = gater && t + l < t1 ? to_f(dt[(long)(t + l) * p.dt_stride + ghead]) : 0.f; };
+    // the gates of the chunk at t, lane l its token l, from the dt loaded for it
+    auto gates = [&](int t, int gb) __attribute__((always_inline)) {
       float d = rdt + bias;
       if (p.softplus) d = softplus_f(d);
       if (t + l >= t1) d = 0.f;
@@ -284,144 +304,115 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         const double o = __shfl_up(gam, m);
         if (l >= m) gam += o;
       }
-      const double end = __shfl(gam, 63);   // tokens behind the last have d = 0
-      gt.d = d;
-      gt.end = (float)end;
-      gt.wt = exp_f((float)(end - gam)) * d;
+      const float gf = (float)gam;
+      lds.gam[gb][ghd][l] = gf;
+      lds.wt[gb][ghd][l] = exp_f((float)(__shfl(gam, 63) - gam)) * d;   // tokens behind the last have d = 0
       if constexpr (OUT) {
-        gt.gam = (float)gam;
-        gt.rem = (float)(gam - (double)gt.gam);
-        gt.eg = exp_f(gt.gam);
-        gt.ut = exp_f((float)(__shfl(gam, l | 15) - gam)) * d;
+        lds.d[gb][ghd][l] = d;
+        lds.eg[gb][ghd][l] = exp_f(gf);
+        lds.ut[gb][ghd][l] = exp_f((float)(__shfl(gam, l | 15) - gam)) * d;
+        if constexpr (F32) lds.rem[gb][ghd][l] = (float)(gam - (double)gf);
       }
     };
     lds_barrier();   // the tiles of the run before are no longer read
     load_dt(t0);
     if constexpr (Lds::NBUF == 2) copy(t0, 0);
-    gates(t0);
-    int buf = 0;
+    if (gater) gates(t0, 0);
+    load_dt(t0 + SC);
+    int buf = 0, gb = 0;
     for (int t = t0; t < t1; t += SC) {
       const int len = min(SC, t1 - t);
-      const float gend = gt.end;
-      if constexpr (OUT) {
-        lds.gam[w][l] = gt.gam;
-        if constexpr (F32) lds.rem[w][l] = gt.rem;
-        lds.d[w][l] = gt.d;
-        lds.eg[w][l] = gt.eg;
-        lds.ut[w][l] = gt.ut;
-      }
-      lds.wt[w][l] = gt.wt;
-      total_gam += gend;
       if constexpr (Lds::NBUF == 1) {
         lds_barrier();
         copy(t, 0);
       }
       __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies have landed
-      lds_barrier();                        // everyone's have, and the other buffer is no longer read
-      if (t + SC < t1) {
-        load_dt(t + SC);
-        if constexpr (Lds::NBUF == 2) copy(t + SC, buf ^ 1);
-      }
+      lds_barrier();                        // everyone's have, and the other buffers are no longer read
+      if constexpr (Lds::NBUF == 2)
+        if (t + SC < t1) copy(t + SC, buf ^ 1);
       const T* tb = lds.b[buf];
       const T* tc = lds.c[OUT ? buf : 0];
-      const T* tx = lds.x[buf][w / 4];
-      frag xf[2][2];   // x^T: columns 16 pt.., tokens 32 jb..
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-        for (int jb = 0; jb < 2; ++jb) xf[pt][jb] = rd.down_x(tx, jb, pt);
 
       if constexpr (OUT) {
-        // scores, transposed: tile (jt, it) holds B_j . C_i, rows j, columns i
+        // scores, transposed: tile (jt, it) holds B_j . C_i, rows j, columns i.
+        // Tiles left of the diagonal take e^{gam_i - gam_j} as two factors at
+        // the end of tile jt, both at most 1: one exponential for four values.
         for (int idx = w; idx < 10; idx += NW) {
           const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
           f32x4 s = zero4();
 #pragma unroll
-          for (int kb = 0; kb < NK; ++kb)
-            s = K::mma(rd.along(tb, jt, kb), rd.along(tc, it, kb), s);
-          lds.score[idx * 64 + l] = s;
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // y^T, rows = channels, columns = tokens: first e^{gam_i} h^T C_i
-        f32x4 acc[4][2];
+          for (int kb = 0; kb < NK; ++kb) s = K::mma(rd.along(tb, jt, kb), rd.along(tc, it, kb), s);
+#pragma unroll 1
+          for (int k = 0; k < heads; ++k) {
+            const float* gk = lds.gam[gb][k];
+            const float gi = gk[16 * it + c];
+            f32x4 pm;
+            if (jt < it) {
+              const f32x4 uj = *reinterpret_cast<const f32x4*>(&lds.ut[gb][k][16 * jt + 4 * q]);
+              float df = gi - gk[16 * jt + 15];
+              if constexpr (F32) df += lds.rem[gb][k][16 * it + c] - lds.rem[gb][k][16 * jt + 15];
+              pm = s * (uj * exp_f(df));
+            } else {
+              const f32x4 gj = *reinterpret_cast<const f32x4*>(&gk[16 * jt + 4 * q]);
+              const f32x4 dj = *reinterpret_cast<const f32x4*>(&lds.d[gb][k][16 * jt + 4 * q]);
+              f32x4 rj = zero4();
+              float ri = 0.f;
+              if constexpr (F32) {
+                rj = *reinterpret_cast<const f32x4*>(&lds.rem[gb][k][16 * jt + 4 * q]);
+                ri = lds.rem[gb][k][16 * it + c];
+              }
+              const float skip = p.D ? p.D[head0 + k] : 0.f;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) acc[it][0] = acc[it][1] = zero4();
+              for (int e = 0; e < 4; ++e) {
+                const float v = s[e] * (exp_f(gi - gj[e] + (ri - rj[e])) * dj[e]);
+                // D x_i joins the product as the diagonal's part of it
+                pm[e] = 4 * q + e < c ? v : 4 * q + e == c ? v + skip : 0.f;
+              }
+            }
+            lds.score[k][idx * 64 + l] = K::four(pm);
+          }
+        }
+      }
+      if (gater && t + SC < t1) gates(t + SC, gb ^ 1);
+      if (t + 2 * SC < t1) load_dt(t + 2 * SC);
+
+      f32x4 acc[4];
+      if constexpr (OUT) {
+        // y^T, rows = channels, columns = tokens: first e^{gam_i} h^T C_i
+#pragma unroll
+        for (int it = 0; it < 4; ++it) acc[it] = zero4();
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-          const frag h0 = K::acc(h[kb][0][0], h[kb][1][0]), h1 = K::acc(h[kb][0][1], h[kb][1][1]);
+          const frag hf = K::acc(h[kb][0], h[kb][1]);
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const frag cf = rd.along(tc, it, kb);
-            acc[it][0] = K::mma(h0, cf, acc[it][0]);
-            acc[it][1] = K::mma(h1, cf, acc[it][1]);
-          }
-          __builtin_amdgcn_sched_barrier(0);   // one block's operands at a time in registers
+          for (int it = 0; it < 4; ++it) acc[it] = K::mma(hf, rd.along(tc, it, kb), acc[it]);
         }
-        lds_barrier();
+#pragma unroll
+        for (int it = 0; it < 4; ++it) acc[it] *= lds.eg[gb][hd][16 * it + c];
+        lds_barrier();   // the scores are there
+      }
+      frag xf[2];   // x^T: this wave's columns, tokens 32 jb..
+#pragma unroll
+      for (int jb = 0; jb < 2; ++jb) xf[jb] = rd.down_x(lds.x[buf][w / 8], jb);
+      if constexpr (OUT) {
+        // then the tokens of the chunk up to i
         const rsrc_t yr = make_rsrc_u(y + (long)t * HP, (long)len * HP * (long)sizeof(T));
         const uint32_t yoff = (uint32_t)((c * (int)HP + chan + 4 * q) * (int)sizeof(T));
-        // then the tokens of the chunk up to i.  Tiles left of the diagonal
-        // take e^{gam_i - gam_j} as two factors at the end of tile jt, both
-        // at most 1, which saves three quarters of their exponentials.
+        const typename K::quad* sc = lds.score[hd] + l;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
           if (16 * it >= len) break;
-          const int i = 16 * it + c;
-          const float gi = lds.gam[w][i], ei = lds.eg[w][i];
-          const float ri = F32 ? lds.rem[F32 ? w : 0][i] : 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[it][0][e] *= ei;
-            acc[it][1][e] *= ei;
-          }
 #pragma unroll
           for (int jb = 0; 2 * jb <= it; ++jb) {
-            f32x4 pm[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int jt = 2 * jb + k;
-              pm[k] = zero4();
-              if (jt > it) continue;
-              const f32x4 s = lds.score[(it * (it + 1) / 2 + jt) * 64 + l];
-              if (jt < it) {
-                const f32x4 uj = *reinterpret_cast<const f32x4*>(&lds.ut[w][16 * jt + 4 * q]);
-                float df = gi - lds.gam[w][16 * jt + 15];
-                if constexpr (F32) df += ri - lds.rem[w][16 * jt + 15];
-                const float f = exp_f(df);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) pm[k][e] = s[e] * (uj[e] * f);
-              } else {
-                const f32x4 gj = *reinterpret_cast<const f32x4*>(&lds.gam[w][16 * jt + 4 * q]);
-                const f32x4 dj = *reinterpret_cast<const f32x4*>(&lds.d[w][16 * jt + 4 * q]);
-                f32x4 rj = zero4();
-                if constexpr (F32) rj = *reinterpret_cast<const f32x4*>(&lds.rem[w][16 * jt + 4 * q]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float df = gi - gj[e];
-                  if constexpr (F32) df += ri - rj[e];
-                  const float v = s[e] * (exp_f(df) * dj[e]);
-                  // D x_i joins the product as the diagonal's part of it
-                  pm[k][e] = 4 * q + e < c ? v : 4 * q + e == c ? v + skip : 0.f;
-                }
-              }
-            }
-            const frag pf = K::acc(pm[0], pm[1]);
-            acc[it][0] = K::mma(xf[0][jb], pf, acc[it][0]);
-            acc[it][1] = K::mma(xf[1][jb], pf, acc[it][1]);
+            const typename K::quad* s0 = sc + (it * (it + 1) / 2 + 2 * jb) * 64;
+            acc[it] = K::mma(xf[jb], K::join(s0[0], 2 * jb < it ? s0[64] : K::four(zero4())), acc[it]);
           }
           // rows behind the chunk's last lie behind the descriptor
           if (live) {
-#pragma unroll
-            for (int pt = 0; pt < 2; ++pt) {
-              const uint32_t off = yoff + (uint32_t)((16 * it * (int)HP + 16 * pt) * (int)sizeof(T));
-              if constexpr (F32) {
-                buf_store16(yr, off, __builtin_bit_cast(uint4, acc[it][pt]));
-              } else {
-                buf_store8(yr, off, make_uint2(K::pair(acc[it][pt][0], acc[it][pt][1]), K::pair(acc[it][pt][2], acc[it][pt][3])));
-              }
-            }
+            const uint32_t off = yoff + (uint32_t)(16 * it * (int)HP * (int)sizeof(T));
+            if constexpr (F32) buf_store16(yr, off, __builtin_bit_cast(uint4, acc[it]));
+            else buf_store8(yr, off, K::four(acc[it]));
           }
-          __builtin_amdgcn_sched_barrier(0);   // and one tile's
         }
       }
 
@@ -429,54 +420,54 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       // product w x is taken as three bf16 terms of 8 bits each, so that the
       // state is as exact as fp32 operands would make it (one term would leave
       // 2^-8, two 2^-16); B and x are bf16 as they are.
-      if (t + SC < t1) gates(t + SC);
-      const float en = exp_f(gend);
+      const float gend = lds.gam[gb][hd][SC - 1], en = exp_f(gend);
+      total_gam += gend;
 #pragma unroll
       for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int pt = 0; pt < 2; ++pt) h[kb][u][pt] *= en;
+        for (int u = 0; u < 2; ++u) h[kb][u] *= en;
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb) {
         if (32 * jb >= len) break;
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds.wt[w][32 * jb + 4 * q]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds.wt[w][32 * jb + 16 + 4 * q]);
+        f32x4 u0 = *reinterpret_cast<const f32x4*>(&lds.wt[gb][hd][32 * jb + 4 * q]);
+        f32x4 u1 = *reinterpret_cast<const f32x4*>(&lds.wt[gb][hd][32 * jb + 16 + 4 * q]);
         constexpr int TERMS = F32 ? 1 : 3;
-        frag wx[TERMS][2];
+        frag wx[TERMS];
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) {
-          f32x4 u, v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            u[e] = K::get(xf[pt][jb], e) * w0[e];
-            v[e] = K::get(xf[pt][jb], 4 + e) * w1[e];
-          }
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            wx[k][pt] = K::acc(u, v);
-            if (k + 1 < TERMS)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                u[e] -= K::get(wx[k][pt], e);
-                v[e] -= K::get(wx[k][pt], 4 + e);
-              }
-          }
+        for (int e = 0; e < 4; ++e) {
+          u0[e] *= K::get(xf[jb], e);
+          u1[e] *= K::get(xf[jb], 4 + e);
         }
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-          const frag b0 = rd.down_b(tb, jb, kb, 0), b1 = rd.down_b(tb, jb, kb, 1);
-          // term by term over the four tiles, so that no product waits for the one before
+        for (int k = 0; k < TERMS; ++k) {
+          wx[k] = K::acc(u0, u1);
+          if (k + 1 < TERMS)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              u0[e] -= K::get(wx[k], e);
+              u1[e] -= K::get(wx[k], 4 + e);
+            }
+        }
+        // two blocks at a time, term by term over their four tiles, so that no
+        // product waits for the one before
+#pragma unroll
+        for (int kb = 0; kb < NK; kb += 2) {
+          constexpr int KB = NK > 1 ? 2 : 1;
+          frag bf[KB][2];
+#pragma unroll
+          for (int i = 0; i < KB; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) bf[i][u] = rd.down_b(tb, jb, kb + i, u);
 #pragma unroll
           for (int k = 0; k < TERMS; ++k)
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt) {
-              h[kb][0][pt] = K::mma(b0, wx[k][pt], h[kb][0][pt]);
-              h[kb][1][pt] = K::mma(b1, wx[k][pt], h[kb][1][pt]);
-            }
+            for (int i = 0; i < KB; ++i)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) h[kb + i][u] = K::mma(bf[i][u], wx[k], h[kb + i][u]);
         }
       }
       if constexpr (Lds::NBUF == 2) buf ^= 1;
+      gb ^= 1;
     }
   };
 
@@ -545,17 +536,17 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmParams p) {
   }
 }
 
-// Waves of a workgroup: 8 (256 channels share the tiles of B and C), or 4
-// where a group has no more than 128 channels, and in fp32, whose tiles take
-// twice the LDS.
+// Waves of a workgroup: 16 (256 channels share the tiles of B and C), or 8
+// where a group has no more than 128 channels, where 256 would be more heads
+// than the gates have room for, and in fp32, whose tiles take twice the LDS.
 static int ssm_waves(DType dt, const SsmParams& p) {
-  return dt == DType::BF16 && p.H / p.G * p.P > 128 ? 8 : 4;
+  return dt == DType::BF16 && p.P >= 64 && p.H / p.G * p.P > 128 ? 16 : 8;
 }
 
 // Segments: enough workgroups for every compute unit, but not under 256
 // tokens, where the two further launches cost more than they save.
 void ssm_plan(DType dt, SsmParams& p) {
-  const int hp = p.H / p.G * p.P, cols = 32 * ssm_waves(dt, p);
+  const int hp = p.H / p.G * p.P, cols = 16 * ssm_waves(dt, p);
   p.wgs = p.G * ((hp + cols - 1) / cols);
   const long most = (p.s.Ttot + 255) / 256;
   long segs = (kComputeUnits + p.wgs - 1) / p.wgs;
@@ -599,8 +590,8 @@ static hipError_t ssm_scan_n(const SsmParams& p, hipStream_t st) {
   return p.N == 64 ? ssm_scan<T, 64, NW>(p, st) : ssm_scan<T, 128, NW>(p, st);
 }
 hipError_t launch_ssm_scan(DType dt, const SsmParams& p, hipStream_t st) {
-  if (dt != DType::BF16) return ssm_scan_n<float, 4>(p, st);
-  return ssm_waves(dt, p) == 8 ? ssm_scan_n<bf16, 8>(p, st) : ssm_scan_n<bf16, 4>(p, st);
+  if (dt != DType::BF16) return ssm_scan_n<float, 8>(p, st);
+  return ssm_waves(dt, p) == 16 ? ssm_scan_n<bf16, 16>(p, st) : ssm_scan_n<bf16, 8>(p, st);
 }
 
 }  // namespace gdr
