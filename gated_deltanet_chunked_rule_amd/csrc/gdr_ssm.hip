@@ -182,9 +182,6 @@ struct SsmLds {
   static constexpr int XT = NW / 8;                                // x tiles of 128 channels
   static constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;              // fp32 fills the LDS with one
   static constexpr int REM = OUT && sizeof(T) == 4;
-  T b[NBUF][SC * ND];
-  T x[NBUF][XT][SC * 128];
-  T c[OUT ? NBUF : 1][OUT ? SC * ND : 8];
   // per head, tiles (jt <= it) of the decayed scores, by lane: rows j, columns i
   typename Blk<T>::quad score[OUT ? SHEADS : 1][OUT ? 10 * 64 : 1];
   // per head and token: gam as a float (and its remainder, fp32), d, e^gam,
@@ -194,6 +191,11 @@ struct SsmLds {
   float d[2][OUT ? SHEADS : 1][OUT ? SC : 1], eg[2][OUT ? SHEADS : 1][OUT ? SC : 1], ut[2][OUT ? SHEADS : 1][OUT ? SC : 1];
   float rem[2][REM ? SHEADS : 1][REM ? SC : 1];
   int32_t cu[SCU];
+  // the tiles last: what stands before them is in reach of an LDS access's
+  // offset field, and needs no address registers of its own
+  alignas(16) T b[NBUF][SC * ND];
+  alignas(16) T x[NBUF][XT][SC * 128];
+  alignas(16) T c[OUT ? NBUF : 1][OUT ? SC * ND : 8];
 };
 
 template <typename T, int ND, int NW, bool OUT>
@@ -208,17 +210,20 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   const int id = xcd_remap(blockIdx.x, total);
   if (id >= total) return;
   const SeqFinder sf = seq_finder<SCU>(p.s, lds.cu);
-  const int hp = p.H / p.G * p.P;                       // channels of a group
+  // quotients come from vector instructions: the same for every lane, they and
+  // the addresses that follow from them go to scalar registers
+  auto div = [](int a, int b) { return __builtin_amdgcn_readfirstlane(a / b); };
+  const int hp = div(p.H, p.G) * p.P;                   // channels of a group
   const int per_group = (hp + COLS - 1) / COLS;
-  const int seg = id / p.wgs, wi = id - seg * p.wgs;
-  const int g = wi / per_group, col0 = (wi - g * per_group) * COLS;
+  const int seg = div(id, p.wgs), wi = id - seg * p.wgs;
+  const int g = div(wi, per_group), col0 = (wi - g * per_group) * COLS;
   const int cols = min(COLS, hp - col0);
   const int w = wave_id(), l = lane_id(), c = l & 15, q = l >> 4;
   const bool live = 16 * w < cols;                      // waves without channels still help with copies, scores and gates
   const int chan0 = g * hp + col0;                      // the workgroup's first channel: the first of a head
-  const int head0 = chan0 / p.P, heads = cols / p.P;
+  const int head0 = div(chan0, p.P), heads = div(cols, p.P);
   const int chan = chan0 + (live ? 16 * w : 0);
-  const int head = chan / p.P, hd = head - head0, pc = chan - head * p.P;
+  const int head = div(chan, p.P), hd = head - head0, pc = chan - head * p.P;
   const long sstride = (long)p.N * p.P;
   const T* x = static_cast<const T*>(p.x);
   const T* dt = static_cast<const T*>(p.dt);
@@ -273,6 +278,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   const int seg0 = seg * p.seg, seg1 = min(seg0 + p.seg, p.s.Ttot);
   float total_gam = 0.f;
   const Reader<T, NB, NX> rd(w);
+  const uint32_t dt_off = (uint32_t)(l * (int)p.dt_stride * (int)sizeof(T));
+  const uint32_t y_off = (uint32_t)((c * (int)HP + chan + 4 * q) * (int)sizeof(T));
   TileCopy<T, NB, NW> cb, cc;
   TileCopy<T, NX, NW> cx[Lds::XT];
   cb.plan(p.b_stride, ND);
@@ -280,6 +287,14 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
 #pragma unroll
   for (int i = 0; i < Lds::XT; ++i) cx[i].plan(p.x_stride, cols - 128 * i);
 
+  // The sequence of token t is the same for every lane: told so, the compiler
+  // keeps what follows from it in scalar registers.
+  auto find = [&](int t, int& start, int& end) {
+    const int n = __builtin_amdgcn_readfirstlane(sf.find(t, start, end));
+    start = __builtin_amdgcn_readfirstlane(start);
+    end = __builtin_amdgcn_readfirstlane(end);
+    return n;
+  };
   // One run of tokens [t0, t1) of a sequence, from the state in h.
   auto run = [&](int t0, int t1) __attribute__((always_inline)) {
     float rdt = 0.f;
@@ -291,7 +306,12 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       for (int i = 0; i < Lds::XT; ++i)
         cx[i].issue(lds.x[buf][i], x + (long)t * p.x_stride + chan0 + 128 * i, p.x_stride, len, max(cols - 128 * i, 0));
     };
-    auto load_dt = [&](int t) { rdt = gater && t + l < t1 ? to_f(dt[(long)(t + l) * p.dt_stride + ghead]) : 0.f; };
+    auto load_dt = [&](int t) __attribute__((always_inline)) {   // tokens behind the run read as zero
+      if (!gater || t >= t1) return;
+      const rsrc_t r = make_rsrc_u(dt + (long)t * p.dt_stride + ghead, ((long)(min(SC, t1 - t) - 1) * p.dt_stride + 1) * (long)sizeof(T));
+      if constexpr (F32) rdt = buf_load_f32(r, dt_off);
+      else rdt = __builtin_bit_cast(float, (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, dt_off, 0, 0) << 16);
+    };
     // the gates of the chunk at t, lane l its token l, from the dt loaded for it
     auto gates = [&](int t, int gb) __attribute__((always_inline)) {
       float d = rdt + bias;
@@ -396,8 +416,6 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       for (int jb = 0; jb < 2; ++jb) xf[jb] = rd.down_x(lds.x[buf][w / 8], jb);
       if constexpr (OUT) {
         // then the tokens of the chunk up to i
-        const rsrc_t yr = make_rsrc_u(y + (long)t * HP, (long)len * HP * (long)sizeof(T));
-        const uint32_t yoff = (uint32_t)((c * (int)HP + chan + 4 * q) * (int)sizeof(T));
         const typename K::quad* sc = lds.score[hd] + l;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -409,9 +427,9 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
           }
           // rows behind the chunk's last lie behind the descriptor
           if (live) {
-            const uint32_t off = yoff + (uint32_t)(16 * it * (int)HP * (int)sizeof(T));
-            if constexpr (F32) buf_store16(yr, off, __builtin_bit_cast(uint4, acc[it]));
-            else buf_store8(yr, off, K::four(acc[it]));
+            const rsrc_t yr = make_rsrc_u(y + (long)(t + 16 * it) * HP, (long)(len - 16 * it) * HP * (long)sizeof(T));
+            if constexpr (F32) buf_store16(yr, y_off, __builtin_bit_cast(uint4, acc[it]));
+            else buf_store8(yr, y_off, K::four(acc[it]));
           }
         }
       }
@@ -473,7 +491,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
 
   if constexpr (!OUT) {
     int start, end;
-    const int n = sf.find(seg1 - 1, start, end);
+    const int n = find(seg1 - 1, start, end);
     float* decay = p.seg_decay + (long)seg * p.H + head;
     const bool through = n >= 0 && end > seg1;     // the sequence goes on behind the segment
     const bool began = start >= seg0;              // and began in it
@@ -486,7 +504,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   } else {
     for (int t = seg0; t < seg1;) {
       int start, end;
-      const int n = sf.find(t, start, end);
+      const int n = find(t, start, end);
       const int stop = min(end, seg1);
       if (n < 0) {
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
