@@ -172,8 +172,34 @@ struct TileCopy {
   }
 };
 
+// A double moved between lanes by a DPP control; lanes without a source, and
+// rows outside the mask, get 0.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Inclusive sum over the lanes of a wave: shifts within the rows of 16, then
+// the last lane of the rows before (no LDS: a sixth of the latency of shuffles).
+__device__ __forceinline__ double wave_scan(double x) {
+  x += dpp_f64<0x111>(x);        // row_shr 1, 2, 4, 8
+  x += dpp_f64<0x112>(x);
+  x += dpp_f64<0x114>(x);
+  x += dpp_f64<0x118>(x);
+  x += dpp_f64<0x142, 0xA>(x);   // lane 15 of a row to rows 1 and 3
+  x += dpp_f64<0x143, 0xC>(x);   // lane 31 to rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane) << 32) |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane));
+}
+
 constexpr int SHEADS = 4;       // heads of a workgroup, at most
-constexpr int SCU = 256;        // staged sequence offsets
+constexpr int SCU = 128;        // staged sequence offsets
 
 template <typename T, int ND, int NW, bool OUT>
 struct SsmLds {
@@ -184,18 +210,23 @@ struct SsmLds {
   static constexpr int REM = OUT && sizeof(T) == 4;
   // per head, tiles (jt <= it) of the decayed scores, by lane: rows j, columns i
   typename Blk<T>::quad score[OUT ? SHEADS : 1][OUT ? 10 * 64 : 1];
-  // per head and token: gam as a float (and its remainder, fp32), d, e^gam,
-  // and two weights: at the end of the token's tile of 16, and in the chunk's
-  // end state.  Two buffers: the next chunk's are made during this one.
-  float gam[2][SHEADS][SC], wt[2][SHEADS][SC];
-  float d[2][OUT ? SHEADS : 1][OUT ? SC : 1], eg[2][OUT ? SHEADS : 1][OUT ? SC : 1], ut[2][OUT ? SHEADS : 1][OUT ? SC : 1];
-  float rem[2][REM ? SHEADS : 1][REM ? SC : 1];
+  // per head and token: gam as a float (and its remainder, fp32), d, and two
+  // weights: at the end of the token's tile of 16, and in the chunk's end
+  // state.  Rings: while one chunk is read, the next one's scores are made
+  // from its gates, and the gates of the one after that are made.
+  float gam[3][SHEADS][SC], wt[3][SHEADS][SC];
+  float d[2][OUT ? SHEADS : 1][OUT ? SC : 1], ut[2][OUT ? SHEADS : 1][OUT ? SC : 1];
+  float rem[3][REM ? SHEADS : 1][REM ? SC : 1];
   int32_t cu[SCU];
   // the tiles last: what stands before them is in reach of an LDS access's
   // offset field, and needs no address registers of its own
   alignas(16) T b[NBUF][SC * ND];
-  alignas(16) T x[NBUF][XT][SC * 128];
+  alignas(16) T x[OUT ? 1 : NBUF][XT][SC * 128];
   alignas(16) T c[OUT ? NBUF : 1][OUT ? SC * ND : 8];
+  // a chunk of y, to leave in whole rows (bf16): the 16 channels of wave w in
+  // row r stand at w ^ (r % NW)
+  static constexpr bool STAGE = OUT && sizeof(T) == 2;
+  alignas(16) T y[STAGE ? SC * 16 * NW : 8];
 };
 
 template <typename T, int ND, int NW, bool OUT>
@@ -298,13 +329,16 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   // One run of tokens [t0, t1) of a sequence, from the state in h.
   auto run = [&](int t0, int t1) __attribute__((always_inline)) {
     float rdt = 0.f;
-    auto copy = [&](int t, int buf) __attribute__((always_inline)) {
-      const int len = min(SC, t1 - t);
-      cb.issue(lds.b[buf], Bp + (long)t * p.b_stride, p.b_stride, len, ND);
-      if constexpr (OUT) cc.issue(lds.c[buf], Cp + (long)t * p.c_stride, p.c_stride, len, ND);
+    auto copy_b = [&](int t, int buf) __attribute__((always_inline)) {
+      cb.issue(lds.b[buf], Bp + (long)t * p.b_stride, p.b_stride, min(SC, t1 - t), ND);
+    };
+    auto copy_c = [&](int t, int buf) __attribute__((always_inline)) {
+      cc.issue(lds.c[buf], Cp + (long)t * p.c_stride, p.c_stride, min(SC, t1 - t), ND);
+    };
+    auto copy_x = [&](int t, int buf) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < Lds::XT; ++i)
-        cx[i].issue(lds.x[buf][i], x + (long)t * p.x_stride + chan0 + 128 * i, p.x_stride, len, max(cols - 128 * i, 0));
+        cx[i].issue(lds.x[buf][i], x + (long)t * p.x_stride + chan0 + 128 * i, p.x_stride, min(SC, t1 - t), max(cols - 128 * i, 0));
     };
     auto load_dt = [&](int t) __attribute__((always_inline)) {   // tokens behind the run read as zero
       if (!gater || t >= t1) return;
@@ -313,92 +347,112 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       else rdt = __builtin_bit_cast(float, (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, dt_off, 0, 0) << 16);
     };
     // the gates of the chunk at t, lane l its token l, from the dt loaded for it
-    auto gates = [&](int t, int gb) __attribute__((always_inline)) {
+    auto gates = [&](int t, int gb, int db) __attribute__((always_inline)) {
       float d = rdt + bias;
       if (p.softplus) d = softplus_f(d);
       if (t + l >= t1) d = 0.f;
       // gam in 64 bits: a difference of two far sums keeps fp32's accuracy
-      double gam = (double)d * (double)A;
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) {
-        const double o = __shfl_up(gam, m);
-        if (l >= m) gam += o;
-      }
+      const double gam = wave_scan((double)d * (double)A);
       const float gf = (float)gam;
       lds.gam[gb][ghd][l] = gf;
-      lds.wt[gb][ghd][l] = exp_f((float)(__shfl(gam, 63) - gam)) * d;   // tokens behind the last have d = 0
+      lds.wt[gb][ghd][l] = exp_f((float)(lane_f64(gam, 63) - gam)) * d;   // tokens behind the last have d = 0
       if constexpr (OUT) {
-        lds.d[gb][ghd][l] = d;
-        lds.eg[gb][ghd][l] = exp_f(gf);
-        lds.ut[gb][ghd][l] = exp_f((float)(__shfl(gam, l | 15) - gam)) * d;
+        lds.d[db][ghd][l] = d;
+        lds.ut[db][ghd][l] = exp_f((float)(dpp_f64<0x15F>(gam) - gam)) * d;   // row_newbcast 15
         if constexpr (F32) lds.rem[gb][ghd][l] = (float)(gam - (double)gf);
       }
     };
-    lds_barrier();   // the tiles of the run before are no longer read
-    load_dt(t0);
-    if constexpr (Lds::NBUF == 2) copy(t0, 0);
-    if (gater) gates(t0, 0);
-    load_dt(t0 + SC);
-    int buf = 0, gb = 0;
-    for (int t = t0; t < t1; t += SC) {
-      const int len = min(SC, t1 - t);
-      if constexpr (Lds::NBUF == 1) {
-        lds_barrier();
-        copy(t, 0);
-      }
-      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies have landed
-      lds_barrier();                        // everyone's have, and the other buffers are no longer read
-      if constexpr (Lds::NBUF == 2)
-        if (t + SC < t1) copy(t + SC, buf ^ 1);
+    // Scores, transposed: tile (jt, it) holds B_j . C_i, rows j, columns i, with
+    // each head's decays.  Tiles left of the diagonal take e^{gam_i - gam_j} as
+    // two factors at the end of tile jt, both at most 1: one exponential for
+    // four values.  All SHEADS rows are made, unused ones from what LDS holds.
+    auto scores = [&](int buf, int gb, int db) __attribute__((always_inline)) {
       const T* tb = lds.b[buf];
       const T* tc = lds.c[OUT ? buf : 0];
-
-      if constexpr (OUT) {
-        // scores, transposed: tile (jt, it) holds B_j . C_i, rows j, columns i.
-        // Tiles left of the diagonal take e^{gam_i - gam_j} as two factors at
-        // the end of tile jt, both at most 1: one exponential for four values.
-        for (int idx = w; idx < 10; idx += NW) {
-          const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
-          f32x4 s = zero4();
+      for (int idx = w; idx < 10; idx += NW) {
+        const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
+        f32x4 s = zero4();
 #pragma unroll
-          for (int kb = 0; kb < NK; ++kb) s = K::mma(rd.along(tb, jt, kb), rd.along(tc, it, kb), s);
-#pragma unroll 1
+        for (int kb = 0; kb < NK; ++kb) s = K::mma(rd.along(tb, jt, kb), rd.along(tc, it, kb), s);
+        if (jt < it) {
+#pragma unroll 2
           for (int k = 0; k < heads; ++k) {
-            const float* gk = lds.gam[gb][k];
-            const float gi = gk[16 * it + c];
+            const f32x4 uj = *reinterpret_cast<const f32x4*>(&lds.ut[db][k][16 * jt + 4 * q]);
+            float df = lds.gam[gb][k][16 * it + c] - lds.gam[gb][k][16 * jt + 15];
+            if constexpr (F32) df += lds.rem[gb][k][16 * it + c] - lds.rem[gb][k][16 * jt + 15];
+            lds.score[k][idx * 64 + l] = K::four(s * (uj * exp_f(df)));
+          }
+        } else {
+#pragma unroll 2
+          for (int k = 0; k < heads; ++k) {
+            const float gi = lds.gam[gb][k][16 * it + c];
+            const f32x4 gj = *reinterpret_cast<const f32x4*>(&lds.gam[gb][k][16 * jt + 4 * q]);
+            const f32x4 dj = *reinterpret_cast<const f32x4*>(&lds.d[db][k][16 * jt + 4 * q]);
+            f32x4 rj = zero4();
+            float ri = 0.f;
+            if constexpr (F32) {
+              rj = *reinterpret_cast<const f32x4*>(&lds.rem[gb][k][16 * jt + 4 * q]);
+              ri = lds.rem[gb][k][16 * it + c];
+            }
+            const float skip = p.D ? p.D[head0 + k] : 0.f;
             f32x4 pm;
-            if (jt < it) {
-              const f32x4 uj = *reinterpret_cast<const f32x4*>(&lds.ut[gb][k][16 * jt + 4 * q]);
-              float df = gi - gk[16 * jt + 15];
-              if constexpr (F32) df += lds.rem[gb][k][16 * it + c] - lds.rem[gb][k][16 * jt + 15];
-              pm = s * (uj * exp_f(df));
-            } else {
-              const f32x4 gj = *reinterpret_cast<const f32x4*>(&gk[16 * jt + 4 * q]);
-              const f32x4 dj = *reinterpret_cast<const f32x4*>(&lds.d[gb][k][16 * jt + 4 * q]);
-              f32x4 rj = zero4();
-              float ri = 0.f;
-              if constexpr (F32) {
-                rj = *reinterpret_cast<const f32x4*>(&lds.rem[gb][k][16 * jt + 4 * q]);
-                ri = lds.rem[gb][k][16 * it + c];
-              }
-              const float skip = p.D ? p.D[head0 + k] : 0.f;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float v = s[e] * (exp_f(gi - gj[e] + (ri - rj[e])) * dj[e]);
-                // D x_i joins the product as the diagonal's part of it
-                pm[e] = 4 * q + e < c ? v : 4 * q + e == c ? v + skip : 0.f;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const float v = s[e] * (exp_f(gi - gj[e] + (ri - rj[e])) * dj[e]);
+              // D x_i joins the product as the diagonal's part of it
+              pm[e] = 4 * q + e < c ? v : 4 * q + e == c ? v + skip : 0.f;
             }
             lds.score[k][idx * 64 + l] = K::four(pm);
           }
         }
       }
-      if (gater && t + SC < t1) gates(t + SC, gb ^ 1);
-      if (t + 2 * SC < t1) load_dt(t + 2 * SC);
+    };
+    auto next = [](int gb) { return gb == 2 ? 0 : gb + 1; };
 
-      f32x4 acc[4];
+    // Two phases a chunk, a barrier before each.  The first reads C, x and the
+    // chunk's scores; the second reads B, and makes the next chunk's scores
+    // (ten waves) and the gates of the one after that (others).  Tiles are
+    // copied where the phase before has given up their place: B in the first
+    // phase, for the second; C and x in the second, C for the next but one.
+    // The states pass has the second phase only, with two places for each.
+    lds_barrier();   // the tiles of the run before are no longer read
+    load_dt(t0);
+    copy_b(t0, 0);
+    copy_x(t0, 0);
+    if constexpr (OUT) {
+      copy_c(t0, 0);
+      if (Lds::NBUF == 2 && t0 + SC < t1) copy_c(t0 + SC, 1);
+    }
+    if (gater) gates(t0, 0, 0);
+    load_dt(t0 + SC);
+    if (gater && t0 + SC < t1) gates(t0 + SC, 1, 1);
+    load_dt(t0 + 2 * SC);
+    int buf = 0, gb = 0, db = 0;
+    if constexpr (OUT) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+      lds_barrier();
+      scores(0, 0, 0);
+    }
+    for (int t = t0; t < t1; t += SC) {
+      const int len = min(SC, t1 - t);
+      const bool more = t + SC < t1;
+      const int buf1 = Lds::NBUF == 2 ? buf ^ 1 : 0;
+      // This wave's copies of x, C (and B) have landed: vmcnt counts down in
+      // order, and two stores at least were issued behind them.
+      if (Lds::STAGE && t > t0) __builtin_amdgcn_s_waitcnt(0x0F72);
+      else __builtin_amdgcn_s_waitcnt(0x0F70);
+      lds_barrier();   // everyone's have, and the scores are there
+      if (Lds::NBUF == 2 && more) {
+        copy_b(t + SC, buf1);
+        if constexpr (!OUT) copy_x(t + SC, buf1);
+      }
+      frag xf[2];   // x^T: this wave's columns, tokens 32 jb..
+#pragma unroll
+      for (int jb = 0; jb < 2; ++jb) xf[jb] = rd.down_x(lds.x[OUT ? 0 : buf][w / 8], jb);
       if constexpr (OUT) {
         // y^T, rows = channels, columns = tokens: first e^{gam_i} h^T C_i
+        const T* tc = lds.c[buf];
+        f32x4 acc[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it) acc[it] = zero4();
 #pragma unroll
@@ -408,13 +462,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
           for (int it = 0; it < 4; ++it) acc[it] = K::mma(hf, rd.along(tc, it, kb), acc[it]);
         }
 #pragma unroll
-        for (int it = 0; it < 4; ++it) acc[it] *= lds.eg[gb][hd][16 * it + c];
-        lds_barrier();   // the scores are there
-      }
-      frag xf[2];   // x^T: this wave's columns, tokens 32 jb..
-#pragma unroll
-      for (int jb = 0; jb < 2; ++jb) xf[jb] = rd.down_x(lds.x[buf][w / 8], jb);
-      if constexpr (OUT) {
+        for (int it = 0; it < 4; ++it) acc[it] *= exp_f(lds.gam[gb][hd][16 * it + c]);
         // then the tokens of the chunk up to i
         const typename K::quad* sc = lds.score[hd] + l;
 #pragma unroll
@@ -425,19 +473,37 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
             const typename K::quad* s0 = sc + (it * (it + 1) / 2 + 2 * jb) * 64;
             acc[it] = K::mma(xf[jb], K::join(s0[0], 2 * jb < it ? s0[64] : K::four(zero4())), acc[it]);
           }
-          // rows behind the chunk's last lie behind the descriptor
-          if (live) {
+          if constexpr (Lds::STAGE) {
+            *reinterpret_cast<typename K::quad*>(lds.y + ((16 * it + c) * NW + (w ^ (c % NW))) * 16 + 4 * q) = K::four(acc[it]);
+          } else if (live) {   // rows behind the chunk's last lie behind the descriptor
             const rsrc_t yr = make_rsrc_u(y + (long)(t + 16 * it) * HP, (long)(len - 16 * it) * HP * (long)sizeof(T));
-            if constexpr (F32) buf_store16(yr, y_off, __builtin_bit_cast(uint4, acc[it]));
-            else buf_store8(yr, y_off, K::four(acc[it]));
+            buf_store16(yr, y_off, __builtin_bit_cast(uint4, acc[it]));
           }
         }
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // B of the next chunk has landed
+        lds_barrier();                        // second phase
+        if (more) copy_x(t + SC, 0);
+        if (Lds::NBUF == 2 && t + 2 * SC < t1) copy_c(t + 2 * SC, buf);
+        if constexpr (Lds::STAGE) {
+          // whole rows of the workgroup's channels; those behind the last
+          // token or channel lie behind the descriptor
+          const rsrc_t yr = make_rsrc_u(y + (long)t * HP, (long)len * HP * (long)sizeof(T));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int i = (int)threadIdx.x + 64 * NW * k, r = i / (2 * NW), u = (i / 2) % NW, ch = 16 * (u ^ (r % NW)) + 8 * (i & 1);
+            buf_store16(yr, ch < cols ? (uint32_t)((r * (int)HP + chan0 + ch) * 2) : 0x80000000u, *reinterpret_cast<const uint4*>(lds.y + i * 8));
+          }
+        }
+        if (Lds::NBUF == 2 && more) scores(buf1, next(gb), db ^ 1);
       }
+      if (gater && t + 2 * SC < t1) gates(t + 2 * SC, next(next(gb)), db);
+      if (t + 3 * SC < t1) load_dt(t + 3 * SC);
 
       // h' = e^{gam_n} h + B^T (w x), w_j = e^{gam_n - gam_j} d_j.  The fp32
       // product w x is taken as three bf16 terms of 8 bits each, so that the
       // state is as exact as fp32 operands would make it (one term would leave
       // 2^-8, two 2^-16); B and x are bf16 as they are.
+      const T* tb = lds.b[buf];
       const float gend = lds.gam[gb][hd][SC - 1], en = exp_f(gend);
       total_gam += gend;
 #pragma unroll
@@ -482,10 +548,25 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
             for (int i = 0; i < KB; ++i)
 #pragma unroll
               for (int u = 0; u < 2; ++u) h[kb + i][u] = K::mma(bf[i][u], wx[k], h[kb + i][u]);
+          }
+      }
+      if constexpr (Lds::NBUF == 1) {
+        // one place for B and C: the next chunk's come when this one's are read
+        if (more) {
+          lds_barrier();
+          copy_b(t + SC, 0);
+          if constexpr (OUT) copy_c(t + SC, 0);
+          else copy_x(t + SC, 0);
+          if constexpr (OUT) {
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+            lds_barrier();
+            scores(0, next(gb), db ^ 1);
+          }
         }
       }
-      if constexpr (Lds::NBUF == 2) buf ^= 1;
-      gb ^= 1;
+      buf = buf1;
+      gb = next(gb);
+      db ^= 1;
     }
   };
 
