@@ -81,15 +81,16 @@ def _entry(name):
     return fn
 
 
-def _call(dev, name, shape, *args):
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _call(index, fn, shape, *args):
     """Calls an entry point with the tensors' device current and its current stream last."""
-    index = dev.index
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
-        rc = _entry(name)(shape, *args, stream)
+    if _device() == index:
+        rc = fn(shape, *args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = _entry(name)(shape, *args, stream)
+            rc = fn(shape, *args, _raw_stream(index))
     if rc:
         raise GdrError(f"libgdr status {rc}: {load_library().gdr_last_error().decode()}")
 
@@ -101,81 +102,69 @@ def _bytes(name, shape) -> int:
     return n
 
 
-def _workspace(workspace, n, dev):
+def _workspace(workspace, n, index):
     if workspace is None:
-        return torch.empty(n, device=dev, dtype=torch.uint8)
-    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < n:
-        raise GdrError(f"workspace must be a contiguous uint8 tensor of at least {n} bytes on {dev}")
+        return torch.empty(n, device=index, dtype=torch.uint8)
+    if workspace.get_device() != index or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < n:
+        raise GdrError(f"workspace must be a contiguous uint8 tensor of at least {n} bytes on device {index}")
     return workspace
 
 
 def _code(t) -> int:
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return GDR_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return GDR_F32
     raise GdrError(f"unsupported dtype {t.dtype} (bfloat16 or float32)")
 
 
-def _shaped(t, name, shape, dtype):
+# The checks below run on every call of a serving step: one test of what is
+# expected first, and what is wrong with the tensor only where that fails.
+def _refuse(t, name, shape, dtype, index, contiguous=True):
     if tuple(t.shape) != shape:
         raise GdrError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {shape}")
     if t.dtype != dtype:
         raise GdrError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise GdrError(f"{name} must be a device tensor")
+    if t.get_device() != index:
+        raise GdrError(f"{name} is on {t.device}, expected device {index}")
+    if contiguous and not t.is_contiguous():
+        raise GdrError(f"{name} must be contiguous")
 
 
-def _dense(t, name, shape, dtype, dev):
+def _dense(t, name, shape, dtype, index):
     """Pointer of a contiguous device tensor of this shape and type (None stays None)."""
     if t is None:
         return None
-    _shaped(t, name, shape, dtype)
-    if not t.is_cuda:
-        raise GdrError(f"{name} must be a device tensor")
-    if t.device != dev:
-        raise GdrError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise GdrError(f"{name} must be contiguous")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or index < 0 or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, index)
     return t.data_ptr()
 
 
-def _strided(t, name, shape, dtype, dev, lead):
+def _rows_of(t, name, shape, dtype, index, lead):
     """(pointer, token stride) of a tensor whose last dimensions are dense and whose first `lead` ones (batch, token)
     have one stride."""
-    _shaped(t, name, shape, dtype)
-    if not t.is_cuda:
-        raise GdrError(f"{name} must be a device tensor")
-    if t.device != dev:
-        raise GdrError(f"{name} is on {t.device}, expected {dev}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or index < 0:
+        _refuse(t, name, shape, dtype, index, False)
     if t.is_contiguous():
         return t.data_ptr(), 0
+    st = t.stride()
     width = 1
-    for n, st in zip(reversed(shape[lead:]), reversed(t.stride()[lead:])):
-        if n != 1 and st != width:
+    for n, s in zip(reversed(shape[lead:]), reversed(st[lead:])):
+        if n != 1 and s != width:
             raise GdrError(f"{name}: the values of a token must be contiguous")
         width *= n
     if lead == 1:
-        return t.data_ptr(), (t.stride(0) if shape[0] > 1 else 0)   # a stride of 0 (expanded) is refused below
-    B, T = shape[:2]
-    token = t.stride(1) if T > 1 else t.stride(0) if B > 1 else 0
-    if B > 1 and T > 1 and t.stride(0) != T * token:
-        raise GdrError(f"{name}: batch and token must have one stride")
-    return t.data_ptr(), token
-
-
-def _no_overlap(name, t, stride, lead):
-    # 0 stands for dense in the library; an expanded tensor has that stride too
-    tokens = 1
-    for n in t.shape[:lead]:
-        tokens *= n
-    if stride == 0 and tokens > 1 and not t.is_contiguous():
+        token, tokens = (st[0] if shape[0] > 1 else 0), shape[0]
+    else:
+        B, T = shape[:2]
+        token, tokens = (st[1] if T > 1 else st[0] if B > 1 else 0), B * T
+        if B > 1 and T > 1 and st[0] != T * token:
+            raise GdrError(f"{name}: batch and token must have one stride")
+    if token == 0 and tokens > 1:   # 0 stands for dense in the library
         raise GdrError(f"{name}: rows overlap (expanded tensor): call .contiguous()")
-
-
-def _rows_of(t, name, shape, dtype, dev, lead):
-    ptr, stride = _strided(t, name, shape, dtype, dev, lead)
-    if stride == 0:
-        _no_overlap(name, t, stride, lead)
-    return ptr, stride
+    return t.data_ptr(), token
 
 
 def _offsets(cu_seqlens, B, T, dev):
@@ -198,25 +187,27 @@ def _offsets(cu_seqlens, B, T, dev):
     return cu, cu.numel() - 1
 
 
+_grad_enabled = torch._C.is_grad_enabled if hasattr(torch._C, "is_grad_enabled") else torch.is_grad_enabled
+
+
 def _inference(name, *tensors):
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise GdrError(f"{name} offers no gradient: call it under torch.no_grad(), or detach its inputs")
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise GdrError(f"{name} offers no gradient: call it under torch.no_grad(), or detach its inputs")
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _pool(state, name, tail, dtype, dev, rows, slots):
+def _pool(state, name, tail, dtype, index, rows, slots):
     if state.dim() != 1 + len(tail):
         raise GdrError(f"shape mismatch: {name} is {tuple(state.shape)}, expected (slots, {', '.join(map(str, tail))})")
     n = state.shape[0]
-    ptr = _dense(state, name, (n, *tail), dtype, dev)
+    ptr = _dense(state, name, (n, *tail), dtype, index)
     if n < 1 or (slots is None and n < rows):
         raise GdrError(f"{name} holds {n} slots for {rows} rows")
-    return ptr, n, _dense(slots, "slots", (rows,), torch.int32, dev)
+    return ptr, n, _dense(slots, "slots", (rows,), torch.int32, index)
 
 
 _ACT = {None: 0, "none": 0, "silu": 1}
@@ -234,11 +225,11 @@ def _conv_args(x, weight, bias, cu_seqlens, activation):
         raise GdrError("x must be [B, T, D] and weight [D, W]")
     B, T, D = x.shape
     W = weight.shape[1]
-    act, code, dev = _activation(activation), _code(x), x.device
-    xp, xs = _rows_of(x, "x", (B, T, D), x.dtype, dev, 2)
-    wp = _dense(weight, "weight", (D, W), x.dtype, dev)
-    bp = _dense(bias, "bias", (D,), x.dtype, dev)
-    cu, N = _offsets(cu_seqlens, B, T, dev)
+    act, code, dev, ty = _activation(activation), _code(x), x.get_device(), x.dtype
+    xp, xs = _rows_of(x, "x", (B, T, D), ty, dev, 2)
+    wp = _dense(weight, "weight", (D, W), ty, dev)
+    bp = _dense(bias, "bias", (D,), ty, dev)
+    cu, N = _offsets(cu_seqlens, B, T, x.device)
     return _ConvShape(B, T, D, W, N, code, act, xs), xp, wp, bp, cu, N, dev
 
 
@@ -251,7 +242,7 @@ def gdr_causal_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=Non
     hp = _dense(initial_state, "initial_state", state, x.dtype, dev)
     y = torch.empty(x.shape, device=dev, dtype=x.dtype)
     ht = torch.empty(state, device=dev, dtype=x.dtype) if output_final_state else None
-    _call(dev, "gdr_causal_conv_fwd", sh, xp, wp, bp, hp, _ptr(cu), y.data_ptr(), _ptr(ht))
+    _call(dev, _entry("gdr_causal_conv_fwd"), sh, xp, wp, bp, hp, _ptr(cu), y.data_ptr(), _ptr(ht))
     return y, ht
 
 
@@ -269,7 +260,7 @@ def gdr_causal_conv_bwd(x, weight, bias, dy, initial_state=None, dht=None, cu_se
     db = None if bias is None else torch.empty_like(bias)
     dh0 = None if initial_state is None else torch.empty_like(initial_state)
     ws = _workspace(workspace, _bytes("gdr_causal_conv_bwd_workspace_size", sh), dev)
-    _call(dev, "gdr_causal_conv_bwd", sh, xp, wp, bp, hp, _ptr(cu), dyp, dhp, dx.data_ptr(), dw.data_ptr(), _ptr(db),
+    _call(dev, _entry("gdr_causal_conv_bwd"), sh, xp, wp, bp, hp, _ptr(cu), dyp, dhp, dx.data_ptr(), dw.data_ptr(), _ptr(db),
           _ptr(dh0), ws.data_ptr(), ws.numel())
     return dx, dw, db, dh0
 
@@ -278,17 +269,18 @@ def gdr_causal_conv_step(x, state, weight, bias=None, *, slots=None, activation=
     """One new token per row: x [rows, D] (strided), state [slots, W - 1, D] moves on in place.  Returns y [rows, D]."""
     if x.dim() != 2 or weight.dim() != 2:
         raise GdrError("x must be [rows, D] and weight [D, W]")
-    _inference("gdr_causal_conv_step", x, state, weight, bias)
+    if _grad_enabled():
+        _inference("gdr_causal_conv_step", x, state, weight, bias)
     rows, D = x.shape
     W = weight.shape[1]
-    act, code, dev = _activation(activation), _code(x), x.device
-    xp, xs = _rows_of(x, "x", (rows, D), x.dtype, dev, 1)
-    wp = _dense(weight, "weight", (D, W), x.dtype, dev)
-    bp = _dense(bias, "bias", (D,), x.dtype, dev)
-    sp, n, lp = _pool(state, "state", (W - 1, D), x.dtype, dev, rows, slots)
-    y = torch.empty((rows, D), device=dev, dtype=x.dtype)
+    act, code, dev, ty = _activation(activation), _code(x), x.get_device(), x.dtype
+    xp, xs = _rows_of(x, "x", (rows, D), ty, dev, 1)
+    wp = _dense(weight, "weight", (D, W), ty, dev)
+    bp = _dense(bias, "bias", (D,), ty, dev)
+    sp, n, lp = _pool(state, "state", (W - 1, D), ty, dev, rows, slots)
+    y = torch.empty(rows, D, device=dev, dtype=ty)
     if rows:
-        _call(dev, "gdr_causal_conv_step", _ConvShape(rows, 1, D, W, 0, code, act, xs), xp, wp, bp, sp, n, lp, y.data_ptr())
+        _call(dev, _entry("gdr_causal_conv_step"), _ConvShape(rows, 1, D, W, 0, code, act, xs), xp, wp, bp, sp, n, lp, y.data_ptr())
     return y
 
 
@@ -326,19 +318,20 @@ def gdr_step(q, k, v, g, beta, state, scale=None, *, slots=None):
     fp32, state [slots, Hv, K, V] fp32, in place.  Returns o [rows, Hv, V]."""
     if q.dim() != 3 or v.dim() != 3:
         raise GdrError("q and v must be 3-D: [rows, Hq, K] and [rows, Hv, V]")
-    _inference("gdr_step", q, k, v, g, beta, state)
+    if _grad_enabled():
+        _inference("gdr_step", q, k, v, g, beta, state)
     rows, Hq, K = q.shape
     Hv, V = v.shape[1], v.shape[2]
-    code, dev, dt = _code(q), q.device, q.dtype
+    code, dev, dt = _code(q), q.get_device(), q.dtype
     qp, qs = _rows_of(q, "q", (rows, Hq, K), dt, dev, 1)
     kp, ks = _rows_of(k, "k", (rows, Hq, K), dt, dev, 1)
     vp, vs = _rows_of(v, "v", (rows, Hv, V), dt, dev, 1)
     gp = _dense(g, "g", (rows, Hv), torch.float32, dev)
     bp = _dense(beta, "beta", (rows, Hv), torch.float32, dev)
     sp, n, lp = _pool(state, "state", (Hv, K, V), torch.float32, dev, rows, slots)
-    o = torch.empty((rows, Hv, V), device=dev, dtype=dt)
+    o = torch.empty(rows, Hv, V, device=dev, dtype=dt)
     if rows:
-        _call(dev, "gdr_step", _Shape(rows, 1, Hq, Hv, K, V, 0, code), qp, qs, kp, ks, vp, vs, gp, bp,
+        _call(dev, _entry("gdr_step"), _Shape(rows, 1, Hq, Hv, K, V, 0, code), qp, qs, kp, ks, vp, vs, gp, bp,
               K ** -0.5 if scale is None else float(scale), sp, n, lp, o.data_ptr())
     return o
 
@@ -350,10 +343,11 @@ def gdr_ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, c
     [H] fp32; initial_state [N_seqs, H, N, P] fp32.  Returns (y, final_state or None).  No gradient."""
     if x.dim() != 4 or B.dim() != 4:
         raise GdrError("x and B must be 4-D: [batch, T, H, P] and [batch, T, G, N]")
-    _inference("gdr_ssm_scan_fwd", x, dt, A, B, C, D, dt_bias, initial_state)
+    if _grad_enabled():
+        _inference("gdr_ssm_scan_fwd", x, dt, A, B, C, D, dt_bias, initial_state)
     b, T, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
-    code, dev, ty = _code(x), x.device, x.dtype
+    code, dev, ty = _code(x), x.get_device(), x.dtype
     xp, xs = _rows_of(x, "x", (b, T, H, P), ty, dev, 2)
     dp, ds = _rows_of(dt, "dt", (b, T, H), ty, dev, 2)
     Bp, bs = _rows_of(B, "B", (b, T, G, N), ty, dev, 2)
@@ -361,13 +355,13 @@ def gdr_ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, c
     Ap = _dense(A, "A", (H,), torch.float32, dev)
     Dp = _dense(D, "D", (H,), torch.float32, dev)
     ip = _dense(dt_bias, "dt_bias", (H,), torch.float32, dev)
-    cu, S = _offsets(cu_seqlens, b, T, dev)
+    cu, S = _offsets(cu_seqlens, b, T, x.device)
     hp = _dense(initial_state, "initial_state", (S, H, N, P), torch.float32, dev)
     sh = _SsmShape(b, T, H, G, P, N, S, code, 1 if dt_softplus else 0, xs, ds, bs, cs)
     y = torch.empty((b, T, H, P), device=dev, dtype=ty)
     ht = torch.empty((S, H, N, P), device=dev, dtype=torch.float32) if output_final_state else None
     ws = _workspace(workspace, _bytes("gdr_ssm_scan_fwd_workspace_size", sh), dev)
-    _call(dev, "gdr_ssm_scan_fwd", sh, xp, dp, Ap, Bp, Cp, Dp, ip, hp, _ptr(cu), y.data_ptr(), _ptr(ht), ws.data_ptr(),
+    _call(dev, _entry("gdr_ssm_scan_fwd"), sh, xp, dp, Ap, Bp, Cp, Dp, ip, hp, _ptr(cu), y.data_ptr(), _ptr(ht), ws.data_ptr(),
           ws.numel())
     return y, ht
 
@@ -377,10 +371,11 @@ def gdr_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None, dt_
     [slots, H, N, P] fp32, in place.  Returns y [rows, H, P]."""
     if x.dim() != 3 or B.dim() != 3:
         raise GdrError("x and B must be 3-D: [rows, H, P] and [rows, G, N]")
-    _inference("gdr_ssm_step", x, dt, A, B, C, state, D, dt_bias)
+    if _grad_enabled():
+        _inference("gdr_ssm_step", x, dt, A, B, C, state, D, dt_bias)
     rows, H, P = x.shape
     G, N = B.shape[1], B.shape[2]
-    code, dev, ty = _code(x), x.device, x.dtype
+    code, dev, ty = _code(x), x.get_device(), x.dtype
     xp, xs = _rows_of(x, "x", (rows, H, P), ty, dev, 1)
     dp, ds = _rows_of(dt, "dt", (rows, H), ty, dev, 1)
     Bp, bs = _rows_of(B, "B", (rows, G, N), ty, dev, 1)
@@ -389,23 +384,20 @@ def gdr_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None, dt_
     Dp = _dense(D, "D", (H,), torch.float32, dev)
     ip = _dense(dt_bias, "dt_bias", (H,), torch.float32, dev)
     sp, n, lp = _pool(state, "state", (H, N, P), torch.float32, dev, rows, slots)
-    y = torch.empty((rows, H, P), device=dev, dtype=ty)
+    y = torch.empty(rows, H, P, device=dev, dtype=ty)
     if rows:
-        _call(dev, "gdr_ssm_step", _SsmShape(rows, 1, H, G, P, N, 0, code, 1 if dt_softplus else 0, xs, ds, bs, cs),
+        _call(dev, _entry("gdr_ssm_step"), _SsmShape(rows, 1, H, G, P, N, 0, code, 1 if dt_softplus else 0, xs, ds, bs, cs),
               xp, dp, Ap, Bp, Cp, Dp, ip, sp, n, lp, y.data_ptr())
     return y
 
 
 # -------------------------------------------------------------------- norm --
-def _norm_rows(t, name, shape, dtype, dev):
+def _norm_rows(t, name, shape, dtype, index):
     """(pointer, outer stride, inner stride) of [..., inner, dim] rows; all leading dimensions have one stride."""
     if t is None:
         return None, 0, 0
-    _shaped(t, name, shape, dtype)
-    if not t.is_cuda:
-        raise GdrError(f"{name} must be a device tensor")
-    if t.device != dev:
-        raise GdrError(f"{name} is on {t.device}, expected {dev}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or index < 0:
+        _refuse(t, name, shape, dtype, index, False)
     if t.is_contiguous():
         return t.data_ptr(), 0, 0
     st = t.stride()
@@ -433,11 +425,10 @@ def _norm_rows(t, name, shape, dtype, dev):
 def _norm_shape(x):
     if x.dim() < 2:
         raise GdrError("x must be [..., dim] with at least two dimensions")
-    shape = tuple(x.shape)
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    return shape, rows, (shape[-2] if len(shape) > 2 and rows else 1), shape[-1]
+    shape = x.shape
+    dim = shape[-1]
+    rows = x.numel() // dim if dim else 0
+    return shape, rows, (shape[-2] if len(shape) > 2 and rows else 1), dim
 
 
 def gdr_rms_norm_fwd(x, weight, residual=None, gate=None, *, eps=1e-6, quant=False):
@@ -445,16 +436,16 @@ def gdr_rms_norm_fwd(x, weight, residual=None, gate=None, *, eps=1e-6, quant=Fal
     (strided).  Returns (y, scales, h): with quant, y is float8_e4m3fn and scales [..., ceil(dim / 128)] fp32 hold one
     scale for each 128 values; h is the sum x + residual (None without a residual)."""
     shape, rows, inner, dim = _norm_shape(x)
-    code, dev, dt = _code(x), x.device, x.dtype
+    code, dev, dt = _code(x), x.get_device(), x.dtype
     xp, xo, xi = _norm_rows(x, "x", shape, dt, dev)
     rp, ro, ri = _norm_rows(residual, "residual", shape, dt, dev)
     gp, go, gi = _norm_rows(gate, "gate", shape, dt, dev)
     wp = _dense(weight, "weight", (dim,), dt, dev)
-    y = torch.empty(shape, device=dev, dtype=torch.float8_e4m3fn if quant else dt)
-    scales = torch.empty((*shape[:-1], (dim + 127) // 128), device=dev, dtype=torch.float32) if quant else None
-    h = torch.empty(shape, device=dev, dtype=dt) if residual is not None else None
+    y = torch.empty(*shape, device=dev, dtype=torch.float8_e4m3fn if quant else dt)
+    scales = torch.empty(*shape[:-1], (dim + 127) // 128, device=dev, dtype=torch.float32) if quant else None
+    h = torch.empty(*shape, device=dev, dtype=dt) if residual is not None else None
     sh = _NormShape(rows, inner, dim, code, eps, 1 if quant else 0, xo, xi, ro, ri, go, gi)
-    _call(dev, "gdr_rms_norm_fwd", sh, xp, rp, gp, wp, y.data_ptr(), _ptr(scales), _ptr(h))
+    _call(dev, _entry("gdr_rms_norm_fwd"), sh, xp, rp, gp, wp, y.data_ptr(), _ptr(scales), _ptr(h))
     return y, scales, h
 
 
@@ -462,7 +453,7 @@ def gdr_rms_norm_bwd(h, weight, dy, gate=None, dres=None, *, eps=1e-6, workspace
     """Backward of gdr_rms_norm_fwd at h = x + residual; dres is the gradient of h from elsewhere.  Returns
     (dh, dw, dgate); dh is the gradient of x and of residual, dgate is None without a gate."""
     shape, rows, inner, dim = _norm_shape(h)
-    code, dev, dt = _code(h), h.device, h.dtype
+    code, dev, dt = _code(h), h.get_device(), h.dtype
     hp, ho, hi = _norm_rows(h, "h", shape, dt, dev)
     gp, go, gi = _norm_rows(gate, "gate", shape, dt, dev)
     wp = _dense(weight, "weight", (dim,), dt, dev)
@@ -473,7 +464,7 @@ def gdr_rms_norm_bwd(h, weight, dy, gate=None, dres=None, *, eps=1e-6, workspace
     dgate = torch.empty(shape, device=dev, dtype=dt) if gate is not None else None
     sh = _NormShape(rows, inner, dim, code, eps, 0, ho, hi, 0, 0, go, gi)
     ws = _workspace(workspace, _bytes("gdr_rms_norm_bwd_workspace_size", sh), dev)
-    _call(dev, "gdr_rms_norm_bwd", sh, hp, gp, wp, dyp, drp, dh.data_ptr(), dw.data_ptr(), _ptr(dgate), ws.data_ptr(),
+    _call(dev, _entry("gdr_rms_norm_bwd"), sh, hp, gp, wp, dyp, drp, dh.data_ptr(), dw.data_ptr(), _ptr(dgate), ws.data_ptr(),
           ws.numel())
     return dh, dw, dgate
 
