@@ -273,32 +273,42 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
   vec_store<float, VEC>(part + (long)W * p.D, nd, db);
 }
 
-// dw[d][j], db[d]: the tiles' partial sums, in 4 strands of every fourth tile
-// that are then added in order.
+// dw[d][j], db[d]: the tiles' partial sums, in 32 strands of every 32nd tile
+// that are then added in order; 32 columns a workgroup (128-byte pieces).
 template <typename T, int W>
 __global__ __launch_bounds__(256) void k_conv_dw(ConvParams p) {
-  __shared__ float acc[4][W + 1][64];
-  const int lane = threadIdx.x & 63, strand = threadIdx.x >> 6;
-  const int d = blockIdx.x * 64 + lane;
-  float s[W + 1];
+  __shared__ f32x4 acc[32][W + 1][8];
+  const int lane = threadIdx.x & 7, strand = threadIdx.x >> 3;
+  const int d = blockIdx.x * 32 + 4 * lane, nd = min(4, p.D - d);
+  f32x4 s[W + 1];
 #pragma unroll
-  for (int j = 0; j <= W; ++j) s[j] = 0.f;
-  if (d < p.D)
-    for (int tile = strand; tile < p.tiles; tile += 4) {
+  for (int j = 0; j <= W; ++j) s[j] = zero4();
+  if (nd > 0)
+    for (int tile = strand; tile < p.tiles; tile += 32) {
       const float* q = p.part + (long)tile * (W + 1) * p.D + d;
 #pragma unroll
-      for (int j = 0; j <= W; ++j) s[j] += q[(long)j * p.D];
+      for (int j = 0; j <= W; ++j) {
+        float f[4];
+        vec_load<float, 4>(q + (long)j * p.D, nd, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] += f[e];
+      }
     }
 #pragma unroll
   for (int j = 0; j <= W; ++j) acc[strand][j][lane] = s[j];
   __syncthreads();
-  if (strand != 0 || d >= p.D) return;
+  // thread (j, column group) adds the strands
+  const int j = threadIdx.x >> 3;
+  if (j > W || nd <= 0) return;
+  f32x4 v = zero4();
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) v += acc[i][j][lane];
 #pragma unroll
-  for (int j = 0; j <= W; ++j) {
-    const float v = (acc[0][j][lane] + acc[1][j][lane]) + (acc[2][j][lane] + acc[3][j][lane]);
-    if (j < W) static_cast<T*>(p.dw)[(long)d * W + j] = from_f<T>(v);
-    else if (p.db) static_cast<T*>(p.db)[d] = from_f<T>(v);
-  }
+  for (int e = 0; e < 4; ++e)
+    if (e < nd) {
+      if (j < W) static_cast<T*>(p.dw)[(long)(d + e) * W + j] = from_f<T>(v[e]);
+      else if (p.db) static_cast<T*>(p.db)[d + e] = from_f<T>(v[e]);
+    }
 }
 
 // One new token per row: blocks of one wave walk the channels of one row.
@@ -373,7 +383,7 @@ static hipError_t conv_bwd(const ConvParams& p, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   timing_before("conv_dw", st);
-  hipLaunchKernelGGL((k_conv_dw<T, W>), dim3((unsigned)((p.D + 63) / 64)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((k_conv_dw<T, W>), dim3((unsigned)((p.D + 31) / 32)), dim3(256), 0, st, p);
   e = hipGetLastError();
   timing_after(st);
   return e;

@@ -59,90 +59,110 @@ __device__ __forceinline__ long row_at(long row, int inner, long outer_stride, l
   return o * outer_stride + (row - o * inner) * inner_stride;
 }
 
-template <typename T, int TPR, int NV, bool QUANT>
+// Short rows (a head's 64 to 512 values) go R to a lane group: one row has but
+// two 16-byte loads per lane in flight.
+template <typename T, int TPR, int NV, int R, bool QUANT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+  static_assert(R == 1 || TPR <= 64, "rows of several waves meet in LDS, one at a time");
   __shared__ float red[NT / 64][2];
   const int t = threadIdx.x & (TPR - 1);
-  const long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool live = row < p.rows;   // rows behind the last read row 0 and write nothing
-  const long rr = live ? row : 0;
-  const T* x = static_cast<const T*>(p.x) + row_at(rr, p.inner, p.xo, p.xi);
-  const T* res = p.residual ? static_cast<const T*>(p.residual) + row_at(rr, p.inner, p.ro, p.ri) : nullptr;
-  const T* gate = p.gate ? static_cast<const T*>(p.gate) + row_at(rr, p.inner, p.go, p.gi) : nullptr;
-  typename VecIO<T, 8>::raw raw[NV], rawr[NV], rawg[NV];
+  typename VecIO<T, 8>::raw raw_r[R][NV], rawr_r[R][NV], rawg_r[R][NV];
+  float w[NV][8];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int d = (v * TPR + t) * 8;
-    raw[v] = vec_raw<T, 8>(x + d, max(0, p.dim - d));
-    if (res) rawr[v] = vec_raw<T, 8>(res + d, max(0, p.dim - d));
-    if (gate) rawg[v] = vec_raw<T, 8>(gate + d, max(0, p.dim - d));
-  }
-  float h[NV][8], ss = 0.f, unused = 0.f;
+  for (int k = 0; k < R; ++k) {
+    const long row = ((long)blockIdx.x * R + k) * RPB + threadIdx.x / TPR;
+    const bool live = row < p.rows;   // rows behind the last read row 0 and write nothing
+    const long rr = live ? row : 0;
+    const T* x = static_cast<const T*>(p.x) + row_at(rr, p.inner, p.xo, p.xi);
+    const T* res = p.residual ? static_cast<const T*>(p.residual) + row_at(rr, p.inner, p.ro, p.ri) : nullptr;
+    const T* gate = p.gate ? static_cast<const T*>(p.gate) + row_at(rr, p.inner, p.go, p.gi) : nullptr;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    VecIO<T, 8>::up(raw[v], h[v]);
-    if (res) {
-      float f[8];
-      VecIO<T, 8>::up(rawr[v], f);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) h[v][c] += f[c];
+    for (int v = 0; v < NV; ++v) {
+      const int d = (v * TPR + t) * 8;
+      raw_r[k][v] = vec_raw<T, 8>(x + d, max(0, p.dim - d));
+      if (res) rawr_r[k][v] = vec_raw<T, 8>(res + d, max(0, p.dim - d));
+      if (gate) rawg_r[k][v] = vec_raw<T, 8>(gate + d, max(0, p.dim - d));
     }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) ss = fmaf(h[v][c], h[v][c], ss);
   }
-  row_sum2<TPR>(ss, unused, red);
-  const float r = 1.f / sqrtf(ss / (float)p.dim + p.eps);
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
-    if (p.h_out && live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.h_out) + row * p.dim + d, nd, h[v]);
-    float w[8], y[8];
-    vec_load<T, 8>(static_cast<const T*>(p.weight) + d, max(0, nd), w);
+  for (int v = 0; v < NV; ++v) vec_load<T, 8>(static_cast<const T*>(p.weight) + (v * TPR + t) * 8, max(0, p.dim - (v * TPR + t) * 8), w[v]);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) y[c] = h[v][c] * r * w[c];
-    if (gate) {
-      float g[8];
-      VecIO<T, 8>::up(rawg[v], g);
+  for (int k = 0; k < R; ++k) {
+    const long row = ((long)blockIdx.x * R + k) * RPB + threadIdx.x / TPR;
+    const bool live = row < p.rows;
+    const auto& raw = raw_r[k];
+    const auto& rawr = rawr_r[k];
+    const auto& rawg = rawg_r[k];
+    const bool res = p.residual != nullptr, gate = p.gate != nullptr;
+    float h[NV][8], ss = 0.f, unused = 0.f;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) y[c] *= g[c] * sigmoid_f(g[c]);
-    }
-    if constexpr (QUANT) {
-      // a group of 128 values is 16 lanes of 8; the largest magnitude is taken
-      // on the bits, where a NaN is above everything
-      uint32_t m = 0;
+    for (int v = 0; v < NV; ++v) {
+      VecIO<T, 8>::up(raw[v], h[v]);
+      if (res) {
+        float f[8];
+        VecIO<T, 8>::up(rawr[v], f);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) m = max(m, c < nd ? (__builtin_bit_cast(uint32_t, y[c]) & 0x7fffffffu) : 0u);
-      m = max16_u32(m);
-      m = max(m, __builtin_bit_cast(uint32_t, kQuantTiny));
-      const float scale = __builtin_bit_cast(float, m) / kE4M3Max;
-      if (nd <= 0 || !live) continue;
-      // true division: the value that is rounded is y / scale to half an ulp
-      // (the kernel stays bound by memory), clamped so that the largest one
-      // cannot pass 448 (fminf and fmaxf would drop a NaN, these compares keep it)
-      int q[2] = {0, 0};
-      float f[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        f[c] = y[c] / scale;
-        f[c] = f[c] > kE4M3Max ? kE4M3Max : f[c] < -kE4M3Max ? -kE4M3Max : f[c];
+        for (int c = 0; c < 8; ++c) h[v][c] += f[c];
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);
-        q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], q[i], true);
+      for (int c = 0; c < 8; ++c) ss = fmaf(h[v][c], h[v][c], ss);
+    }
+    row_sum2<TPR>(ss, unused, red);
+    const float r = 1.f / sqrtf(ss / (float)p.dim + p.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+      if (p.h_out && live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.h_out) + row * p.dim + d, nd, h[v]);
+      float y[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) y[c] = h[v][c] * r * w[v][c];
+      if (gate) {
+        float g[8];
+        VecIO<T, 8>::up(rawg[v], g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] *= g[c] * sigmoid_f(g[c]);
       }
-      uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.dim + d;
-      if (nd == 8) {
-        *reinterpret_cast<u32x2_u1*>(out) = u32x2_u1{(uint32_t)q[0], (uint32_t)q[1]};
+      if constexpr (QUANT) {
+        // a group of 128 values is 16 lanes of 8; the largest magnitude is taken
+        // on the bits, where a NaN is above everything
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m = max(m, c < nd ? (__builtin_bit_cast(uint32_t, y[c]) & 0x7fffffffu) : 0u);
+        m = max16_u32(m);
+        m = max(m, __builtin_bit_cast(uint32_t, kQuantTiny));
+        const float scale = __builtin_bit_cast(float, m) / kE4M3Max;
+        if (nd <= 0 || !live) continue;
+        // y times the reciprocal of the scale (an ulp and a half off y / scale; a
+        // true division made heads of 128 bound by its instructions: 50 us where
+        // this takes 39 for 262144 of them), clamped so that the largest
+        // value cannot pass 448 (fminf and fmaxf would drop a NaN, these compares
+        // keep it)
+        const float inv = __builtin_amdgcn_rcpf(scale);
+        int q[2] = {0, 0};
+        float f[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          f[c] = y[c] * inv;
+          f[c] = f[c] > kE4M3Max ? kE4M3Max : f[c] < -kE4M3Max ? -kE4M3Max : f[c];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);
+          q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], q[i], true);
+        }
+        uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.dim + d;
+        if (nd == 8) {
+          *reinterpret_cast<u32x2_u1*>(out) = u32x2_u1{(uint32_t)q[0], (uint32_t)q[1]};
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < nd) out[c] = (uint8_t)((uint32_t)q[c / 4] >> (8 * (c % 4)));
+        }
+        if ((t & 15) == 0) p.scales[row * ((p.dim + 127) / 128) + d / 128] = scale;
       } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c < nd) out[c] = (uint8_t)((uint32_t)q[c / 4] >> (8 * (c % 4)));
+        if (nd > 0 && live) vec_store<T, 8>(static_cast<T*>(p.y) + row * p.dim + d, nd, y);
       }
-      if ((t & 15) == 0) p.scales[row * ((p.dim + 127) / 128) + d / 128] = scale;
-    } else {
-      if (nd > 0 && live) vec_store<T, 8>(static_cast<T*>(p.y) + row * p.dim + d, nd, y);
     }
   }
 }
@@ -157,69 +177,88 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
   __shared__ float red[2][NT / 64][2];
   __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NV * 8 : 1];
   const int t = threadIdx.x & (TPR - 1), sub = threadIdx.x / TPR;
+  typedef typename VecIO<T, 8>::raw raw_t;
   float dw[NV][8];
+  raw_t wr[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    const int d = (v * TPR + t) * 8;
+    wr[v] = vec_raw<T, 8>(static_cast<const T*>(p.weight) + d, max(0, p.dim - d));
 #pragma unroll
     for (int c = 0; c < 8; ++c) dw[v][c] = 0.f;
+  }
   const float inv = 1.f / (float)p.dim;
-  int buf = 0;
-  // every thread of the workgroup makes the same number of steps (barriers)
-  for (long base = (long)blockIdx.x * RPB; base < p.rows; base += (long)gridDim.x * RPB, buf ^= 1) {
-    const long row = base + sub;
-    const bool live = row < p.rows;
-    const long rr = live ? row : 0;
+  const bool gate = p.gate != nullptr, dres = p.dres != nullptr;
+  raw_t hn[NV], gn[NV], zn[NV], sn[NV];   // the next step's row, on its way
+  auto fetch = [&](long row) {
+    const long rr = row < p.rows ? row : 0;
     const T* h = static_cast<const T*>(p.x) + row_at(rr, p.inner, p.xo, p.xi);
     const T* dy = static_cast<const T*>(p.dy) + rr * p.dim;
-    const T* gate = p.gate ? static_cast<const T*>(p.gate) + row_at(rr, p.inner, p.go, p.gi) : nullptr;
-    const T* dres = p.dres ? static_cast<const T*>(p.dres) + rr * p.dim : nullptr;
-    typename VecIO<T, 8>::raw hr[NV], gr[NV], zr[NV], sr[NV];
+    const T* z = static_cast<const T*>(p.gate) + (gate ? row_at(rr, p.inner, p.go, p.gi) : 0);
+    const T* s = static_cast<const T*>(p.dres) + rr * p.dim;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int d = (v * TPR + t) * 8, nd = max(0, p.dim - d);
-      hr[v] = vec_raw<T, 8>(h + d, nd);
-      gr[v] = vec_raw<T, 8>(dy + d, nd);
-      if (gate) zr[v] = vec_raw<T, 8>(gate + d, nd);
-      if (dres) sr[v] = vec_raw<T, 8>(dres + d, nd);
+      hn[v] = vec_raw<T, 8>(h + d, nd);
+      gn[v] = vec_raw<T, 8>(dy + d, nd);
+      if (gate) zn[v] = vec_raw<T, 8>(z + d, nd);
+      if (dres) sn[v] = vec_raw<T, 8>(s + d, nd);
     }
+  };
+  // 1024 lanes have 128 registers each: no room for a second row
+  constexpr bool AHEAD = TPR < 1024;
+  const long step = (long)gridDim.x * RPB;
+  int buf = 0;
+  if (AHEAD && (long)blockIdx.x * RPB < p.rows) fetch((long)blockIdx.x * RPB + sub);
+  // every thread of the workgroup makes the same number of steps (barriers)
+  for (long base = (long)blockIdx.x * RPB; base < p.rows; base += step, buf ^= 1) {
+    const long row = base + sub;
+    const bool live = row < p.rows;
+    if (!AHEAD) fetch(row);
+    float hf[NV][8], g[NV][8];
+    raw_t zr[NV], sr[NV];
     float ss = 0.f, su = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int d = (v * TPR + t) * 8;
-      float hf[8], g[8], w[8];
-      VecIO<T, 8>::up(hr[v], hf);
-      VecIO<T, 8>::up(gr[v], g);
-      vec_load<T, 8>(static_cast<const T*>(p.weight) + d, max(0, p.dim - d), w);
+      float w[8];
+      VecIO<T, 8>::up(hn[v], hf[v]);
+      VecIO<T, 8>::up(gn[v], g[v]);
+      VecIO<T, 8>::up(wr[v], w);
+      zr[v] = zn[v];
+      sr[v] = sn[v];
       if (gate) {
         float z[8];
         VecIO<T, 8>::up(zr[v], z);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) g[c] *= z[c] * sigmoid_f(z[c]);
-      }
+        for (int c = 0; c < 8; ++c) {
+          ss = fmaf(hf[v][c], hf[v][c], ss);
+          su = fmaf(g[v][c] * (z[c] * sigmoid_f(z[c])) * w[c], hf[v][c], su);
+        }
+      } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        ss = fmaf(hf[c], hf[c], ss);
-        su = fmaf(g[c] * w[c], hf[c], su);
+        for (int c = 0; c < 8; ++c) {
+          ss = fmaf(hf[v][c], hf[v][c], ss);
+          su = fmaf(g[v][c] * w[c], hf[v][c], su);
+        }
       }
     }
+    if (AHEAD && base + step < p.rows) fetch(row + step);
     row_sum2<TPR>(ss, su, red[buf]);   // two buffers: the next step's sums do not meet this step's readers
     const float r = 1.f / sqrtf(ss * inv + p.eps);
     const float m = su * r * inv;      // mean(u n)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
-      float hf[8], g[8], w[8], o[8];
-      VecIO<T, 8>::up(hr[v], hf);
-      VecIO<T, 8>::up(gr[v], g);
-      vec_load<T, 8>(static_cast<const T*>(p.weight) + d, max(0, nd), w);
+      float w[8], o[8];
+      VecIO<T, 8>::up(wr[v], w);
       if (gate) {
         float z[8], dz[8];
         VecIO<T, 8>::up(zr[v], z);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float s = sigmoid_f(z[c]);
-          dz[c] = g[c] * hf[c] * r * w[c] * (s * fmaf(z[c], 1.f - s, 1.f));
-          g[c] *= z[c] * s;
+          dz[c] = g[v][c] * hf[v][c] * r * w[c] * (s * fmaf(z[c], 1.f - s, 1.f));
+          g[v][c] *= z[c] * s;
         }
         if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dgate) + row * p.dim + d, nd, dz);
       }
@@ -227,9 +266,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
       if (dres) VecIO<T, 8>::up(sr[v], s);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float n = hf[c] * r;
-        o[c] = r * (g[c] * w[c] - n * m) + (dres ? s[c] : 0.f);
-        dw[v][c] += live ? g[c] * n : 0.f;
+        const float n = hf[v][c] * r;
+        o[c] = r * (g[v][c] * w[c] - n * m) + (dres ? s[c] : 0.f);
+        dw[v][c] += live ? g[v][c] * n : 0.f;
       }
       if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dh) + row * p.dim + d, nd, o);
     }
@@ -256,24 +295,30 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
   }
 }
 
-// dw: the workgroups' partial rows, in 16 strands of every 16th that are then
-// added in order; 16 columns per workgroup keep many workgroups busy at the
-// usual widths.
+// dw: the workgroups' partial rows, in 64 strands of every 64th that are then
+// added in order; 32 columns a workgroup (128-byte pieces of a row) keep the
+// strands short and many compute units busy.
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_dw(NormParams p) {
-  __shared__ float acc[16][17];
-  const int c = threadIdx.x & 15, strand = threadIdx.x >> 4;
-  const int d = blockIdx.x * 16 + c;
-  float s = 0.f;
-  if (d < p.dim)
-    for (int b = strand; b < p.blocks; b += 16) s += p.part[(long)b * p.dim + d];
+__global__ __launch_bounds__(512) void k_norm_dw(NormParams p) {
+  __shared__ f32x4 acc[64][8];
+  const int c = threadIdx.x & 7, strand = threadIdx.x >> 3;
+  const int d = blockIdx.x * 32 + 4 * c, nd = min(4, p.dim - d);
+  f32x4 s = zero4();
+  if (nd > 0)
+    for (int b = strand; b < p.blocks; b += 64) {
+      float f[4];
+      vec_load<float, 4>(p.part + (long)b * p.dim + d, nd, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += f[e];
+    }
   acc[strand][c] = s;
   __syncthreads();
-  if (strand != 0 || d >= p.dim) return;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s += acc[i][c];
-  static_cast<T*>(p.dw)[d] = from_f<T>(s);
+  if (strand != 0 || nd <= 0) return;
+  s = zero4();
+#pragma unroll 8
+  for (int i = 0; i < 64; ++i) s += acc[i][c];
+  const float o[4] = {s[0], s[1], s[2], s[3]};
+  vec_store<T, 4>(static_cast<T*>(p.dw) + d, nd, o);
 }
 
 // Lanes per row and vectors per lane by the row's length.
@@ -287,13 +332,25 @@ __global__ __launch_bounds__(256) void k_norm_dw(NormParams p) {
   else if (p.dim <= 8192) { CALL(512, 2); }    \
   else { CALL(1024, 2); }
 
+template <typename T, int TPR, int NV, int R, bool QUANT>
+static void norm_fwd_launch(const NormParams& p, hipStream_t st) {
+  constexpr int NT = TPR < 256 ? 256 : TPR;
+  const long per = (long)R * (NT / TPR);
+  hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, R, QUANT>), dim3((unsigned)((p.rows + per - 1) / per)), dim3(NT), 0, st, p);
+}
+// Two rows a lane group where that still leaves eight workgroups a compute unit
+// (262144 heads of 128 with gate, to 8 bits: 39 us; one row 40.5, four 41.5).
+template <typename T, int TPR, int NV, bool QUANT>
+static void norm_fwd_rows(const NormParams& p, hipStream_t st) {
+  if constexpr (TPR <= 64) {
+    if (p.rows >= 2L * (256 / TPR) * 8 * kComputeUnits) return norm_fwd_launch<T, TPR, NV, 2, QUANT>(p, st);
+  }
+  norm_fwd_launch<T, TPR, NV, 1, QUANT>(p, st);
+}
 template <typename T, bool QUANT>
 static hipError_t norm_fwd(const NormParams& p, hipStream_t st) {
   timing_before("norm_fwd", st);
-#define CALL(TPR, NV)                                                                                              \
-  hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, QUANT>),                                                              \
-                     dim3((unsigned)((p.rows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))), \
-                     dim3(TPR < 256 ? 256 : TPR), 0, st, p)
+#define CALL(TPR, NV) norm_fwd_rows<T, TPR, NV, QUANT>(p, st)
   NORM_DISPATCH(CALL);
 #undef CALL
   const hipError_t e = hipGetLastError();
@@ -305,11 +362,11 @@ hipError_t launch_norm_fwd(DType dt, bool quant, const NormParams& p, hipStream_
   return quant ? norm_fwd<float, true>(p, st) : norm_fwd<float, false>(p, st);
 }
 
-// Workgroups of the backward: enough to fill the GPU's waves (8 workgroups of
-// 4 waves a compute unit), fewer where the rows end first.
+// Workgroups of the backward: as many as are resident at once by the registers
+// they take, fewer where the rows end first.
 static int norm_rows_per_block(int dim) { return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 512 ? 4 : dim <= 1024 ? 2 : 1; }
 int norm_bwd_blocks(long rows, int dim) {
-  const long want = dim <= 4096 ? 4 * kComputeUnits : dim <= 8192 ? 2 * kComputeUnits : kComputeUnits;
+  const long want = dim <= 2048 ? 4 * kComputeUnits : dim <= 4096 ? 2 * kComputeUnits : kComputeUnits;
   const long most = (rows + norm_rows_per_block(dim) - 1) / norm_rows_per_block(dim);
   return (int)(most < want ? most : want);
 }
@@ -327,7 +384,7 @@ static hipError_t norm_bwd(const NormParams& p, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   timing_before("norm_dw", st);
-  hipLaunchKernelGGL(k_norm_dw<T>, dim3((unsigned)((p.dim + 15) / 16)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL(k_norm_dw<T>, dim3((unsigned)((p.dim + 31) / 32)), dim3(512), 0, st, p);
   e = hipGetLastError();
   timing_after(st);
   return e;
