@@ -16,9 +16,12 @@
 // wave computes a 16 x 16 tile of them and leaves it in LDS with each head's
 // decays applied, so that nothing of it is computed twice; the gates of the
 // next chunk are made meanwhile by waves without a tile.  16 waves of 128
-// registers hide each other's latencies: 8 waves of 32 channels took 76 us
-// where these take SCAN_US (8192 tokens, 64 heads of 64, N = 128), 4 of 64
-// channels took 89.
+// registers hide each other's latencies: their output pass takes 68 us (8192
+// tokens, 64 heads of 64, N = 128) where 8 waves of 32 channels took 76, 4 of
+// 64 channels 89, and two workgroups of 8 waves a compute unit 78.
+// What bounds it: the three-term state update (19 us of it), the chunk's
+// products and decays (21) and the tiles' movement (31) share two barriered
+// phases and overlap in part only.
 //
 // Long prompts are cut into segments that run side by side: a first pass
 // computes what each segment adds to the state and its decay, k_ssm_join
@@ -484,16 +487,6 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         lds_barrier();                        // second phase
         if (more) copy_x(t + SC, 0);
         if (Lds::NBUF == 2 && t + 2 * SC < t1) copy_c(t + 2 * SC, buf);
-        if constexpr (Lds::STAGE) {
-          // whole rows of the workgroup's channels; those behind the last
-          // token or channel lie behind the descriptor
-          const rsrc_t yr = make_rsrc_u(y + (long)t * HP, (long)len * HP * (long)sizeof(T));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int i = (int)threadIdx.x + 64 * NW * k, r = i / (2 * NW), u = (i / 2) % NW, ch = 16 * (u ^ (r % NW)) + 8 * (i & 1);
-            buf_store16(yr, ch < cols ? (uint32_t)((r * (int)HP + chan0 + ch) * 2) : 0x80000000u, *reinterpret_cast<const uint4*>(lds.y + i * 8));
-          }
-        }
         if (Lds::NBUF == 2 && more) scores(buf1, next(gb), db ^ 1);
       }
       if (gater && t + 2 * SC < t1) gates(t + 2 * SC, next(next(gb)), db);
@@ -549,6 +542,16 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
 #pragma unroll
               for (int u = 0; u < 2; ++u) h[kb + i][u] = K::mma(bf[i][u], wx[k], h[kb + i][u]);
           }
+      }
+      if constexpr (Lds::STAGE) {
+        // whole rows of the workgroup's channels; those behind the last
+        // token or channel lie behind the descriptor
+        const rsrc_t yr = make_rsrc_u(y + (long)t * HP, (long)len * HP * (long)sizeof(T));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = (int)threadIdx.x + 64 * NW * k, r = i / (2 * NW), u = (i / 2) % NW, ch = 16 * (u ^ (r % NW)) + 8 * (i & 1);
+          buf_store16(yr, ch < cols ? (uint32_t)((r * (int)HP + chan0 + ch) * 2) : 0x80000000u, *reinterpret_cast<const uint4*>(lds.y + i * 8));
+        }
       }
       if constexpr (Lds::NBUF == 1) {
         // one place for B and C: the next chunk's come when this one's are read
