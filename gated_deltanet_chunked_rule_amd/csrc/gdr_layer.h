@@ -64,7 +64,7 @@ struct SsmParams {
 struct NormParams {
   long rows;
   int inner, dim;
-  float eps;
+  float eps, inv_dim;            // inv_dim = 1 / dim
   const void *x, *residual, *gate, *weight;
   long xo, xi, ro, ri, go, gi;   // outer and inner strides of x, residual, gate
   void *y, *h_out;

@@ -142,7 +142,7 @@ void row_stride(const gdr_norm_shape* sh, const gdr_row_stride& s, long& outer, 
 }
 gdr::NormParams norm_params(const gdr_norm_shape* sh) {
   gdr::NormParams p = {};
-  p.rows = sh->rows; p.inner = sh->inner; p.dim = sh->dim; p.eps = sh->eps;
+  p.rows = sh->rows; p.inner = sh->inner; p.dim = sh->dim; p.eps = sh->eps; p.inv_dim = 1.f / (float)sh->dim;
   row_stride(sh, sh->x_stride, p.xo, p.xi);
   row_stride(sh, sh->residual_stride, p.ro, p.ri);
   row_stride(sh, sh->gate_stride, p.go, p.gi);

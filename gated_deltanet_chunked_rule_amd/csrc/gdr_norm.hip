@@ -43,6 +43,34 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2]) {
   }
 }
 
+// A double from another lane of the row of 16 by a DPP control.
+template <int C>
+__device__ __forceinline__ double dpp_d(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, C, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), C, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Sum over the TPR lanes of a row in 64 bits, as row_sum2.
+template <int TPR>
+__device__ __forceinline__ double row_sum_d(double a, double* lds) {
+  a += dpp_d<0xB1>(a);
+  a += dpp_d<0x4E>(a);
+  a += dpp_d<0x141>(a);
+  a += dpp_d<0x140>(a);
+#pragma unroll
+  for (int m = 16; m < (TPR < 64 ? TPR : 64); m <<= 1) a += __shfl_xor(a, m);
+  if constexpr (TPR > 64) {
+    if (lane_id() == 0) lds[threadIdx.x >> 6] = a;
+    __syncthreads();
+    const int first = (threadIdx.x / TPR) * (TPR / 64);
+    a = 0.0;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) a += lds[first + i];
+  }
+  return a;
+}
+
 __device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
 #define GDR_MAX_STEP(C) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, C, 0xF, 0xF, true))
   GDR_MAX_STEP(0xB1);
@@ -66,6 +94,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
   static_assert(R == 1 || TPR <= 64, "rows of several waves meet in LDS, one at a time");
   __shared__ float red[NT / 64][2];
+  __shared__ double red_d[QUANT && TPR > 64 ? NT / 64 : 1];
   const int t = threadIdx.x & (TPR - 1);
   typename VecIO<T, 8>::raw raw_r[R][NV], rawr_r[R][NV], rawg_r[R][NV];
   float w[NV][8];
@@ -95,6 +124,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
     const auto& rawr = rawr_r[k];
     const auto& rawg = rawg_r[k];
     const bool res = p.residual != nullptr, gate = p.gate != nullptr;
+    // x + residual in 64 bits
+    auto wide = [&](int v, double (&out)[8]) __attribute__((always_inline)) {
+      float f[8], g[8];
+      VecIO<T, 8>::up(raw[v], f);
+      if (res) VecIO<T, 8>::up(rawr[v], g);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        // (the asm keeps the values from being made once and held for all uses)
+        if (QUANT) asm volatile("" : "+v"(f[c]));
+        out[c] = res ? (double)f[c] + (double)g[c] : (double)f[c];
+      }
+    };
     float h[NV][8], ss = 0.f, unused = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -108,8 +149,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
 #pragma unroll
       for (int c = 0; c < 8; ++c) ss = fmaf(h[v][c], h[v][c], ss);
     }
-    row_sum2<TPR>(ss, unused, red);
-    const float r = 1.f / sqrtf(ss / (float)p.dim + p.eps);
+    // to 8 bits, rows of several waves are summed in 64 bits, for the borders
+    // below; others are then where a value lies next to one
+    double ssd = 0.0;
+    if constexpr (QUANT && TPR > 64) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        double hd[8];
+        wide(v, hd);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ssd = fma(hd[c], hd[c], ssd);
+      }
+      ssd = row_sum_d<TPR>(ssd, red_d);
+      ss = (float)ssd;
+    } else {
+      row_sum2<TPR>(ss, unused, red);
+    }
+    const float r = __builtin_amdgcn_rsqf(fmaf(ss, p.inv_dim, p.eps));   // an ulp
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
@@ -131,26 +187,65 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
         for (int c = 0; c < 8; ++c) m = max(m, c < nd ? (__builtin_bit_cast(uint32_t, y[c]) & 0x7fffffffu) : 0u);
         m = max16_u32(m);
         m = max(m, __builtin_bit_cast(uint32_t, kQuantTiny));
-        const float scale = __builtin_bit_cast(float, m) / kE4M3Max;
-        if (nd <= 0 || !live) continue;
-        // y times the reciprocal of the scale (an ulp and a half off y / scale; a
-        // true division made heads of 128 bound by its instructions: 50 us where
-        // this takes 39 for 262144 of them), clamped so that the largest
-        // value cannot pass 448 (fminf and fmaxf would drop a NaN, these compares
-        // keep it)
-        const float inv = __builtin_amdgcn_rcpf(scale);
-        int q[2] = {0, 0};
-        float f[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          f[c] = y[c] * inv;
-          f[c] = f[c] > kE4M3Max ? kE4M3Max : f[c] < -kE4M3Max ? -kE4M3Max : f[c];
-        }
+        float scale = __builtin_bit_cast(float, m) * (1.f / kE4M3Max);
+        // y / scale rounded to e4m3.  A value within 2^-20 of itself of a border
+        // between two of them may be on either side by fp32's own roundings:
+        // where both ends of that range round to the same value (no compare and
+        // no clamp is needed: 448 (1 + 2^-20) still rounds to 448), it is
+        // right; else the wave takes its groups again in 64 bits (one wave in
+        // about 60).
+        const float inv = __builtin_amdgcn_rcpf(scale), inv0 = inv * (1.f - 0x1p-20f), inv1 = inv * (1.f + 0x1p-20f);
+        int q[2] = {0, 0}, q1[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);
-          q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], q[i], true);
+          q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * inv0, y[4 * i + 1] * inv0, q[i], false);
+          q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * inv0, y[4 * i + 3] * inv0, q[i], true);
+          q1[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * inv1, y[4 * i + 1] * inv1, q1[i], false);
+          q1[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * inv1, y[4 * i + 3] * inv1, q1[i], true);
         }
+        if (__builtin_amdgcn_ballot_w64(q[0] != q1[0] || q[1] != q1[1]) != 0) {
+          double sd = ssd;
+          if constexpr (TPR <= 64) {
+            sd = 0.0;
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+              double hd[8];
+              wide(u, hd);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) sd = fma(hd[c], hd[c], sd);
+            }
+            sd = row_sum_d<TPR>(sd, nullptr);
+          }
+          const double rd = 1.0 / sqrt(sd / (double)p.dim + (double)p.eps);
+          float z[8];
+          if (gate) VecIO<T, 8>::up(rawg[v], z);
+          double yd[8], md = kQuantTiny;
+          wide(v, yd);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            yd[c] = yd[c] * rd * (double)w[v][c];
+            if (gate) yd[c] *= (double)z[c] / (1.0 + exp(-(double)z[c]));
+            // compares that a NaN wins
+            const double ad = fabs(yd[c]);
+            if (c < nd) md = ad <= md ? md : ad;
+          }
+#define GDR_MAX_STEP(C) do { const double o = dpp_d<C>(md); md = o <= md || md != md ? md : o; } while (0)
+          GDR_MAX_STEP(0xB1);
+          GDR_MAX_STEP(0x4E);
+          GDR_MAX_STEP(0x141);
+          GDR_MAX_STEP(0x140);
+#undef GDR_MAX_STEP
+          scale = (float)(md / (double)kE4M3Max);
+          float f[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] = (float)(yd[c] / (double)scale);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);
+            q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], q[i], true);
+          }
+        }
+        if (nd <= 0 || !live) continue;
         uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.dim + d;
         if (nd == 8) {
           *reinterpret_cast<u32x2_u1*>(out) = u32x2_u1{(uint32_t)q[0], (uint32_t)q[1]};
@@ -187,7 +282,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
 #pragma unroll
     for (int c = 0; c < 8; ++c) dw[v][c] = 0.f;
   }
-  const float inv = 1.f / (float)p.dim;
+  const float inv = p.inv_dim;
   const bool gate = p.gate != nullptr, dres = p.dres != nullptr;
   raw_t hn[NV], gn[NV], zn[NV], sn[NV];   // the next step's row, on its way
   auto fetch = [&](long row) {
@@ -244,7 +339,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
     }
     if (AHEAD && base + step < p.rows) fetch(row + step);
     row_sum2<TPR>(ss, su, red[buf]);   // two buffers: the next step's sums do not meet this step's readers
-    const float r = 1.f / sqrtf(ss * inv + p.eps);
+    const float r = __builtin_amdgcn_rsqf(fmaf(ss, inv, p.eps));   // an ulp
     const float m = su * r * inv;      // mean(u n)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -339,10 +434,12 @@ static void norm_fwd_launch(const NormParams& p, hipStream_t st) {
   hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, R, QUANT>), dim3((unsigned)((p.rows + per - 1) / per)), dim3(NT), 0, st, p);
 }
 // Two rows a lane group where that still leaves eight workgroups a compute unit
-// (262144 heads of 128 with gate, to 8 bits: 39 us; one row 40.5, four 41.5).
+// (262144 rows, bf16: 128 values with a gate 34.8 us, with one row 36.1; 64
+// values without 18.8, with one 20.7).  To 8 bits both take the same, as the
+// second look at values next to a border takes the registers: one row.
 template <typename T, int TPR, int NV, bool QUANT>
 static void norm_fwd_rows(const NormParams& p, hipStream_t st) {
-  if constexpr (TPR <= 64) {
+  if constexpr (TPR <= 64 && !QUANT) {
     if (p.rows >= 2L * (256 / TPR) * 8 * kComputeUnits) return norm_fwd_launch<T, TPR, NV, 2, QUANT>(p, st);
   }
   norm_fwd_launch<T, TPR, NV, 1, QUANT>(p, st);
