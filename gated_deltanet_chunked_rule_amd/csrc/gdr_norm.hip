@@ -51,6 +51,8 @@ __device__ __forceinline__ double dpp_d(double x) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), C, 0xF, 0xF, true);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+// The larger one; a NaN is above everything.
+__device__ __forceinline__ double max_nan(double a, double b) { return b <= a || a != a ? a : b; }
 // Sum over the TPR lanes of a row in 64 bits, as row_sum2.
 template <int TPR>
 __device__ __forceinline__ double row_sum_d(double a, double* lds) {
@@ -225,16 +227,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
           for (int c = 0; c < 8; ++c) {
             yd[c] = yd[c] * rd * (double)w[v][c];
             if (gate) yd[c] *= (double)z[c] / (1.0 + exp(-(double)z[c]));
-            // compares that a NaN wins
             const double ad = fabs(yd[c]);
-            if (c < nd) md = ad <= md ? md : ad;
+            if (c < nd) md = max_nan(md, ad);
           }
-#define GDR_MAX_STEP(C) do { const double o = dpp_d<C>(md); md = o <= md || md != md ? md : o; } while (0)
-          GDR_MAX_STEP(0xB1);
-          GDR_MAX_STEP(0x4E);
-          GDR_MAX_STEP(0x141);
-          GDR_MAX_STEP(0x140);
-#undef GDR_MAX_STEP
+          md = max_nan(md, dpp_d<0xB1>(md));
+          md = max_nan(md, dpp_d<0x4E>(md));
+          md = max_nan(md, dpp_d<0x141>(md));
+          md = max_nan(md, dpp_d<0x140>(md));
           scale = (float)(md / (double)kE4M3Max);
           float f[8];
 #pragma unroll

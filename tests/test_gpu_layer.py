@@ -592,3 +592,37 @@ def test_timing_hooks_name_the_kernels():
     gdr.timing.enable(False)
     gdr.timing.reset()
     assert set(got) == {"norm_bwd", "norm_dw"}
+
+
+def test_norm_to_8_bits_at_borders_beside_what_is_not_finite():
+    # 17 lies between 16 and 18 where the largest value is 448: such rows are looked at again in 64 bits, with the other
+    # rows of their wave, among them one with an infinity (whose scale is NaN) and one of zeros
+    x = torch.zeros(4, 128)
+    x[0, 3] = float("inf")
+    x[1, 5], x[1, 6], x[1, 7] = 448.0, 17.0, -19.0
+    x[2] = torch.linspace(-448, 448, 128)
+    w = torch.ones(128)
+    q, s, _ = gdr.gdr_rms_norm_fwd(cuda(x), cuda(w), quant=True)
+    assert s[0].isnan().all() and q[0].float().isnan().all()
+    y, _, _ = ref.norm(x, w)
+    want = torch.zeros(128, dtype=torch.float64)
+    unit = y[1, 5] / 448
+    check(s[1], unit[None], unit[None])
+    want[5], want[6], want[7] = 448, 16, -20              # ties go to the even value
+    assert torch.equal(q[1].cpu().double(), want)
+    assert not q[3].float().any()
+    rs, bound = ref.e4m3_parts(y[2:3])
+    assert bool(((q[2].cpu().double() * float(s[2, 0]) - y[2]).abs() <= bound[0]).all())
+
+
+def test_norm_to_8_bits_is_the_rounding_of_the_exact_value():
+    # 2^20 values: fp32 would put about ten of them on the wrong side of a border
+    g = gen(21)
+    x, w, z = randn(g, 2048, 4, 128, dtype=BF), (1 + randn(g, 128, std=0.2)).to(BF), randn(g, 2048, 4, 128, dtype=BF)
+    q, s, _ = gdr.gdr_rms_norm_fwd(cuda(x), cuda(w), None, cuda(z), quant=True)
+    y, _, _ = ref.norm(x, w, None, z)
+    v = y / (y.abs().amax(-1, keepdim=True) / 448).float().double()
+    unit = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    want = torch.round(v / unit) * unit
+    # a value whose 64-bit sum was added in another order may still differ where it ties to 2^-50
+    assert int((q.cpu().double() != want).sum()) <= 1
