@@ -229,6 +229,8 @@ const char* gdr_last_error(void);
  *   numbered b * T + t through one stride.
  * Alignment: tensors need the alignment of their elements only, except where
  *   16-byte rows are asked for (the scan and the steps).
+ * Overlap: outputs must not overlap inputs, or each other, except where an
+ *   entry point says so (states of the steps, residual_out).
  * Sequences: cu_seqlens is read on the device only; no host copy is needed
  *   and a captured graph may be replayed with other offsets.  It must be
  *   non-decreasing; offsets are clamped to [0, T], so that no value of it can

@@ -626,3 +626,95 @@ def test_norm_to_8_bits_is_the_rounding_of_the_exact_value():
     want = torch.round(v / unit) * unit
     # a value whose 64-bit sum was added in another order may still differ where it ties to 2^-50
     assert int((q.cpu().double() != want).sum()) <= 1
+
+
+def test_no_tokens():
+    w, b = cuda(randn(gen(30), 16, 4)), cuda(randn(gen(31), 16))
+    for x, cu, N in ((torch.empty(2, 0, 16), None, 2), (torch.empty(1, 0, 16), torch.zeros(4, dtype=torch.int32), 3)):
+        h0 = cuda(randn(gen(32), N, 3, 16))
+        y, ht = gdr.gdr_causal_conv_fwd(cuda(x), w, b, h0, cuda(cu), output_final_state=True)
+        assert y.shape == x.shape and torch.equal(ht, h0)
+        dht = cuda(randn(gen(33), N, 3, 16))
+        dx, dw, db, dh0 = gdr.gdr_causal_conv_bwd(cuda(x), w, b, cuda(x), h0, dht, cuda(cu))
+        assert dx.shape == x.shape and not dw.any() and not db.any() and torch.equal(dh0, dht)
+        c = ref.scan_inputs(gen(34), x.shape[0], 0, 4, 2, 32, 64, F32, seqs=N)
+        y, ht = run_scan(c, cu)
+        assert y.shape == (x.shape[0], 0, 4, 32) and torch.equal(ht.cpu(), c["h0"])
+    state = torch.zeros(2, 3, 16, device="cuda")
+    assert gdr.gdr_causal_conv_step(torch.empty(0, 16, device="cuda"), state, w).shape == (0, 16)
+
+
+def test_differentiable_calls_with_their_defaults():
+    g = gen(35)
+    x, w = cuda(randn(g, 2, 9, 16)).requires_grad_(True), cuda(randn(g, 16, 3)).requires_grad_(True)
+    y, ht = gdr.causal_conv(x, w)
+    assert ht is None
+    dy = randn(g, 2, 9, 16)
+    want = ref.conv_bwd(x, w, None, dy)
+    for t, r in zip(torch.autograd.grad(y, (x, w), cuda(dy)), want):
+        check(t, *r)
+    n = cuda(randn(g, 16)).requires_grad_(True)
+    y, h = gdr.rms_norm(x, n)
+    assert h is None
+    want = ref.norm_bwd(x, n, dy)
+    for t, r in zip(torch.autograd.grad(y, (x, n), cuda(dy)), want):
+        check(t, *r)
+
+
+def test_offsets_beyond_32_bits():
+    # the last rows of tensors of over 2^31 elements, against calls on those rows alone
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF)  # noqa: E731
+    T, D = 270000, 8192
+    x, w = rnd(1, T, D), rnd(D, 4)
+    y, _ = gdr.gdr_causal_conv_fwd(x, w)
+    assert torch.equal(y[:, -50:], gdr.gdr_causal_conv_fwd(x[:, -53:].contiguous(), w)[0][:, 3:])
+    dx, _, _, _ = gdr.gdr_causal_conv_bwd(x, w, None, y)
+    assert torch.equal(dx[:, -50:], gdr.gdr_causal_conv_bwd(x[:, -53:].contiguous(), w, None, y[:, -53:].contiguous())[0][:, 3:])
+    del dx
+    rows = x.view(-1, 4096)
+    n = rnd(4096)
+    assert torch.equal(gdr.gdr_rms_norm_fwd(rows, n)[0][-3:], gdr.gdr_rms_norm_fwd(rows[-3:].contiguous(), n)[0])
+    assert torch.equal(gdr.gdr_rms_norm_bwd(rows, n, y.view(-1, 4096))[0][-3:],
+                       gdr.gdr_rms_norm_bwd(rows[-3:].contiguous(), n, y.view(-1, 4096)[-3:].contiguous())[0])
+    del y
+    H, P, N = 64, 128, 32
+    xs, dt, A = x.view(1, T, H, P), rnd(1, T, H), -torch.rand(H, generator=g, device="cuda")
+    B, C = rnd(1, T, 1, N), rnd(1, T, 1, N)
+    cut = T - 70
+    y, last = gdr.gdr_ssm_scan_fwd(xs, dt, A, B, C, output_final_state=True)
+    _, mid = gdr.gdr_ssm_scan_fwd(xs[:, :cut], dt[:, :cut], A, B[:, :cut], C[:, :cut], output_final_state=True)
+    ye, end = gdr.gdr_ssm_scan_fwd(xs[:, cut:].contiguous(), dt[:, cut:], A, B[:, cut:].contiguous(), C[:, cut:].contiguous(),
+                                   initial_state=mid, output_final_state=True)
+    # the chunks fall elsewhere: bf16 roundings of the operands, and fp32 sums in another order
+    assert float((y[:, cut:].float() - ye.float()).norm() / ye.float().norm()) <= 2.0 ** -7
+    assert float((last - end).norm() / end.norm()) <= 1e-5
+
+
+def test_in_place_residual_through_the_c_entry():
+    from gated_deltanet_chunked_rule_amd import layer
+    g = gen(36)
+    x, r, w = cuda(randn(g, 40, 4100, dtype=BF)), cuda(randn(g, 40, 4100, dtype=BF)), cuda(randn(g, 4100, dtype=BF))
+    y, _, h = gdr.gdr_rms_norm_fwd(x, w, r)
+    out = torch.empty_like(x)
+    sh = layer._NormShape(40, 1, 4100, 0, 1e-6, 0, 0, 0, 0, 0, 0, 0)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert layer._entry("gdr_rms_norm_fwd")(sh, x.data_ptr(), r.data_ptr(), None, w.data_ptr(), out.data_ptr(), None, r.data_ptr(), stream) == 0
+    assert torch.equal(out, y) and torch.equal(r, h)
+
+
+def test_two_streams_at_once():
+    # calls on two streams, each with workspaces of its own, against the same calls one after another
+    c = [ref.scan_inputs(gen(40 + i), 1, 3000, 16, 2, 64, 128, BF) for i in range(2)]
+    k = [dict(x=cuda(randn(gen(50 + i), 2, 3000, 512, dtype=BF)), w=cuda(randn(gen(60 + i), 512, 4, dtype=BF))) for i in range(2)]
+    want = [[*run_scan(c[i]), *gdr.gdr_causal_conv_bwd(k[i]["x"], k[i]["w"], None, k[i]["x"])[:2]] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for r in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = [*run_scan(c[i]), *gdr.gdr_causal_conv_bwd(k[i]["x"], k[i]["w"], None, k[i]["x"])[:2]]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
