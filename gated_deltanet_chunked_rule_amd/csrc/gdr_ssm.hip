@@ -220,6 +220,7 @@ struct SsmLds {
   float gam[3][SHEADS][SC], wt[3][SHEADS][SC];
   float d[2][OUT ? SHEADS : 1][OUT ? SC : 1], ut[2][OUT ? SHEADS : 1][OUT ? SC : 1];
   float rem[3][REM ? SHEADS : 1][REM ? SC : 1];
+  float skip[SHEADS];   // D
   int32_t cu[SCU];
   // the tiles last: what stands before them is in reach of an LDS access's
   // offset field, and needs no address registers of its own
@@ -309,6 +310,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
     }
   }
 
+  if (OUT && (int)threadIdx.x < heads) lds.skip[threadIdx.x] = p.D ? p.D[head0 + threadIdx.x] : 0.f;   // read behind the next barrier
+
   const int seg0 = seg * p.seg, seg1 = min(seg0 + p.seg, p.s.Ttot);
   float total_gam = 0.f;
   const Reader<T, NB, NX> rd(w);
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
   };
   // One run of tokens [t0, t1) of a sequence, from the state in h.
   auto run = [&](int t0, int t1) __attribute__((always_inline)) {
-    float rdt = 0.f;
+    uint32_t rdt = 0;
     auto copy_b = [&](int t, int buf) __attribute__((always_inline)) {
       cb.issue(lds.b[buf], Bp + (long)t * p.b_stride, p.b_stride, min(SC, t1 - t), ND);
     };
@@ -346,12 +349,12 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
     auto load_dt = [&](int t) __attribute__((always_inline)) {   // tokens behind the run read as zero
       if (!gater || t >= t1) return;
       const rsrc_t r = make_rsrc_u(dt + (long)t * p.dt_stride + ghead, ((long)(min(SC, t1 - t) - 1) * p.dt_stride + 1) * (long)sizeof(T));
-      if constexpr (F32) rdt = buf_load_f32(r, dt_off);
-      else rdt = __builtin_bit_cast(float, (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, dt_off, 0, 0) << 16);
+      if constexpr (F32) rdt = __builtin_amdgcn_raw_buffer_load_b32(r, dt_off, 0, 0);
+      else rdt = __builtin_amdgcn_raw_buffer_load_b16(r, dt_off, 0, 0);   // widened where it is used: here it would be waited for
     };
     // the gates of the chunk at t, lane l its token l, from the dt loaded for it
     auto gates = [&](int t, int gb, int db) __attribute__((always_inline)) {
-      float d = rdt + bias;
+      float d = __builtin_bit_cast(float, F32 ? rdt : rdt << 16) + bias;
       if (p.softplus) d = softplus_f(d);
       if (t + l >= t1) d = 0.f;
       // gam in 64 bits: a difference of two far sums keeps fp32's accuracy
@@ -368,7 +371,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
     // Scores, transposed: tile (jt, it) holds B_j . C_i, rows j, columns i, with
     // each head's decays.  Tiles left of the diagonal take e^{gam_i - gam_j} as
     // two factors at the end of tile jt, both at most 1: one exponential for
-    // four values.  All SHEADS rows are made, unused ones from what LDS holds.
+    // four values.
     auto scores = [&](int buf, int gb, int db) __attribute__((always_inline)) {
       const T* tb = lds.b[buf];
       const T* tc = lds.c[OUT ? buf : 0];
@@ -397,7 +400,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
               rj = *reinterpret_cast<const f32x4*>(&lds.rem[gb][k][16 * jt + 4 * q]);
               ri = lds.rem[gb][k][16 * it + c];
             }
-            const float skip = p.D ? p.D[head0 + k] : 0.f;
+            const float skip = lds.skip[k];
             f32x4 pm;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -445,6 +448,9 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       if (Lds::STAGE && t > t0) __builtin_amdgcn_s_waitcnt(0x0F72);
       else __builtin_amdgcn_s_waitcnt(0x0F70);
       lds_barrier();   // everyone's have, and the scores are there
+      // dt for the gates of the next but one has landed too: taken here, before
+      // further copies, as the wait for it would be one for them
+      asm volatile("" : "+v"(rdt));
       if (Lds::NBUF == 2 && more) {
         copy_b(t + SC, buf1);
         if constexpr (!OUT) copy_x(t + SC, buf1);
