@@ -458,6 +458,42 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       frag xf[2];   // x^T: this wave's columns, tokens 32 jb..
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb) xf[jb] = rd.down_x(lds.x[OUT ? 0 : buf][w / 8], jb);
+      // h' = e^{gam_n} h + B^T (w x), w_j = e^{gam_n - gam_j} d_j.  The fp32
+      // product w x is taken as three bf16 terms of 8 bits each, so that the
+      // state is as exact as fp32 operands would make it (one term would leave
+      // 2^-8, two 2^-16); B and x are bf16 as they are.  All but the products
+      // is done before the barrier, where the other waves' products leave the
+      // vector unit idle.
+      constexpr int TERMS = F32 ? 1 : 3;
+      frag wx[2][TERMS];
+      auto weigh = [&]() __attribute__((always_inline)) {
+        const float gend = lds.gam[gb][hd][SC - 1], en = exp_f(gend);
+        total_gam += gend;
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) h[kb][u] *= en;
+#pragma unroll
+        for (int jb = 0; jb < 2; ++jb) {
+          f32x4 u0 = *reinterpret_cast<const f32x4*>(&lds.wt[gb][hd][32 * jb + 4 * q]);
+          f32x4 u1 = *reinterpret_cast<const f32x4*>(&lds.wt[gb][hd][32 * jb + 16 + 4 * q]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            u0[e] *= K::get(xf[jb], e);
+            u1[e] *= K::get(xf[jb], 4 + e);
+          }
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            wx[jb][k] = K::acc(u0, u1);
+            if (k + 1 < TERMS)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                u0[e] -= K::get(wx[jb][k], e);
+                u1[e] -= K::get(wx[jb][k], 4 + e);
+              }
+          }
+        }
+      };
       if constexpr (OUT) {
         // y^T, rows = channels, columns = tokens: first e^{gam_i} h^T C_i
         const T* tc = lds.c[buf];
@@ -489,6 +525,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
             buf_store16(yr, y_off, __builtin_bit_cast(uint4, acc[it]));
           }
         }
+        weigh();
         __builtin_amdgcn_s_waitcnt(0x0F70);   // B of the next chunk has landed
         lds_barrier();                        // second phase
         if (more) copy_x(t + SC, 0);
@@ -498,39 +535,11 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       if (gater && t + 2 * SC < t1) gates(t + 2 * SC, next(next(gb)), db);
       if (t + 3 * SC < t1) load_dt(t + 3 * SC);
 
-      // h' = e^{gam_n} h + B^T (w x), w_j = e^{gam_n - gam_j} d_j.  The fp32
-      // product w x is taken as three bf16 terms of 8 bits each, so that the
-      // state is as exact as fp32 operands would make it (one term would leave
-      // 2^-8, two 2^-16); B and x are bf16 as they are.
+      if constexpr (!OUT) weigh();
       const T* tb = lds.b[buf];
-      const float gend = lds.gam[gb][hd][SC - 1], en = exp_f(gend);
-      total_gam += gend;
-#pragma unroll
-      for (int kb = 0; kb < NK; ++kb)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) h[kb][u] *= en;
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb) {
         if (32 * jb >= len) break;
-        f32x4 u0 = *reinterpret_cast<const f32x4*>(&lds.wt[gb][hd][32 * jb + 4 * q]);
-        f32x4 u1 = *reinterpret_cast<const f32x4*>(&lds.wt[gb][hd][32 * jb + 16 + 4 * q]);
-        constexpr int TERMS = F32 ? 1 : 3;
-        frag wx[TERMS];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          u0[e] *= K::get(xf[jb], e);
-          u1[e] *= K::get(xf[jb], 4 + e);
-        }
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-          wx[k] = K::acc(u0, u1);
-          if (k + 1 < TERMS)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              u0[e] -= K::get(wx[k], e);
-              u1[e] -= K::get(wx[k], 4 + e);
-            }
-        }
         // two blocks at a time, term by term over their four tiles, so that no
         // product waits for the one before
 #pragma unroll
@@ -546,7 +555,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
 #pragma unroll
             for (int i = 0; i < KB; ++i)
 #pragma unroll
-              for (int u = 0; u < 2; ++u) h[kb + i][u] = K::mma(bf[i][u], wx[k], h[kb + i][u]);
+              for (int u = 0; u < 2; ++u) h[kb + i][u] = K::mma(bf[i][u], wx[jb][k], h[kb + i][u]);
           }
       }
       if constexpr (Lds::STAGE) {
