@@ -355,7 +355,7 @@ static int tile_for(long groups, int tokens, long threads, int lo, int hi) {
   while (tile > lo && groups * ((tokens + tile - 1) / tile) < threads) tile /= 2;
   return tile;
 }
-int conv_bwd_tile(int tokens, int D) { return tile_for((D + 3) / 4, tokens, 1L << 18, 16, 256); }
+int conv_bwd_tile(int tokens, int D) { return tile_for((D + 3) / 4, tokens, 1L << 19, 16, 256); }
 
 template <typename T, int W>
 static hipError_t conv_fwd(ConvParams p, hipStream_t st) {

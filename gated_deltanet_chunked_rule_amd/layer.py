@@ -190,10 +190,8 @@ def _offsets(cu_seqlens, B, T, dev):
 _grad_enabled = torch._C.is_grad_enabled if hasattr(torch._C, "is_grad_enabled") else torch.is_grad_enabled
 
 
-def _inference(name, *tensors):
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            raise GdrError(f"{name} offers no gradient: call it under torch.no_grad(), or detach its inputs")
+def _no_gradient(name):
+    raise GdrError(f"{name} offers no gradient: call it under torch.no_grad(), or detach its inputs")
 
 
 def _ptr(t):
@@ -204,7 +202,9 @@ def _pool(state, name, tail, dtype, index, rows, slots):
     if state.dim() != 1 + len(tail):
         raise GdrError(f"shape mismatch: {name} is {tuple(state.shape)}, expected (slots, {', '.join(map(str, tail))})")
     n = state.shape[0]
-    ptr = _dense(state, name, (n, *tail), dtype, index)
+    if state.shape[1:] != tail or state.dtype is not dtype or state.get_device() != index or index < 0 or not state.is_contiguous():
+        _refuse(state, name, (n, *tail), dtype, index)
+    ptr = state.data_ptr()
     if n < 1 or (slots is None and n < rows):
         raise GdrError(f"{name} holds {n} slots for {rows} rows")
     return ptr, n, _dense(slots, "slots", (rows,), torch.int32, index)
@@ -269,8 +269,9 @@ def gdr_causal_conv_step(x, state, weight, bias=None, *, slots=None, activation=
     """One new token per row: x [rows, D] (strided), state [slots, W - 1, D] moves on in place.  Returns y [rows, D]."""
     if x.dim() != 2 or weight.dim() != 2:
         raise GdrError("x must be [rows, D] and weight [D, W]")
-    if _grad_enabled():
-        _inference("gdr_causal_conv_step", x, state, weight, bias)
+    if _grad_enabled() and (x.requires_grad or state.requires_grad or weight.requires_grad
+                            or (bias is not None and bias.requires_grad)):
+        _no_gradient("gdr_causal_conv_step")
     rows, D = x.shape
     W = weight.shape[1]
     act, code, dev, ty = _activation(activation), _code(x), x.get_device(), x.dtype
@@ -278,7 +279,7 @@ def gdr_causal_conv_step(x, state, weight, bias=None, *, slots=None, activation=
     wp = _dense(weight, "weight", (D, W), ty, dev)
     bp = _dense(bias, "bias", (D,), ty, dev)
     sp, n, lp = _pool(state, "state", (W - 1, D), ty, dev, rows, slots)
-    y = torch.empty(rows, D, device=dev, dtype=ty)
+    y = torch.empty(rows, D, device=dev, dtype=ty) if xs else torch.empty_like(x)
     if rows:
         _call(dev, _entry("gdr_causal_conv_step"), _ConvShape(rows, 1, D, W, 0, code, act, xs), xp, wp, bp, sp, n, lp, y.data_ptr())
     return y
@@ -318,8 +319,9 @@ def gdr_step(q, k, v, g, beta, state, scale=None, *, slots=None):
     fp32, state [slots, Hv, K, V] fp32, in place.  Returns o [rows, Hv, V]."""
     if q.dim() != 3 or v.dim() != 3:
         raise GdrError("q and v must be 3-D: [rows, Hq, K] and [rows, Hv, V]")
-    if _grad_enabled():
-        _inference("gdr_step", q, k, v, g, beta, state)
+    if _grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
+                            or beta.requires_grad or state.requires_grad):
+        _no_gradient("gdr_step")
     rows, Hq, K = q.shape
     Hv, V = v.shape[1], v.shape[2]
     code, dev, dt = _code(q), q.get_device(), q.dtype
@@ -329,7 +331,7 @@ def gdr_step(q, k, v, g, beta, state, scale=None, *, slots=None):
     gp = _dense(g, "g", (rows, Hv), torch.float32, dev)
     bp = _dense(beta, "beta", (rows, Hv), torch.float32, dev)
     sp, n, lp = _pool(state, "state", (Hv, K, V), torch.float32, dev, rows, slots)
-    o = torch.empty(rows, Hv, V, device=dev, dtype=dt)
+    o = torch.empty(rows, Hv, V, device=dev, dtype=dt) if vs else torch.empty_like(v)
     if rows:
         _call(dev, _entry("gdr_step"), _Shape(rows, 1, Hq, Hv, K, V, 0, code), qp, qs, kp, ks, vp, vs, gp, bp,
               K ** -0.5 if scale is None else float(scale), sp, n, lp, o.data_ptr())
@@ -343,8 +345,8 @@ def gdr_ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, c
     [H] fp32; initial_state [N_seqs, H, N, P] fp32.  Returns (y, final_state or None).  No gradient."""
     if x.dim() != 4 or B.dim() != 4:
         raise GdrError("x and B must be 4-D: [batch, T, H, P] and [batch, T, G, N]")
-    if _grad_enabled():
-        _inference("gdr_ssm_scan_fwd", x, dt, A, B, C, D, dt_bias, initial_state)
+    if _grad_enabled() and any(t is not None and t.requires_grad for t in (x, dt, A, B, C, D, dt_bias, initial_state)):
+        _no_gradient("gdr_ssm_scan_fwd")
     b, T, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
     code, dev, ty = _code(x), x.get_device(), x.dtype
@@ -371,8 +373,8 @@ def gdr_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None, dt_
     [slots, H, N, P] fp32, in place.  Returns y [rows, H, P]."""
     if x.dim() != 3 or B.dim() != 3:
         raise GdrError("x and B must be 3-D: [rows, H, P] and [rows, G, N]")
-    if _grad_enabled():
-        _inference("gdr_ssm_step", x, dt, A, B, C, state, D, dt_bias)
+    if _grad_enabled() and any(t is not None and t.requires_grad for t in (x, dt, A, B, C, state, D, dt_bias)):
+        _no_gradient("gdr_ssm_step")
     rows, H, P = x.shape
     G, N = B.shape[1], B.shape[2]
     code, dev, ty = _code(x), x.get_device(), x.dtype
@@ -384,7 +386,7 @@ def gdr_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None, dt_
     Dp = _dense(D, "D", (H,), torch.float32, dev)
     ip = _dense(dt_bias, "dt_bias", (H,), torch.float32, dev)
     sp, n, lp = _pool(state, "state", (H, N, P), torch.float32, dev, rows, slots)
-    y = torch.empty(rows, H, P, device=dev, dtype=ty)
+    y = torch.empty(rows, H, P, device=dev, dtype=ty) if xs else torch.empty_like(x)
     if rows:
         _call(dev, _entry("gdr_ssm_step"), _SsmShape(rows, 1, H, G, P, N, 0, code, 1 if dt_softplus else 0, xs, ds, bs, cs),
               xp, dp, Ap, Bp, Cp, Dp, ip, sp, n, lp, y.data_ptr())
