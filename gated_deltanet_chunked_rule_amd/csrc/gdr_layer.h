@@ -89,8 +89,8 @@ int norm_bwd_blocks(long rows, int dim);
 
 // ------------------------------------------------------------- device part --
 // VEC consecutive elements that need the alignment of one element only:
-// global accesses of 8 and 16 bytes work at any element address on gfx950
-// (measured no slower on aligned rows), so odd row lengths take the same path.
+// global accesses of 8 and 16 bytes work at any element address on gfx950, so
+// odd row lengths take the same path.
 typedef uint32_t u32x4_u2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_u2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_u4 __attribute__((ext_vector_type(4), aligned(4)));

