@@ -70,6 +70,15 @@ template <> struct Blk<bf16> {
     const uint32_t v = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
     return __builtin_bit_cast(float, e & 1 ? v & 0xffff0000u : v << 16);
   }
+  // NaN if a value is not finite (0 * it), else 0
+  static __device__ __forceinline__ float unsound(const frag& f, float sum) {
+    const uint4 u = __builtin_bit_cast(uint4, f);
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v[i]), __builtin_bit_cast(bf16x2, 0u), sum, false);
+    return sum;
+  }
+  static __device__ __forceinline__ void set(frag& f, int e, float v) { f[e] = (bf16)v; }
 };
 template <> struct Blk<float> {
   struct frag { float v[8]; };
@@ -85,6 +94,12 @@ template <> struct Blk<float> {
     return frag{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
   }
   static __device__ __forceinline__ float get(const frag& f, int e) { return f.v[e]; }
+  static __device__ __forceinline__ float unsound(const frag& f, float sum) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(f.v[e], 0.f, sum);
+    return sum;
+  }
+  static __device__ __forceinline__ void set(frag& f, int e, float v) { f.v[e] = v; }
 };
 
 // Operand reads from staged tiles.  A lane's byte address is its row's start
@@ -495,6 +510,38 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         }
       };
       if constexpr (OUT) {
+        // A value of x that is not finite would reach the tokens before it too,
+        // through the zeros above the diagonal: such a channel is NaN from the
+        // token on (bit 4 it + e of nan_at), and the product takes a zero for it.
+        const bool unsound = __builtin_amdgcn_ballot_w64(!(K::unsound(xf[1], K::unsound(xf[0], 0.f)) == 0.f)) != 0;
+        uint32_t nan_at = 0;
+        if (__builtin_expect(unsound, 0)) {
+          int behind = 4 * q - c;
+          asm volatile("" : "+v"(behind));   // nothing of this is kept over the chunk loop
+#pragma unroll
+          for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) K::set(xf[jb], e, K::get(xf[jb], e) * 0.f == 0.f ? 0.f : 1.f);
+#pragma unroll 1
+          for (int it = 3; it >= 0; --it) {
+            f32x4 count = zero4();   // of them up to token i
+#pragma unroll
+            for (int jb = 0; jb < 2; ++jb) {
+              frag upto;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) K::set(upto, e, behind + 32 * jb + 16 * (e / 4) + e % 4 <= 16 * it ? 1.f : 0.f);
+              count = K::mma(xf[jb], upto, count);
+            }
+#pragma unroll
+            for (int e = 3; e >= 0; --e) nan_at = nan_at << 1 | (count[e] > 0.f);
+          }
+#pragma unroll
+          for (int jb = 0; jb < 2; ++jb) {
+            xf[jb] = rd.down_x(lds.x[0][w / 8], jb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) K::set(xf[jb], e, K::get(xf[jb], e) * 0.f == 0.f ? K::get(xf[jb], e) : 0.f);
+          }
+        }
         // y^T, rows = channels, columns = tokens: first e^{gam_i} h^T C_i
         const T* tc = lds.c[buf];
         f32x4 acc[4];
@@ -508,6 +555,12 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         }
 #pragma unroll
         for (int it = 0; it < 4; ++it) acc[it] *= exp_f(lds.gam[gb][hd][16 * it + c]);
+        if (__builtin_expect(unsound, 0)) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[it][e] = nan_at >> (4 * it + e) & 1 ? __builtin_nanf("") : acc[it][e];
+        }
         // then the tokens of the chunk up to i
         const typename K::quad* sc = lds.score[hd] + l;
 #pragma unroll
@@ -525,6 +578,9 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
             buf_store16(yr, y_off, __builtin_bit_cast(uint4, acc[it]));
           }
         }
+        if (__builtin_expect(unsound, 0))
+#pragma unroll
+          for (int jb = 0; jb < 2; ++jb) xf[jb] = rd.down_x(lds.x[0][w / 8], jb);
         weigh();
         __builtin_amdgcn_s_waitcnt(0x0F70);   // B of the next chunk has landed
         lds_barrier();                        // second phase

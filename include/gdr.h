@@ -242,10 +242,9 @@ const char* gdr_last_error(void);
  *   slots[r] (slots NULL: slot r, rows <= num_slots), in place.  A row whose
  *   slot is outside [0, num_slots), or was named by an earlier row of the same
  *   call, is padding: its output row is zero and no state changes.
- * Non-finite inputs propagate as in the formulas; in the scan one may also
- *   reach the outputs of the same heads up to 63 tokens before it in its own
- *   sequence (the products of a chunk multiply it with the zeros above the
- *   diagonal).  It never reaches another sequence. */
+ * Non-finite inputs reach what the formulas let them reach and nothing else:
+ *   no earlier token, no other sequence, no other row.  In the scan an
+ *   infinity may come out as a NaN. */
 
 typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
 

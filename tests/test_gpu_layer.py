@@ -260,6 +260,41 @@ def test_scan_keeps_what_is_not_finite_to_its_sequence():
     assert torch.equal(ht[0], clean_h[0]) and torch.equal(ht[2], clean_h[2]) and ht[1].isnan().any()
 
 
+@pytest.mark.parametrize("what", ["x", "dt", "B", "C", "all"])
+@pytest.mark.parametrize("H,P,N,dtype", [(4, 64, 128, BF), (8, 32, 32, BF), (2, 64, 64, F32)])
+def test_scan_keeps_what_is_not_finite_from_earlier_tokens(H, P, N, dtype, what):
+    # a padded batch whose rows end anywhere in a chunk and hold anything behind that
+    c = ref.scan_inputs(gen(P + N), 4, 400, H, 1, P, N, dtype)
+    clean, _ = run_scan(c)
+    widths = {"x": slice(0, H * P), "B": slice(H * P, H * P + N), "C": slice(H * P + N, H * P + 2 * N), "all": slice(0, H * P + 2 * N)}
+    ends = (1, 77, 207, 399)
+    for b, end in enumerate(ends):
+        bad = float("nan") if b % 2 else float("-inf")
+        if what in widths:
+            c["row"][b, end:, widths[what]] = bad
+        if what in ("dt", "all"):
+            c["dt"][b, end:] = bad
+    y, _ = run_scan(c)
+    for b, end in enumerate(ends):
+        assert torch.equal(y[b, :end], clean[b, :end])
+        if what in ("x", "all"):
+            assert not torch.isfinite(y[b, end:]).any()
+
+
+def test_scan_keeps_what_is_not_finite_to_its_channel():
+    # one value of x: its channel's outputs from there on, its column of the state, and nothing else
+    c = ref.scan_inputs(gen(8), 1, 300, 8, 2, 64, 64, BF)
+    clean_y, clean_h = run_scan(c)
+    c["row"][0, 170, 3 * 64 + 37] = float("inf")
+    y, ht = run_scan(c)
+    assert not torch.isfinite(y[0, 170:, 3, 37]).any() and not torch.isfinite(ht[0, 3, :, 37]).any()
+    for got, want in ((y[0], clean_y[0]), (ht, clean_h)):
+        got, want = got.clone(), want.clone()
+        where = (slice(170, None), 3, 37) if got.dim() == 3 else (0, 3, slice(None), 37)
+        got[where] = want[where] = 0
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("rows,H,G,P,N,dtype", [(1, 1, 1, 32, 32, BF), (3, 4, 2, 64, 128, F32), (70, 6, 1, 128, 64, BF), (64, 8, 8, 64, 128, BF)])
 def test_ssm_step(rows, H, G, P, N, dtype):
     g = gen(rows + N)
