@@ -157,6 +157,9 @@ bool all_aligned(const void* const (&p)[M], size_t a) {
   return true;
 }
 
+// The overlap that comes about most easily: an output in an input's place.
+bool in_place(const void* out, const void* in) { return out != nullptr && out == in; }
+
 }  // namespace
 
 extern "C" {
@@ -168,6 +171,7 @@ gdr_status gdr_causal_conv_fwd(const gdr_conv_shape* shape, const void* x, const
   if (!weight || (shape->T > 0 && (!x || !y))) return invalid("x, weight and y must be non-NULL");
   const void* ptrs[] = {x, weight, bias, initial_state, y, final_state};
   if (!all_aligned(ptrs, esize(shape->dtype)) || !aligned(cu_seqlens, 4)) return invalid("device pointers must be aligned to their elements");
+  if (in_place(y, x) || in_place(final_state, initial_state)) return invalid("y and final_state must not overlap x and initial_state");
   gdr::ConvParams p = conv_params(shape, x, weight, bias, initial_state, cu_seqlens);
   p.y = y;
   p.ht = final_state;
@@ -187,6 +191,8 @@ gdr_status gdr_causal_conv_bwd(const gdr_conv_shape* shape, const void* x, const
   if (!weight || !dw || (shape->T > 0 && (!x || !dy || !dx))) return invalid("x, weight, dy, dx and dw must be non-NULL");
   const void* ptrs[] = {x, weight, bias, initial_state, dy, dht, dx, dw, db, dh0};
   if (!all_aligned(ptrs, esize(shape->dtype)) || !aligned(cu_seqlens, 4)) return invalid("device pointers must be aligned to their elements");
+  if (in_place(dx, x) || in_place(dx, dy) || in_place(dh0, initial_state) || in_place(dh0, dht))
+    return invalid("dx and dh0 must not overlap x, dy, initial_state and dht");
   if (!workspace || workspace_bytes < conv_bwd_bytes(shape))
     return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_causal_conv_bwd_workspace_size)");
   if (!aligned(workspace, 16)) return invalid("workspace must be 16-byte aligned");
@@ -258,6 +264,7 @@ gdr_status gdr_ssm_scan_fwd(const gdr_ssm_shape* shape, const void* x, const voi
   if (!all_aligned(wide, 16)) return invalid("x, B, C, y, the states and the workspace must be 16-byte aligned");
   const void* f32[] = {A, D, dt_bias, cu_seqlens};
   if (!all_aligned(f32, 4) || !aligned(dt, esize(shape->dtype))) return invalid("device pointers must be aligned to their elements");
+  if (in_place(y, x) || in_place(final_state, initial_state)) return invalid("y and final_state must not overlap x and initial_state");
   gdr::SsmParams p = ssm_params(shape, cu_seqlens);
   if (!workspace || workspace_bytes < ssm_bytes(p))
     return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_ssm_scan_fwd_workspace_size)");

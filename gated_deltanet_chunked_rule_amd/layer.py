@@ -20,6 +20,9 @@ non-decreasing; nothing is copied to the host, so the calls can be captured into
 a graph); on the host it is checked and copied.  Tokens that belong to no sequence
 get zero rows.  ``slots`` name each row's state in the pool: a row whose slot is out
 of range, or was named by an earlier row, is padding and gets a zero row.
+
+``causal_conv`` and ``rms_norm`` can be captured with their backward, as any
+differentiable call of torch: on leaves that no eager graph alive was built from.
 """
 from __future__ import annotations
 

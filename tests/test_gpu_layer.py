@@ -753,3 +753,41 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_captured_training_step_replays():
+    """Convolution and gated norm, forward and backward, captured into one graph and replayed on new inputs and offsets.  The
+    captured leaves are used by no eager graph: torch binds a leaf's gradient to the stream it was first needed on."""
+    def leaves(g):
+        return [cuda(t).requires_grad_(True) for t in (randn(g, 1, 600, 64, dtype=BF), randn(g, 64, 4, dtype=BF), randn(g, 64, dtype=BF),
+                                                       randn(g, 1, 600, 64, dtype=BF), randn(g, 64, dtype=BF), randn(g, 1, 600, 64, dtype=BF))]
+
+    def work(x, w, b, res, wn, z, cu, do, dh):
+        y, _ = gdr.causal_conv(x, w, b, cu_seqlens=cu)
+        o, h = gdr.rms_norm(y, wn, res, z)
+        return [o, h, *torch.autograd.grad((o, h), (x, w, b, res, wn, z), (do, dh))]
+
+    cu = torch.tensor([0, 100, 420, 600], dtype=torch.int32, device="cuda")
+    do, dh = cuda(randn(gen(21), 1, 600, 64, dtype=BF)), cuda(randn(gen(22), 1, 600, 64, dtype=BF))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work(*leaves(gen(20)), cu, do, dh)
+    torch.cuda.current_stream().wait_stream(side)
+    static = leaves(gen(20))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work(*static, cu, do, dh)
+    for r in range(4):
+        fresh = leaves(gen(70 + r))
+        with torch.no_grad():
+            for a, b in zip(static, fresh):
+                a.copy_(b)
+        do.copy_(randn(gen(80 + r), 1, 600, 64))
+        cu.copy_(torch.tensor([0, 1 + r, 300 + 70 * r, 600 - 13 * r]))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.detach().clone() for t in out]
+        want = work(*fresh, cu, do, dh)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), r

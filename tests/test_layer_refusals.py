@@ -182,3 +182,14 @@ def test_python_offsets_are_checked_on_the_host():
     raises("int32 or int64", layer._offsets, torch.tensor([0.0, 4.0]), 1, 4, dev)
     cu, n = layer._offsets([0, 2, 2, 4], 1, 4, dev)
     assert n == 3 and cu.dtype == torch.int32
+
+
+def test_outputs_in_an_inputs_place_are_refused():
+    p = [fake(i) for i in range(12)]
+    f, b, s = (layer._entry(n) for n in ("gdr_causal_conv_fwd", "gdr_causal_conv_bwd", "gdr_ssm_scan_fwd"))
+    assert f(conv_shape(), p[0], p[1], None, None, None, p[0], None, None) == -1 and "overlap" in last()
+    assert f(conv_shape(), p[0], p[1], None, p[2], None, p[3], p[2], None) == -1 and "overlap" in last()
+    for dx, dh0 in ((p[0], p[7]), (p[3], p[7]), (p[5], p[2]), (p[5], p[4])):
+        assert b(conv_shape(), p[0], p[1], None, p[2], None, p[3], p[4], dx, p[6], None, dh0, p[8], 1 << 30, None) == -1 and "overlap" in last()
+    assert s(ssm_shape(), p[0], p[1], p[2], p[3], p[4], None, None, None, None, p[0], None, p[6], 1 << 40, None) == -1 and "overlap" in last()
+    assert s(ssm_shape(), p[0], p[1], p[2], p[3], p[4], None, None, p[7], None, p[5], p[7], p[6], 1 << 40, None) == -1 and "overlap" in last()
