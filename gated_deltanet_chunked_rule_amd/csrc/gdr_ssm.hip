@@ -680,7 +680,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
 }
 
 // States at the segment ends, in place: end_s = b_s + e^{decay_s} end_{s-1}.
-// One thread walks four values over the segments, their loads eight ahead.
+// One thread walks four values over the segments, their loads sixteen ahead
+// (8192 tokens of 64 heads: 12.7 us, eight ahead 13.8).
 __global__ __launch_bounds__(256) void k_ssm_join(SsmParams p) {
   const long per = (long)p.H * p.N * p.P;
   const long i = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -688,17 +689,17 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmParams p) {
   const int head = (int)(i / ((long)p.N * p.P));
   const int n = p.segs - 1;
   f32x4 cur = zero4();
-  for (int s0 = 0; s0 < n; s0 += 8) {
-    f32x4 b[8];
-    float g[8];
+  for (int s0 = 0; s0 < n; s0 += 16) {
+    f32x4 b[16];
+    float g[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 16; ++k) {
       const int s = min(s0 + k, n - 1);
       b[k] = *reinterpret_cast<const f32x4*>(p.seg_state + s * per + i);
       g[k] = p.seg_decay[(long)s * p.H + head];
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 16; ++k) {
       if (s0 + k >= n) break;
       // -inf: the segment's end does not depend on its start (no product with
       // a start that may hold anything)
