@@ -391,8 +391,10 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
     auto scores = [&](int buf, int gb, int db) __attribute__((always_inline)) {
       const T* tb = lds.b[buf];
       const T* tc = lds.c[OUT ? buf : 0];
-      for (int idx = w; idx < 10; idx += NW) {
-        const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
+      // the four on the diagonal first, which take longest: one for each SIMD
+      for (int o = w; o < 10; o += NW) {
+        const int it = o < 4 ? o : o >= 7 ? 3 : o >= 5 ? 2 : 1, jt = o < 4 ? o : o - 4 - it * (it - 1) / 2;
+        const int idx = it * (it + 1) / 2 + jt;
         f32x4 s = zero4();
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) s = K::mma(rd.along(tb, jt, kb), rd.along(tc, it, kb), s);
