@@ -16,9 +16,9 @@
 // wave computes a 16 x 16 tile of them and leaves it in LDS with each head's
 // decays applied, so that nothing of it is computed twice; the gates of the
 // next chunk are made meanwhile by waves without a tile.  16 waves of 128
-// registers hide each other's latencies: their output pass takes 68 us (8192
-// tokens, 64 heads of 64, N = 128) where 8 waves of 32 channels took 76, 4 of
-// 64 channels 89, and two workgroups of 8 waves a compute unit 78.
+// registers hide each other's latencies: their output pass takes 65 us (8192
+// tokens, 64 heads of 64, N = 128), and took 68 where 8 waves of 32 channels
+// took 76, 4 of 64 channels 89, and two workgroups of 8 waves a compute unit 78.
 // What bounds it: the three-term state update (19 us of it), the chunk's
 // products and decays (21) and the tiles' movement (31) share two barriered
 // phases and overlap in part only.
@@ -244,7 +244,7 @@ struct SsmLds {
   alignas(16) T c[OUT ? NBUF : 1][OUT ? SC * ND : 8];
   // a chunk of y, to leave in whole rows (bf16): the 16 channels of wave w in
   // row r stand at w ^ (r % NW), their halves swapped in rows 8 to 15 of 16, so
-  // that the rows of a tile are written to different banks (2 us of 68 less)
+  // that the rows of a tile are written to different banks (65.8 us for 67.7)
   static constexpr bool STAGE = OUT && sizeof(T) == 2;
   alignas(16) T y[STAGE ? SC * 16 * NW : 8];
 };
