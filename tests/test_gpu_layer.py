@@ -227,6 +227,13 @@ def test_scan_packed(cu, dtype):
     scan_check(c, *run_scan(c, cu), cu=cu)
 
 
+@pytest.mark.parametrize("H,G,P,N", [(10, 2, 64, 128), (6, 1, 128, 64), (7, 1, 64, 32)])
+def test_scan_packed_with_a_part_of_a_workgroups_channels(H, G, P, N):
+    cu = torch.tensor([2, 2, 70, 71, 199, 460, 460, 600], dtype=torch.int32)
+    c = ref.scan_inputs(gen(H), 1, 640, H, G, P, N, BF, seqs=len(cu) - 1)
+    scan_check(c, *run_scan(c, cu), cu=cu)
+
+
 def test_scan_without_options_and_initial_state():
     c = ref.scan_inputs(gen(3), 2, 90, 2, 1, 64, 64, F32)
     c["dt"] = torch.nn.functional.softplus(c["dt"] - 3)
