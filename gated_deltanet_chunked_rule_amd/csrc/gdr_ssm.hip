@@ -117,6 +117,15 @@ template <int NB, int NX> struct Reader<bf16, NB, NX> {
     xrow = r * NX * 16 + 8 * (s & 1);
     xx = wx ^ (16 * ((s >> 1) ^ ssm_swz<bf16, NX>(r)));
   }
+  // four channels 4 q of this wave's columns of x, of token c of the first tile; further tiles 256 NX bytes on
+  static __device__ __forceinline__ const char* own_x(const bf16* t, int w, int c, int q) {
+    return reinterpret_cast<const char*>(t) + c * NX * 16 + ((32 * (w & 7)) ^ (16 * ((q >> 1) ^ ssm_swz<bf16, NX>(c)))) + 8 * (q & 1);
+  }
+  static __device__ __forceinline__ f32x4 x4(const char* a) {
+    const uint2 u = *reinterpret_cast<const uint2*>(a);
+    return f32x4{__builtin_bit_cast(float, u.x << 16), __builtin_bit_cast(float, u.x & 0xffff0000u),
+                 __builtin_bit_cast(float, u.y << 16), __builtin_bit_cast(float, u.y & 0xffff0000u)};
+  }
   // n along row 16 it + c
   __device__ __forceinline__ bf16x8 along(const bf16* t, int it, int kb) const {
     return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(t) + arow + ((64 * kb) ^ ax) + it * 256 * NB);
@@ -146,6 +155,10 @@ template <int NB, int NX> struct Reader<float, NB, NX> {
     xrow = 4 * q * NX * 16 + 4 * (c & 3);
     xx = wx ^ (16 * ((c >> 2) ^ ssm_swz<float, NX>(4 * q)));
   }
+  static __device__ __forceinline__ const char* own_x(const float* t, int w, int c, int q) {
+    return reinterpret_cast<const char*>(t) + c * NX * 16 + ((64 * (w & 7)) ^ (16 * (q ^ ssm_swz<float, NX>(c))));
+  }
+  static __device__ __forceinline__ f32x4 x4(const char* a) { return *reinterpret_cast<const f32x4*>(a); }
   __device__ __forceinline__ frag along(const float* t, int it, int kb) const {
     const char* p = reinterpret_cast<const char*>(t) + arow + it * 256 * NB;
     const f32x4 lo = *reinterpret_cast<const f32x4*>(p + ((128 * kb) ^ ax)), hi = *reinterpret_cast<const f32x4*>(p + ((128 * kb + 16) ^ ax));
@@ -235,7 +248,6 @@ struct SsmLds {
   float gam[3][SHEADS][SC], wt[3][SHEADS][SC];
   float d[2][OUT ? SHEADS : 1][OUT ? SC : 1], ut[2][OUT ? SHEADS : 1][OUT ? SC : 1];
   float rem[3][REM ? SHEADS : 1][REM ? SC : 1];
-  float skip[SHEADS];   // D
   int32_t cu[SCU];
   // the tiles last: what stands before them is in reach of an LDS access's
   // offset field, and needs no address registers of its own
@@ -326,7 +338,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
     }
   }
 
-  if (OUT && (int)threadIdx.x < heads) lds.skip[threadIdx.x] = p.D ? p.D[head0 + threadIdx.x] : 0.f;   // read behind the next barrier
+  const float skip = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(OUT && p.D ? __builtin_bit_cast(int, p.D[head]) : 0));
 
   const int seg0 = seg * p.seg, seg1 = min(seg0 + p.seg, p.s.Ttot);
   float total_gam = 0.f;
@@ -418,14 +430,9 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
               rj = *reinterpret_cast<const f32x4*>(&lds.rem[gb][k][16 * jt + 4 * q]);
               ri = lds.rem[gb][k][16 * it + c];
             }
-            const float skip = lds.skip[k];
             f32x4 pm;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float v = s[e] * (exp_f(gi - gj[e] + (ri - rj[e])) * dj[e]);
-              // D x_i joins the product as the diagonal's part of it
-              pm[e] = 4 * q + e < c ? v : 4 * q + e == c ? v + skip : 0.f;
-            }
+            for (int e = 0; e < 4; ++e) pm[e] = 4 * q + e <= c ? s[e] * (exp_f(gi - gj[e] + (ri - rj[e])) * dj[e]) : 0.f;
             lds.score[k][idx * 64 + l] = K::four(pm);
           }
         }
@@ -566,6 +573,13 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
         }
         // then the tokens of the chunk up to i
         const typename K::quad* sc = lds.score[hd] + l;
+        // and last D x_i, in fp32: on the scores' diagonal it would be rounded with
+        // them (the usual layer's y 2.28e-3 off its 64-bit values for 1.72e-3, of
+        // which its own rounding is 1.66e-3), and put first, the largest term, it
+        // would have the others rounded to its last place (fp32: 1.3e-7 for 5.7e-8)
+        int l1 = l;
+        asm volatile("" : "+v"(l1));   // the address is made here: kept over the chunk loop it would spill
+        const char* own = rd.own_x(lds.x[0][w / 8], w, l1 & 15, l1 >> 4);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
           if (16 * it >= len) break;
@@ -574,6 +588,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
             const typename K::quad* s0 = sc + (it * (it + 1) / 2 + 2 * jb) * 64;
             acc[it] = K::mma(xf[jb], K::join(s0[0], 2 * jb < it ? s0[64] : K::four(zero4())), acc[it]);
           }
+          acc[it] += skip * rd.x4(own + it * 256 * NX);
           if constexpr (Lds::STAGE) {
             *reinterpret_cast<typename K::quad*>(lds.y + ((16 * it + c) * NW + (w ^ (c % NW))) * 16 + 4 * (q ^ (c >> 3 << 1))) = K::four(acc[it]);
           } else if (live) {   // rows behind the chunk's last lie behind the descriptor

@@ -300,7 +300,10 @@ gdr_status gdr_step(const gdr_shape* shape, const void* q, int64_t q_stride, con
  *   d_t = dt_t + dt_bias, through softplus if dt_softplus
  *   S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T,   y_t = S_t^T C_t + D x_t
  * per head, with an fp32 [N, P] state; head h reads group h / (H / G) of B and
- * C.  No gradient is offered. */
+ * C.  States, gates, sums and D x are fp32.  With bf16, y's products over a
+ * chunk of tokens take two operands rounded to bf16: the decayed scores
+ * d_j (C_i . B_j) e^(sum of d A), and the chunk's entry state (the state itself is not
+ * rounded).  No gradient is offered. */
 typedef struct {
   int32_t B, T;               /* as in gdr_shape */
   int32_t H, G;               /* heads; groups of B and C (H % G == 0) */
