@@ -218,11 +218,17 @@ struct SeqFinder {
   const int32_t* cu;   // global, or the staged copy
   int N, T, Ttot;
   bool packed;
-  __device__ __forceinline__ int at(int n) const { return packed ? min(max(cu[n], 0), Ttot) : n * T; }
+  __host__ __device__ __forceinline__ int at(int n) const {
+    if (!packed) return n * T;
+    const int v = cu[n] < 0 ? 0 : cu[n];
+    return v < Ttot ? v : Ttot;
+  }
   // The run of tokens from t on (t < Ttot) that share a sequence: [start, end)
   // with start <= t < end, returns n; outside every sequence returns -1 and
-  // end is the first token to look at again.
-  __device__ __forceinline__ int find(int t, int& start, int& end) const {
+  // end is the first token to look at again.  Where offsets decrease, start
+  // may lie before the run that ended at t: 0 <= start <= t < end <= Ttot and
+  // 0 <= n < N are all that holds for any table.
+  __host__ __device__ __forceinline__ int find(int t, int& start, int& end) const {
     if (!packed) {
       const int n = t / T;
       start = n * T;
@@ -248,6 +254,10 @@ struct SeqFinder {
     end = e;
     return lo;
   }
+  // Whether the run found at t goes on from a piece [.., piece) of the token
+  // axis that another workgroup walked: its state is then that piece's.  Only
+  // at the piece's own first token, and never at token 0, whatever the table.
+  static __host__ __device__ __forceinline__ bool goes_on(int t, int piece, int start) { return t == piece && start < t; }
 };
 // Every thread of the workgroup calls this (barrier inside).
 template <int STAGE = kCuLds>

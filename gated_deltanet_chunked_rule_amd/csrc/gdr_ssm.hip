@@ -686,8 +686,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
           vec_store<T, 4>(y + (t + r) * HP + chan0 + 4 * (i - r * (cols / 4)), 4, zero);
         }
       } else {
-        if (start == t) load_state(p.h0 ? state_at(p.h0 + n * (long)p.H * sstride) : nullptr);
-        else load_state(state_at(p.seg_state + (seg - 1) * (long)p.H * sstride));
+        if (SeqFinder::goes_on(t, seg0, start)) load_state(state_at(p.seg_state + (seg - 1) * (long)p.H * sstride));
+        else load_state(p.h0 ? state_at(p.h0 + n * (long)p.H * sstride) : nullptr);
         run(t, stop);
         if (p.ht && stop == end) store_state(const_cast<float*>(state_at(p.ht + n * (long)p.H * sstride)));
       }
