@@ -50,6 +50,8 @@ gdr_status conv_check(const gdr_conv_shape* sh, bool packed) {
   if (!sh) return invalid("shape is NULL");
   if (gdr_status st = check_tokens(sh->B, sh->T, packed, sh->num_seqs, sh->dtype)) return st;
   if (sh->D < 1) return invalid("D must be positive");
+  // channel numbers plus a workgroup's channels (and an item's group of 8) fit an int
+  if (sh->D > (1 << 30)) return unsupported("D must be at most 2^30");
   if (sh->W < 2 || sh->W > 4) return unsupported("W must be 2, 3 or 4");
   if (sh->activation != GDR_ACT_NONE && sh->activation != GDR_ACT_SILU) return invalid("unknown activation");
   if (sh->x_stride != 0 && sh->x_stride < sh->D) return invalid("x_stride must be 0 or at least D");

@@ -254,7 +254,7 @@ typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
  * initial state (zeros without one).  Sums are fp32. */
 typedef struct {
   int32_t B, T;               /* as in gdr_shape */
-  int32_t D, W;               /* channels; taps, 2 to 4 */
+  int32_t D, W;               /* channels, at most 2^30; taps, 2 to 4 */
   int32_t num_seqs;           /* N in packed mode; ignored otherwise */
   gdr_dtype dtype;            /* of x, weight, bias, states, y and the gradients */
   gdr_activation activation;
