@@ -172,14 +172,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
     for (int v = 0; v < NV; ++v) {
       const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
       if (p.h_out && live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.h_out) + row * p.dim + d, nd, h[v]);
-      float y[8];
+      float y[8], low = 0.f;   // low: how far below zero the lane's gates reach
 #pragma unroll
       for (int c = 0; c < 8; ++c) y[c] = h[v][c] * r * w[v][c];
       if (gate) {
         float g[8];
         VecIO<T, 8>::up(rawg[v], g);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) y[c] *= g[c] * sigmoid_f(g[c]);
+        for (int c = 0; c < 8; ++c) {
+          y[c] *= g[c] * sigmoid_f(g[c]);
+          if (QUANT) low = fmaxf(low, -g[c]);
+        }
       }
       if constexpr (QUANT) {
         // a group of 128 values is 16 lanes of 8; the largest magnitude is taken
@@ -190,13 +193,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
         m = max16_u32(m);
         m = max(m, __builtin_bit_cast(uint32_t, kQuantTiny));
         float scale = __builtin_bit_cast(float, m) * (1.f / kE4M3Max);
-        // y / scale rounded to e4m3.  A value within 2^-20 of itself of a border
-        // between two of them may be on either side by fp32's own roundings:
-        // where both ends of that range round to the same value (no compare and
-        // no clamp is needed: 448 (1 + 2^-20) still rounds to 448), it is
-        // right; else the wave takes its groups again in 64 bits (by the
-        // density of the borders, 8 an octave, one wave of 512 values in 90).
-        const float inv = __builtin_amdgcn_rcpf(scale), inv0 = inv * (1.f - 0x1p-20f), inv1 = inv * (1.f + 0x1p-20f);
+        // y / scale rounded to e4m3 (from its fp32 rounding).  A value next to a
+        // border between two of them may be on either side by fp32's own
+        // roundings: where both ends of the range that these may move it over
+        // round to the same value (no compare and no clamp is needed: 448 (1 +
+        // 2^-16) still rounds to 448), it is right; else the wave takes its
+        // groups again in 64 bits (by the density of the borders, 8 an octave,
+        // one wave of 512 values in 90, in 45 with gates about zero).
+        // The range, in u = 2^-24: r is in y and in the group's largest value,
+        // and cancels; h, h r and w leave 3 u in each of the two, 1 / 448, scale,
+        // inv and the products with it 6 (the reciprocal's ulp is 2 u), and the
+        // scale's rounding beside the exact one 1: 13, 16 are taken.  A gate
+        // leaves 7.4 u more in each (exp2, 1 + e, reciprocal, two products, and
+        // the exponent's rounding at gates above zero), and below zero e^-g is
+        // off by 1.23 |g| u, the rounding of g log2 e: 28 + 2.45 |g| u in all, 32
+        // + 2.5 |g| are taken.  From 80 on e^-g nears fp32's end: 64 bits.
+        // (262144 x 128 with gates of std 1: 37.9 us; with the range of 2^-20 for
+        // all, which left 1 in 3e5 values wrong at gates of -30 to -40, 36.4.)
+        float margin = 0x1p-20f;
+        bool far = false;
+        if (gate) {
+          low = __builtin_bit_cast(float, max16_u32(__builtin_bit_cast(uint32_t, low)));
+          margin = fmaf(low, 2.5f * 0x1p-24f, 0x1p-19f);
+          far = low > 80.f;
+        }
+        const float inv = __builtin_amdgcn_rcpf(scale), inv0 = inv * (1.f - margin), inv1 = inv * (1.f + margin);
         int q[2] = {0, 0}, q1[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -205,7 +226,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
           q1[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * inv1, y[4 * i + 1] * inv1, q1[i], false);
           q1[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * inv1, y[4 * i + 3] * inv1, q1[i], true);
         }
-        if (__builtin_amdgcn_ballot_w64(q[0] != q1[0] || q[1] != q1[1]) != 0) {
+        if (__builtin_amdgcn_ballot_w64(far || q[0] != q1[0] || q[1] != q1[1]) != 0) {
           double sd = ssd;
           if constexpr (TPR <= 64) {
             sd = 0.0;
@@ -235,9 +256,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
           md = max_nan(md, dpp_d<0x141>(md));
           md = max_nan(md, dpp_d<0x140>(md));
           scale = (float)(md / (double)kE4M3Max);
+          const double inv_d = 1.0 / (double)scale;
           float f[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] = (float)(yd[c] / (double)scale);
+          for (int c = 0; c < 8; ++c) f[c] = (float)(yd[c] * inv_d);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);

@@ -351,6 +351,7 @@ typedef struct {
 
 /*   y             [rows, dim] of the call's dtype, or with quant one byte per value:
  *                 y = e4m3 value * scale, scale = max(max |y| of the group, 2^-100) / 448;
+ *                 the value is y / scale (of 64 bits) rounded to fp32 and from there to e4m3;
  *                 the last group of a row may be short.  A group with a NaN is NaN.
  *   scales        [rows, ceil(dim / 128)] fp32 (quant only)
  *   residual_out  [rows, dim] dense: h rounded to the call's dtype; nullable without residual.

@@ -37,3 +37,55 @@ def test_scan_skip_term_is_not_rounded_before_the_output(T, H, G, P, N, dtype):
     c["row"][..., H * P + G * N:] = 0       # C = 0: nothing but D x is left
     y, _ = run_scan(c)
     check(y, skip, skip.abs(), slack=2.0 ** -20, label="D x")
+
+
+# -------------------------------------------------------------------- norm --
+def e4m3_of(x, w, z=None, eps=1e-6):
+    """(8-bit values, scales) of the norm of rows in 64 bits, on the GPU; the quotient y / scale is rounded to fp32 and
+    from there to 8 bits, so that what ties in fp32 goes to the even value."""
+    h, w = x.double(), w.double()
+    y = h / torch.sqrt((h * h).mean(-1, keepdim=True) + eps) * w
+    if z is not None:
+        y = y * (z.double() / (1 + torch.exp(-z.double())))
+    y = y.unflatten(-1, (-1, 128))
+    s = (y.abs().amax(-1, keepdim=True).clamp(min=2.0 ** -100) / 448).float()
+    v = (y / s.double()).float().double()
+    unit = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    return (torch.round(v / unit) * unit).flatten(-2), s[..., 0]
+
+
+@pytest.mark.parametrize("lo,hi", [(-15.0, -10.0), (-30.0, -15.0), (-40.0, -30.0), (-85.0, -40.0), (-10.0, 10.0)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_to_8_bits_of_strongly_negative_gates(lo, hi, dtype):
+    # 2^25 values: every one the rounding of its 64-bit value, wherever the gates of a group lie
+    g = torch.Generator(device="cuda").manual_seed(int(-lo))
+    rows = 1 << 16
+    w = (1 + 0.2 * torch.randn(128, generator=g, device="cuda")).to(dtype)
+    wrong = 0
+    for _ in range(4):
+        x = torch.randn(rows, 128, generator=g, device="cuda").to(dtype)
+        z = (lo + (hi - lo) * torch.rand(rows, 128, generator=g, device="cuda")).to(dtype)
+        q, s, _ = gdr.gdr_rms_norm_fwd(x, w, None, z, quant=True)
+        want, scale = e4m3_of(x, w, z)
+        wrong += int((q.double() != want).sum())
+        # the fp32 chain's scale: 30 roundings and exp's argument, rounded at |z| log2 e
+        assert bool(((s / scale - 1).abs() <= (30 + 2 * max(0.0, -lo)) * 2.0 ** -24).all())
+    # a value whose 64-bit sum was added in another order may still differ where its fp32 rounding ties to 2^-50
+    print("wrong", wrong, flush=True)
+    assert wrong <= 1
+
+
+@pytest.mark.parametrize("dim,dtype", [(128, BF), (128, F32), (256, BF), (512, F32), (2048, BF)])
+def test_norm_to_8_bits_without_a_gate(dim, dtype):
+    # 2^25 values, as above
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    w = (1 + 0.2 * torch.randn(dim, generator=g, device="cuda")).to(dtype)
+    wrong = 0
+    for _ in range(4):
+        x = torch.randn(2 ** 23 // dim, dim, generator=g, device="cuda").to(dtype)
+        q, s, _ = gdr.gdr_rms_norm_fwd(x, w, quant=True)
+        want, scale = e4m3_of(x, w)
+        wrong += int((q.double() != want).sum())
+        assert bool(((s / scale - 1).abs() <= 30 * 2.0 ** -24).all())
+    print("wrong", wrong, flush=True)
+    assert wrong <= 1
