@@ -208,8 +208,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
         // the exponent's rounding at gates above zero), and below zero e^-g is
         // off by 1.23 |g| u, the rounding of g log2 e: 28 + 2.45 |g| u in all, 32
         // + 2.5 |g| are taken.  From 80 on e^-g nears fp32's end: 64 bits.
-        // (262144 x 128 with gates of std 1: 37.9 us; with the range of 2^-20 for
-        // all, which left 1 in 3e5 values wrong at gates of -30 to -40, 36.4.)
+        // (262144 x 128 with gates of std 1: 37 us; with the range of 2^-20 for
+        // all, which left 1 in 3e5 values wrong at gates of -30 to -40, 35.5.)
         float margin = 0x1p-20f;
         bool far = false;
         if (gate) {
@@ -226,7 +226,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
           q1[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * inv1, y[4 * i + 1] * inv1, q1[i], false);
           q1[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * inv1, y[4 * i + 3] * inv1, q1[i], true);
         }
-        if (__builtin_amdgcn_ballot_w64(far || q[0] != q1[0] || q[1] != q1[1]) != 0) {
+        auto leave = [&](const int (&q)[2], float scale) __attribute__((always_inline)) {
+          if (nd <= 0 || !live) return;
+          uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.dim + d;
+          if (nd == 8) {
+            *reinterpret_cast<u32x2_u1*>(out) = u32x2_u1{(uint32_t)q[0], (uint32_t)q[1]};
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (c < nd) out[c] = (uint8_t)((uint32_t)q[c / 4] >> (8 * (c % 4)));
+          }
+          if ((t & 15) == 0) p.scales[row * ((p.dim + 127) / 128) + d / 128] = scale;
+        };
+        // The wave takes all of its groups again, and writes only those that need
+        // it a second time: a row's values and scales are its own alone, whatever
+        // rows share the wave.  (Written first, the values take no registers
+        // meanwhile.)
+        const uint64_t again = __builtin_amdgcn_ballot_w64(far || q[0] != q1[0] || q[1] != q1[1]);
+        leave(q, scale);
+        if (again != 0) {
           double sd = ssd;
           if constexpr (TPR <= 64) {
             sd = 0.0;
@@ -265,17 +283,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
             q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], q[i], false);
             q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], q[i], true);
           }
+          if ((again >> (lane_id() & 48) & 0xffff) != 0) leave(q, scale);
         }
-        if (nd <= 0 || !live) continue;
-        uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.dim + d;
-        if (nd == 8) {
-          *reinterpret_cast<u32x2_u1*>(out) = u32x2_u1{(uint32_t)q[0], (uint32_t)q[1]};
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c < nd) out[c] = (uint8_t)((uint32_t)q[c / 4] >> (8 * (c % 4)));
-        }
-        if ((t & 15) == 0) p.scales[row * ((p.dim + 127) / 128) + d / 128] = scale;
       } else {
         if (nd > 0 && live) vec_store<T, 8>(static_cast<T*>(p.y) + row * p.dim + d, nd, y);
       }

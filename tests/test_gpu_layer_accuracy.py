@@ -89,3 +89,20 @@ def test_norm_to_8_bits_without_a_gate(dim, dtype):
         assert bool(((s / scale - 1).abs() <= 30 * 2.0 ** -24).all())
     print("wrong", wrong, flush=True)
     assert wrong <= 1
+
+
+@pytest.mark.parametrize("dim,dtype,gated", [(64, BF, False), (128, BF, True), (128, F32, False), (256, BF, True), (200, F32, True)])
+def test_norm_to_8_bits_of_a_row_does_not_depend_on_its_neighbours(dim, dtype, gated):
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    rows = 20001
+    x, z = (torch.randn(rows, dim, generator=g, device="cuda").to(dtype) for _ in range(2))
+    w = (1 + 0.2 * torch.randn(dim, generator=g, device="cuda")).to(dtype)
+    z = z if gated else None
+    q, s, _ = gdr.gdr_rms_norm_fwd(x, w, None, z, quant=True)
+    for first in (1, 2, 3, 5, 9):      # other rows share the wave
+        q1, s1, _ = gdr.gdr_rms_norm_fwd(x[first:], w, None, None if z is None else z[first:], quant=True)
+        assert torch.equal(q[first:].view(torch.uint8), q1.view(torch.uint8))
+        assert torch.equal(s[first:], s1)
+    for r in (0, 777, rows - 1):       # alone
+        q1, s1, _ = gdr.gdr_rms_norm_fwd(x[r:r + 1], w, None, None if z is None else z[r:r + 1], quant=True)
+        assert torch.equal(q[r:r + 1].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[r:r + 1], s1)
