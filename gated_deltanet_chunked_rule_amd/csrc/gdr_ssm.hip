@@ -385,8 +385,14 @@ __global__ __launch_bounds__(64 * NW, 1) void k_ssm(SsmParams p, int total) {
       float d = __builtin_bit_cast(float, F32 ? rdt : rdt << 16) + bias;
       if (p.softplus) d = softplus_f(d);
       if (t + l >= t1) d = 0.f;
-      // gam in 64 bits: a difference of two far sums keeps fp32's accuracy
-      const double gam = wave_scan((double)d * (double)A);
+      // gam in 64 bits: a difference of two far sums keeps fp32's accuracy.  A
+      // token that forgets everything counts as e^-256, which is zero in fp32
+      // (and stays so behind any growth that fp32 could hold): with its own sum,
+      // gam behind it would lose the small differences of the tokens that follow
+      // (bf16, which keeps gam without its remainder: 3 % where it was -1e6).
+      double step = (double)d * (double)A;
+      if (step < -256.0) step = -256.0;   // a NaN stays
+      const double gam = wave_scan(step);
       const float gf = (float)gam;
       lds.gam[gb][ghd][l] = gf;
       lds.wt[gb][ghd][l] = exp_f((float)(lane_f64(gam, 63) - gam)) * d;   // tokens behind the last have d = 0

@@ -39,6 +39,20 @@ def test_scan_skip_term_is_not_rounded_before_the_output(T, H, G, P, N, dtype):
     check(y, skip, skip.abs(), slack=2.0 ** -20, label="D x")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("step", [100.0, 62464.0, 2.0 ** 60])
+def test_scan_after_a_token_that_forgets_everything(step, dtype):
+    # one token of a chunk whose log-decay is -1600 to -2^64: the decays between later tokens are as exact as before it
+    c = ref.scan_inputs(gen(9), 1, 130, 4, 1, 64, 64, dtype)
+    c["A"] = torch.tensor([-16.0, -4.0, -1.0, -2.5])
+    c["dt"][0, 20] = step
+    c["dt"][0, 70] = step
+    y, ht = run_scan(c)
+    ry, rm, rh, rhm = ref.scan(*(c[n] for n in ("x", "dt", "A", "B", "C", "D", "bias", "h0")))
+    check(y, ry, rm, slack=2.0 ** -8 if dtype == BF else 2.0 ** -17, label="y")
+    check(ht, rh, rhm, slack=2.0 ** -17, label="state")
+
+
 # -------------------------------------------------------------------- norm --
 def e4m3_of(x, w, z=None, eps=1e-6):
     """(8-bit values, scales) of the norm of rows in 64 bits, on the GPU; the quotient y / scale is rounded to fp32 and
