@@ -85,6 +85,9 @@ def _entry(name):
 
 
 _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# The steps write to their states behind torch's back: told so, autograd refuses a
+# backward pass that kept such a state, instead of reading the new one.
+_changed = torch._C._increment_version
 
 
 def _call(index, fn, shape, *args):
@@ -285,6 +288,7 @@ def gdr_causal_conv_step(x, state, weight, bias=None, *, slots=None, activation=
     y = torch.empty(rows, D, device=dev, dtype=ty) if xs else torch.empty_like(x)
     if rows:
         _call(dev, _entry("gdr_causal_conv_step"), _ConvShape(rows, 1, D, W, 0, code, act, xs), xp, wp, bp, sp, n, lp, y.data_ptr())
+        _changed((state,))
     return y
 
 
@@ -338,6 +342,7 @@ def gdr_step(q, k, v, g, beta, state, scale=None, *, slots=None):
     if rows:
         _call(dev, _entry("gdr_step"), _Shape(rows, 1, Hq, Hv, K, V, 0, code), qp, qs, kp, ks, vp, vs, gp, bp,
               K ** -0.5 if scale is None else float(scale), sp, n, lp, o.data_ptr())
+        _changed((state,))
     return o
 
 
@@ -393,6 +398,7 @@ def gdr_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None, dt_
     if rows:
         _call(dev, _entry("gdr_ssm_step"), _SsmShape(rows, 1, H, G, P, N, 0, code, 1 if dt_softplus else 0, xs, ds, bs, cs),
               xp, dp, Ap, Bp, Cp, Dp, ip, sp, n, lp, y.data_ptr())
+        _changed((state,))
     return y
 
 
