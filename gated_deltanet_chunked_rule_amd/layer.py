@@ -21,6 +21,10 @@ a graph); on the host it is checked and copied.  Tokens that belong to no sequen
 get zero rows.  ``slots`` name each row's state in the pool: a row whose slot is out
 of range, or was named by an earlier row, is padding and gets a zero row.
 
+Where gradients are recorded, the entry points other than the ``_bwd`` ones refuse
+inputs that require one: ``causal_conv`` and ``rms_norm`` are the calls that give it.
+The ``_bwd`` ones return plain values.
+
 ``causal_conv`` and ``rms_norm`` can be captured with their backward, as any
 differentiable call of torch: on leaves that no eager graph alive was built from.
 """
@@ -196,8 +200,9 @@ def _offsets(cu_seqlens, B, T, dev):
 _grad_enabled = torch._C.is_grad_enabled if hasattr(torch._C, "is_grad_enabled") else torch.is_grad_enabled
 
 
-def _no_gradient(name):
-    raise GdrError(f"{name} offers no gradient: call it under torch.no_grad(), or detach its inputs")
+def _no_gradient(name, instead=None):
+    raise GdrError(f"{name} offers no gradient: call it under torch.no_grad(), or detach its inputs" if instead is None else
+                   f"{name} records no gradient: call {instead}, or call it under torch.no_grad()")
 
 
 def _ptr(t):
@@ -243,6 +248,9 @@ def gdr_causal_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=Non
                         output_final_state=False):
     """y = act(causal convolution of x): x [B, T, D] (strided), weight [D, W], initial_state [N, W - 1, D].
     Returns (y, final_state or None)."""
+    if _grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)
+                            or (initial_state is not None and initial_state.requires_grad)):
+        _no_gradient("gdr_causal_conv_fwd", "causal_conv")
     sh, xp, wp, bp, cu, N, dev = _conv_args(x, weight, bias, cu_seqlens, activation)
     state = (N, sh.W - 1, sh.D)
     hp = _dense(initial_state, "initial_state", state, x.dtype, dev)
@@ -446,6 +454,9 @@ def gdr_rms_norm_fwd(x, weight, residual=None, gate=None, *, eps=1e-6, quant=Fal
     """y = rms_norm(x + residual) * weight * silu(gate) over the last dimension; x, residual and gate [..., dim]
     (strided).  Returns (y, scales, h): with quant, y is float8_e4m3fn and scales [..., ceil(dim / 128)] fp32 hold one
     scale for each 128 values; h is the sum x + residual (None without a residual)."""
+    if _grad_enabled() and (x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad)
+                            or (gate is not None and gate.requires_grad)):
+        _no_gradient("gdr_rms_norm_fwd", "rms_norm")
     shape, rows, inner, dim = _norm_shape(x)
     code, dev, dt = _code(x), x.get_device(), x.dtype
     xp, xo, xi = _norm_rows(x, "x", shape, dt, dev)
