@@ -742,14 +742,18 @@ static int ssm_waves(DType dt, const SsmParams& p) {
 }
 
 // Segments: enough workgroups for every compute unit, of one chunk at least.
-// Up to three chunks run as one segment: a chunk takes about 8 us one after
-// another, the two further launches 16 (301 tokens of 8 heads, fp32: 33 us in
-// 5 segments, 46 in 2).
+// Up to three chunks (two in fp32) run as one segment: a further chunk takes 5
+// us one after another, in fp32 9 to 13, the two further launches 6 to 8 (one
+// segment / several, us a call: bf16, 64 heads of 64, N = 128, 3 chunks 23.9 /
+// 28.8, 4 chunks 29.1 / 31.1, 6 chunks 39.3 / 37.4; 8 heads, 3 chunks 23.3 /
+// 24.4, 4 chunks 28.5 / 24.5; fp32, 8 heads of 32, N = 64, 2 chunks 22.3 / 22.9,
+// 3 chunks 31.2 / 23.0; 64 heads of 64, N = 128, 2 chunks 32.2 / 33.2, 3 chunks
+// 45.4 / 35.0).
 void ssm_plan(DType dt, SsmParams& p) {
   const int hp = p.H / p.G * p.P, cols = 16 * ssm_waves(dt, p);
   p.wgs = p.G * ((hp + cols - 1) / cols);
   const long chunks = ((long)p.s.Ttot + SC - 1) / SC;
-  long segs = chunks <= 3 ? 1 : (kComputeUnits + p.wgs - 1) / p.wgs;
+  long segs = chunks <= (dt == DType::BF16 ? 3 : 2) ? 1 : (kComputeUnits + p.wgs - 1) / p.wgs;
   segs = segs > chunks ? chunks : segs;
   segs = segs < 1 ? 1 : segs;
   p.seg = (int)((chunks + segs - 1) / segs) * SC;
