@@ -5,8 +5,8 @@
 // All three are bound by memory: a thread owns VEC channels and walks down the
 // tokens of a tile with the last W - 1 inputs in registers, so every input is
 // read once (and W - 1 rows again at a tile's start).  8192 tokens x 8192
-// channels in bf16 take 50 us (5.4 TB/s), the gradient of 32768 x 8192 346
-// and 13 for its sums (4.5 TB/s), one token of 128 sequences 5.7 us, of which
+// channels in bf16 take 53 us (5.1 TB/s), the gradient of 32768 x 8192 338
+// and 14 for its sums (4.6 TB/s), one token of 128 sequences 5.7 us, of which
 // about 3 are a launch's own.
 #include "gdr_layer.h"
 
@@ -359,8 +359,8 @@ static int tile_for(long groups, int tokens, long threads, int lo, int hi) {
   while (tile > lo && groups * ((tokens + tile - 1) / tile) < threads) tile /= 2;
   return tile;
 }
-// The gradient: 32768 x 8192 take 338 + 14 us (sums) in tiles of 128 tokens, 356
-// + 9 in tiles of 256, 380 + 7 in tiles of 512.
+// The gradient: 32768 x 8192 take 338 + 14 us (sums) in tiles of 128 tokens, 354
+// + 9 in tiles of 256, 368 + 7 in tiles of 512.
 int conv_bwd_tile(int tokens, int D) { return tile_for((D + 3) / 4, tokens, 1L << 19, 16, 256); }
 
 template <typename T, int W>

@@ -242,6 +242,9 @@ const char* gdr_last_error(void);
  *   slots[r] (slots NULL: slot r, rows <= num_slots), in place.  A row whose
  *   slot is outside [0, num_slots), or was named by an earlier row of the same
  *   call, is padding: its output row is zero and no state changes.
+ *   Each row looks at the slots of all rows before it: 2 % of a call at 256
+ *   rows, 10 % at 1024, as much again at 4096 (convolution; the rule's and the
+ *   scan's larger states hide it).  Without slots nothing is looked at.
  * Non-finite inputs reach what the formulas let them reach and nothing else:
  *   no earlier token, no other sequence, no other row.  In the scan an
  *   infinity may come out as a NaN. */
