@@ -7,7 +7,7 @@ import torch
 import gated_deltanet_chunked_rule_amd as gdr
 import layer_reference as ref
 from gated_deltanet_chunked_rule_amd import layer
-from layer_reference import gen, randn
+from layer_reference import check, gen, randn
 
 pytestmark = pytest.mark.gpu
 GUARD = 1 << 20
@@ -52,3 +52,21 @@ def test_convolution_on_tables_that_decrease(cu):
     grads = gdr.gdr_causal_conv_bwd(x, w, None, dy, h0, dht, table, workspace=ws)
     assert untouched(whole)
     assert all(bool(torch.isfinite(t).all()) for t in (y, ht, *grads[:2], grads[3]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens", [[0] * 200, [0, 0, 300] + [0] * 150 + [500, 0, 7] + [0] * 40, [900] + [0] * 63, [0] * 129 + [130]])
+def test_scan_of_a_batch_that_is_mostly_empty(lens, dtype):
+    # a table with room for more sequences than there are: the empty ones keep their states, whichever workgroup copies them
+    T, N, H = 900, len(lens), 6
+    c = ref.scan_inputs(gen(N), 1, T, H, 2, 32, 32, dtype, seqs=N)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    d = {n: c[n].contiguous().to("cuda") for n in ("x", "dt", "A", "B", "C", "D", "bias", "h0")}
+    for h0 in (d["h0"], None):
+        y, ht = gdr.gdr_ssm_scan_fwd(*(d[n] for n in ("x", "dt", "A", "B", "C", "D", "bias")), h0, cu.to("cuda"), output_final_state=True)
+        ry, rm, rh, rhm = ref.scan(*(c[n] for n in ("x", "dt", "A", "B", "C", "D", "bias")), None if h0 is None else c["h0"], cu)
+        check(y, ry, rm, slack=2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -17, label="y")
+        check(ht, rh, rhm, slack=2.0 ** -17, label="states")
+        empty = torch.tensor([n for n in range(N) if lens[n] == 0])
+        want = c["h0"][empty] if h0 is not None else torch.zeros_like(c["h0"][empty])
+        assert torch.equal(ht.cpu()[empty], want)
