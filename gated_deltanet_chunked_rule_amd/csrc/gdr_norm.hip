@@ -213,7 +213,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
         float margin = 0x1p-20f;
         bool far = false;
         if (gate) {
-          low = __builtin_bit_cast(float, max16_u32(__builtin_bit_cast(uint32_t, low)));
+          low = __builtin_bit_cast(float, max16_u32(__builtin_bit_cast(uint32_t, low) & 0x7fffffffu));   // (the larger of 0 and -0 may be -0)
           margin = fmaf(low, 2.5f * 0x1p-24f, 0x1p-19f);
           far = low > 80.f;
         }

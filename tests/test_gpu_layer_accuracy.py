@@ -120,3 +120,20 @@ def test_norm_to_8_bits_of_a_row_does_not_depend_on_its_neighbours(dim, dtype, g
     for r in (0, 777, rows - 1):       # alone
         q1, s1, _ = gdr.gdr_rms_norm_fwd(x[r:r + 1], w, None, None if z is None else z[r:r + 1], quant=True)
         assert torch.equal(q[r:r + 1].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[r:r + 1], s1)
+
+
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+def test_norm_to_8_bits_of_gates_that_are_zero_or_strongly_negative(zero):
+    # lanes whose gates are all zero, of either sign, beside lanes whose gates decide the range that is looked at again
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows = 1 << 16
+    w = torch.ones(128, device="cuda", dtype=F32)
+    wrong = 0
+    for _ in range(4):
+        x = torch.randn(rows, 128, generator=g, device="cuda")
+        z = -40 + 10 * torch.rand(rows, 128, generator=g, device="cuda")
+        z[:, 32:48] = zero
+        q, _, _ = gdr.gdr_rms_norm_fwd(x, w, None, z, quant=True)
+        wrong += int((q.double() != e4m3_of(x, w, z)[0]).sum())
+    print("wrong", wrong, flush=True)
+    assert wrong <= 1
