@@ -19,7 +19,9 @@ Functions
     The high-level call of the same listing, differentiable through
     ``torch.autograd``: ``(o, final_state)``.
 ``gdr_step``, ``gdr_causal_conv_fwd`` / ``_bwd`` / ``_step``, ``gdr_ssm_scan_fwd``,
-``gdr_ssm_step``, ``gdr_rms_norm_fwd`` / ``_bwd``, ``causal_conv``, ``rms_norm``
+``gdr_ssm_step``, ``gdr_rms_norm_fwd`` / ``_bwd``, ``gdr_linear_scan_fwd`` / ``_bwd`` / ``_step``,
+``gdr_block_norm_fwd`` / ``_bwd``, ``gdr_quantize_rows``, ``gdr_matmul_i8``, ``causal_conv``, ``rms_norm``,
+``linear_scan``, ``block_norm``
     The operators around the rule in a layer, and its form for one new token
     (the ``layer`` module).
 
@@ -41,7 +43,9 @@ __all__ = ["gdr_chunk_fwd", "gdr_chunk_fwd_noalloc", "gdr_chunk_bwd", "gdr_chunk
            "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd", "Options", "lib_path",
            "load_library", "GdrError", "timing",
            "gdr_step", "gdr_causal_conv_fwd", "gdr_causal_conv_bwd", "gdr_causal_conv_step", "gdr_ssm_scan_fwd",
-           "gdr_ssm_step", "gdr_rms_norm_fwd", "gdr_rms_norm_bwd", "causal_conv", "rms_norm"]
+           "gdr_ssm_step", "gdr_rms_norm_fwd", "gdr_rms_norm_bwd", "causal_conv", "rms_norm",
+           "gdr_linear_scan_fwd", "gdr_linear_scan_bwd", "gdr_linear_scan_step", "gdr_block_norm_fwd", "gdr_block_norm_bwd",
+           "gdr_quantize_rows", "gdr_matmul_i8", "linear_scan", "block_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -415,5 +419,7 @@ class timing:
         return out
 
 
-from .layer import (causal_conv, gdr_causal_conv_bwd, gdr_causal_conv_fwd, gdr_causal_conv_step,  # noqa: E402
-                    gdr_rms_norm_bwd, gdr_rms_norm_fwd, gdr_ssm_scan_fwd, gdr_ssm_step, gdr_step, rms_norm)
+from .layer import (block_norm, causal_conv, gdr_block_norm_bwd, gdr_block_norm_fwd, gdr_causal_conv_bwd,  # noqa: E402
+                    gdr_causal_conv_fwd, gdr_causal_conv_step, gdr_linear_scan_bwd, gdr_linear_scan_fwd,
+                    gdr_linear_scan_step, gdr_matmul_i8, gdr_quantize_rows, gdr_rms_norm_bwd, gdr_rms_norm_fwd,
+                    gdr_ssm_scan_fwd, gdr_ssm_step, gdr_step, linear_scan, rms_norm)

@@ -1,6 +1,6 @@
 // gdr_layer.h -- parameter blocks, launchers and device helpers of the
 // operators around the rule (convolution, single-token steps, state space
-// scan, norm); internal to libgdr.
+// scan, linear recurrence, norms, integer products); internal to libgdr.
 #pragma once
 
 #include "../../include/gdr.h"
@@ -75,6 +75,54 @@ struct NormParams {
   int blocks;
 };
 
+struct LinParams {               // linear scan; the step: Ttot rows, ht the pool of states
+  SeqRanges s;
+  const void *x, *r, *i, *dy;
+  const float *A, *h0, *dht;
+  void *y, *dx, *dr, *di;
+  float *ht, *dh0, *dA;
+  float *P, *S, *Q, *part;       // [tiles][D] each
+  const int32_t* slots;
+  long x_stride, r_stride, i_stride;
+  int D, tiles, cols, num_slots; // tiles of tokens, columns of channels
+};
+
+struct BlockNormParams {
+  long rows;
+  int dim, blocks;
+  float eps, inv_dim;
+  const void *x, *residual, *gate, *post, *pre, *scale;
+  const void *h, *dy, *dres;     // backward; h has residual's stride
+  long x_stride, r_stride, g_stride;
+  void *y, *h_out;
+  void *dx, *dh, *dgate, *dpost, *dpre, *dscale;
+  float* part;                   // [blocks][2 or 3][dim]: sums for dpost, dpre, dscale
+};
+
+struct RowsSum {
+  const float* part;             // [rows][outputs][dim]
+  int rows, dim;
+  void* out[3];
+};
+
+struct QuantParams {
+  long rows;
+  int dim, pad;                  // values of a row, and with the zeros behind them
+  const void* x;
+  int8_t* q;
+  float* scales;
+  long x_stride, q_stride;
+};
+
+struct I8Params {
+  const int8_t *x, *w;           // [M][K], [N][K]
+  const float *xs, *ws, *bias;
+  void* y;
+  long x_stride, w_stride;
+  int M, N, K;
+  int tm, tn, tiles, group;      // tiles of x and the weight, rows of tiles that are walked together
+};
+
 hipError_t launch_conv_fwd(DType dt, int W, const ConvParams& p, hipStream_t st);
 hipError_t launch_conv_bwd(DType dt, int W, const ConvParams& p, hipStream_t st);
 hipError_t launch_conv_step(DType dt, int W, int rows, const ConvParams& p, hipStream_t st);
@@ -86,6 +134,17 @@ hipError_t launch_ssm_scan(DType dt, const SsmParams& p, hipStream_t st);
 hipError_t launch_norm_fwd(DType dt, bool quant, const NormParams& p, hipStream_t st);
 hipError_t launch_norm_bwd(DType dt, const NormParams& p, hipStream_t st);
 int norm_bwd_blocks(long rows, int dim);
+int lin_tiles(int tokens);                  // tiles of the token axis
+int lin_cols(int D);
+hipError_t launch_lin_fwd(DType dt, const LinParams& p, hipStream_t st);
+hipError_t launch_lin_bwd(DType dt, const LinParams& p, hipStream_t st);
+hipError_t launch_lin_step(DType dt, const LinParams& p, hipStream_t st);
+hipError_t launch_block_norm_fwd(DType dt, const BlockNormParams& p, hipStream_t st);
+hipError_t launch_block_norm_bwd(DType dt, const BlockNormParams& p, hipStream_t st);
+int block_norm_bwd_blocks(long rows, int dim);
+hipError_t launch_quant_rows(DType dt, const QuantParams& p, hipStream_t st);
+hipError_t launch_i8_matmul(DType dt, const I8Params& p, hipStream_t st);
+hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t st);   // dt: of the outputs
 
 // ------------------------------------------------------------- device part --
 // VEC consecutive elements that need the alignment of one element only:
@@ -259,6 +318,31 @@ struct SeqFinder {
   // at the piece's own first token, and never at token 0, whatever the table.
   static __host__ __device__ __forceinline__ bool goes_on(int t, int piece, int start) { return t == piece && start < t; }
 };
+// What happens at the `count` (below 32) tokens from t0 on, as bits: first: the
+// token starts a run that does not go on from the tokens before t0; last: it
+// ends its sequence; gap: it belongs to none, or lies behind the last token.
+// A token that starts or ends a run finds a sequence, whatever the table (where
+// offsets decrease, a run's tokens may find different ones).
+struct TokenRuns { uint32_t first, last, gap; };
+__host__ __device__ __forceinline__ TokenRuns token_runs(const SeqFinder& sf, int t0, int count) {
+  TokenRuns m = {0, 0, 0};
+  const int t1 = t0 + count < sf.Ttot ? t0 + count : sf.Ttot;
+  for (int t = t0; t < t1;) {
+    int start, end;
+    const int n = sf.find(t, start, end), stop = end < t1 ? end : t1;
+    if (n < 0) {
+      m.gap |= ((1u << (stop - t)) - 1u) << (t - t0);
+    } else {
+      if (!SeqFinder::goes_on(t, t0, start)) m.first |= 1u << (t - t0);
+      int s, e;
+      if (end <= t1 && sf.find(end - 1, s, e) >= 0) m.last |= 1u << (end - 1 - t0);
+    }
+    t = stop;
+  }
+  const int live = t1 > t0 ? t1 - t0 : 0;
+  if (live < count) m.gap |= ~0u << live;
+  return m;
+}
 // Every thread of the workgroup calls this (barrier inside).
 template <int STAGE = kCuLds>
 __device__ __forceinline__ SeqFinder seq_finder(const SeqRanges& s, int32_t* lds) {

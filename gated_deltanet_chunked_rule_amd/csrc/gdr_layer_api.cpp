@@ -45,6 +45,11 @@ gdr::SeqRanges ranges(int B, int T, int num_seqs, const int32_t* cu) {
   return s;
 }
 
+// Lanes that a row of dim values takes in the kernels that hold whole rows.
+long row_threads(int dim) {
+  return dim <= 128 ? 16 : dim <= 256 ? 32 : dim <= 512 ? 64 : dim <= 1024 ? 128 : dim <= 4096 ? 256 : dim <= 8192 ? 512 : 1024;
+}
+
 // ------------------------------------------------------------ convolution --
 gdr_status conv_check(const gdr_conv_shape* sh, bool packed) {
   if (!sh) return invalid("shape is NULL");
@@ -129,9 +134,7 @@ gdr_status norm_check(const gdr_norm_shape* sh) {
   if (sh->dim > 16384) return unsupported("dim must be at most 16384");
   if (!(std::isfinite(sh->eps) && sh->eps >= 0.f)) return invalid("eps must be finite and not negative");
   if (sh->quant != 0 && sh->quant != 1) return invalid("quant must be 0 or 1");
-  const int per = sh->dim <= 128 ? 16 : sh->dim <= 256 ? 32 : sh->dim <= 512 ? 64 : sh->dim <= 1024 ? 128
-                  : sh->dim <= 4096 ? 256 : sh->dim <= 8192 ? 512 : 1024;
-  if (sh->rows > (kMaxThreads - 1024) / per) return unsupported("too many rows");
+  if (sh->rows > (kMaxThreads - 1024) / row_threads(sh->dim)) return unsupported("too many rows");
   const gdr_row_stride* st[3] = {&sh->x_stride, &sh->residual_stride, &sh->gate_stride};
   for (const gdr_row_stride* s : st)
     if (s->outer < 0 || s->inner < 0) return invalid("row strides must not be negative");
@@ -149,6 +152,59 @@ gdr::NormParams norm_params(const gdr_norm_shape* sh) {
   row_stride(sh, sh->residual_stride, p.ro, p.ri);
   row_stride(sh, sh->gate_stride, p.go, p.gi);
   p.blocks = gdr::norm_bwd_blocks(sh->rows, sh->dim);
+  return p;
+}
+
+// ----------------------------------------------------- linear recurrence --
+gdr_status lin_check(const gdr_linear_scan_shape* sh, bool packed) {
+  if (!sh) return invalid("shape is NULL");
+  if (gdr_status st = check_tokens(sh->B, sh->T, packed, sh->num_seqs, sh->dtype)) return st;
+  if (sh->D < 1) return invalid("D must be positive");
+  if (sh->D > (1 << 30)) return unsupported("D must be at most 2^30");   // channel numbers plus a column's fit an int
+  const int64_t st[3] = {sh->x_stride, sh->r_stride, sh->i_stride};
+  for (int64_t s : st)
+    if (s != 0 && s < sh->D) return invalid("a token stride is smaller than its row");
+  if ((long)gdr::lin_tiles(sh->B * sh->T) * gdr::lin_cols(sh->D) > kMaxThreads / 512) return unsupported("too many tokens times channels");
+  return GDR_OK;
+}
+gdr::LinParams lin_params(const gdr_linear_scan_shape* sh, const void* x, const void* r, const void* i, const float* A,
+                          const float* h0, const int32_t* cu) {
+  gdr::LinParams p = {};
+  p.s = ranges(sh->B, sh->T, sh->num_seqs, cu);
+  p.x = x; p.r = r; p.i = i; p.A = A; p.h0 = h0;
+  p.x_stride = sh->x_stride ? sh->x_stride : sh->D;
+  p.r_stride = sh->r_stride ? sh->r_stride : sh->D;
+  p.i_stride = sh->i_stride ? sh->i_stride : sh->D;
+  p.D = sh->D;
+  p.tiles = gdr::lin_tiles(sh->B * sh->T);
+  p.cols = gdr::lin_cols(sh->D);
+  return p;
+}
+// One row of D fp32 values for each tile of tokens.
+size_t lin_rows_bytes(const gdr_linear_scan_shape* sh) { return align_up((size_t)gdr::lin_tiles(sh->B * sh->T) * sh->D * 4); }
+
+// ------------------------------------------------------ norms of a block --
+gdr_status block_norm_check(const gdr_block_norm_shape* sh) {
+  if (!sh) return invalid("shape is NULL");
+  if (sh->dtype != GDR_BF16 && sh->dtype != GDR_F32) return unsupported("dtype must be GDR_BF16 or GDR_F32");
+  if (sh->rows < 0 || sh->dim < 1) return invalid("rows must not be negative, dim positive");
+  if (sh->dim > 16384) return unsupported("dim must be at most 16384");
+  if (!(std::isfinite(sh->eps) && sh->eps >= 0.f)) return invalid("eps must be finite and not negative");
+  const int64_t st[3] = {sh->x_stride, sh->residual_stride, sh->gate_stride};
+  for (int64_t s : st)
+    if (s != 0 && s < sh->dim) return invalid("a row stride is smaller than its row");
+  if (sh->rows > (kMaxThreads - 1024) / row_threads(sh->dim)) return unsupported("too many rows");
+  return GDR_OK;
+}
+gdr::BlockNormParams block_norm_params(const gdr_block_norm_shape* sh, const void* x, const void* gate, const void* post,
+                                       const void* pre, const void* scale) {
+  gdr::BlockNormParams p = {};
+  p.rows = sh->rows; p.dim = sh->dim; p.eps = sh->eps; p.inv_dim = 1.f / (float)sh->dim;
+  p.x = x; p.gate = gate; p.post = post; p.pre = pre; p.scale = scale;
+  p.x_stride = sh->x_stride ? sh->x_stride : sh->dim;
+  p.r_stride = sh->residual_stride ? sh->residual_stride : sh->dim;
+  p.g_stride = sh->gate_stride ? sh->gate_stride : sh->dim;
+  p.blocks = gdr::block_norm_bwd_blocks(sh->rows, sh->dim);
   return p;
 }
 
@@ -338,6 +394,175 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const vo
   p.x = h; p.gate = gate; p.weight = weight; p.dy = dy; p.dres = d_res; p.dh = dh; p.dw = dw; p.dgate = dgate;
   p.part = static_cast<float*>(workspace);
   return done(gdr::launch_norm_bwd(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdr_linear_scan_fwd_workspace_size(const gdr_linear_scan_shape* shape) {
+  if (lin_check(shape, false) != GDR_OK) return 0;
+  return 2 * lin_rows_bytes(shape);
+}
+
+gdr_status gdr_linear_scan_fwd(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
+                               const float* A, const float* initial_state, const int32_t* cu_seqlens, void* y,
+                               float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+  if (gdr_status st = lin_check(shape, cu_seqlens != nullptr)) return st;
+  if (!A || (shape->T > 0 && (!x || !r || !i || !y))) return invalid("x, r, i, A and y must be non-NULL");
+  const void* ptrs[] = {x, r, i, y};
+  const void* f32[] = {A, initial_state, final_state, cu_seqlens};
+  if (!all_aligned(ptrs, esize(shape->dtype)) || !all_aligned(f32, 4)) return invalid("device pointers must be aligned to their elements");
+  if (in_place(y, x) || in_place(y, r) || in_place(y, i) || in_place(final_state, initial_state))
+    return invalid("y and final_state must not overlap x, r, i and initial_state");
+  if (!workspace || workspace_bytes < 2 * lin_rows_bytes(shape))
+    return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_linear_scan_fwd_workspace_size)");
+  if (!aligned(workspace, 16)) return invalid("workspace must be 16-byte aligned");
+  gdr::LinParams p = lin_params(shape, x, r, i, A, initial_state, cu_seqlens);
+  p.y = y; p.ht = final_state;
+  p.P = static_cast<float*>(workspace);
+  p.S = reinterpret_cast<float*>(static_cast<char*>(workspace) + lin_rows_bytes(shape));
+  return done(gdr::launch_lin_fwd(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdr_linear_scan_bwd_workspace_size(const gdr_linear_scan_shape* shape) {
+  if (lin_check(shape, false) != GDR_OK) return 0;
+  return 4 * lin_rows_bytes(shape);
+}
+
+gdr_status gdr_linear_scan_bwd(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
+                               const float* A, const float* initial_state, const int32_t* cu_seqlens, const void* dy,
+                               const float* dht, void* dx, void* dr, void* di, float* dA, float* dh0, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (gdr_status st = lin_check(shape, cu_seqlens != nullptr)) return st;
+  if (!A || !dA || (shape->T > 0 && (!x || !r || !i || !dy || !dx || !dr || !di)))
+    return invalid("x, r, i, A, dy, dx, dr, di and dA must be non-NULL");
+  const void* ptrs[] = {x, r, i, dy, dx, dr, di};
+  const void* f32[] = {A, initial_state, dht, dA, dh0, cu_seqlens};
+  if (!all_aligned(ptrs, esize(shape->dtype)) || !all_aligned(f32, 4)) return invalid("device pointers must be aligned to their elements");
+  const void* outs[] = {dx, dr, di};
+  for (const void* o : outs)
+    if (in_place(o, x) || in_place(o, r) || in_place(o, i) || in_place(o, dy)) return invalid("dx, dr and di must not overlap x, r, i and dy");
+  if (in_place(dh0, initial_state) || in_place(dh0, dht)) return invalid("dh0 must not overlap initial_state and dht");
+  if (!workspace || workspace_bytes < 4 * lin_rows_bytes(shape))
+    return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_linear_scan_bwd_workspace_size)");
+  if (!aligned(workspace, 16)) return invalid("workspace must be 16-byte aligned");
+  gdr::LinParams p = lin_params(shape, x, r, i, A, initial_state, cu_seqlens);
+  p.dy = dy; p.dht = dht; p.dx = dx; p.dr = dr; p.di = di; p.dA = dA; p.dh0 = dh0;
+  float** rows[] = {&p.P, &p.S, &p.Q, &p.part};
+  for (int k = 0; k < 4; ++k) *rows[k] = reinterpret_cast<float*>(static_cast<char*>(workspace) + k * lin_rows_bytes(shape));
+  return done(gdr::launch_lin_bwd(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+gdr_status gdr_linear_scan_step(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
+                                const float* A, float* state, int32_t num_slots, const int32_t* slots, void* y,
+                                void* stream) {
+  if (gdr_status st = lin_check(shape, false)) return st;
+  if (shape->T != 1) return invalid("a step takes T == 1 (B rows)");
+  if (!x || !r || !i || !A || !state || !y) return invalid("x, r, i, A, state and y must be non-NULL");
+  if (num_slots < 1 || (!slots && num_slots < shape->B)) return invalid("num_slots must cover the rows");
+  const void* ptrs[] = {x, r, i, y};
+  const void* f32[] = {A, state, slots};
+  if (!all_aligned(ptrs, esize(shape->dtype)) || !all_aligned(f32, 4)) return invalid("device pointers must be aligned to their elements");
+  if ((long)shape->B * gdr::lin_cols(shape->D) > kMaxThreads / (64 * 4)) return unsupported("too many rows times channels");
+  gdr::LinParams p = lin_params(shape, x, r, i, A, nullptr, nullptr);
+  p.y = y; p.ht = state; p.slots = slots; p.num_slots = num_slots;
+  return done(gdr::launch_lin_step(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+gdr_status gdr_block_norm_fwd(const gdr_block_norm_shape* shape, const void* x, const void* residual, const void* gate,
+                              const void* post_weight, const void* pre_weight, const void* scale, void* y, void* h,
+                              void* stream) {
+  if (gdr_status st = block_norm_check(shape)) return st;
+  if (!post_weight || !pre_weight || (shape->rows > 0 && (!x || !residual || !y || !h)))
+    return invalid("x, residual, post_weight, pre_weight, y and h must be non-NULL");
+  const void* ptrs[] = {x, residual, gate, post_weight, pre_weight, scale, y, h};
+  if (!all_aligned(ptrs, esize(shape->dtype))) return invalid("device pointers must be aligned to their elements");
+  if (in_place(h, residual) && shape->residual_stride != 0 && shape->residual_stride != shape->dim)
+    return invalid("h may take residual's place only where that is dense");
+  if (in_place(y, h) || in_place(y, x) || in_place(y, residual) || in_place(y, gate) || in_place(h, x) || in_place(h, gate))
+    return invalid("y and h must not overlap x, gate and each other");
+  if (shape->rows == 0) return GDR_OK;
+  gdr::BlockNormParams p = block_norm_params(shape, x, gate, post_weight, pre_weight, scale);
+  p.residual = residual; p.y = y; p.h_out = h;
+  return done(gdr::launch_block_norm_fwd(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdr_block_norm_bwd_workspace_size(const gdr_block_norm_shape* shape) {
+  if (block_norm_check(shape) != GDR_OK) return 0;
+  return align_up(((size_t)gdr::block_norm_bwd_blocks(shape->rows, shape->dim) * 3 * shape->dim + 1) * 4);
+}
+
+gdr_status gdr_block_norm_bwd(const gdr_block_norm_shape* shape, const void* x, const void* h, const void* gate,
+                              const void* post_weight, const void* pre_weight, const void* scale, const void* dy,
+                              const void* d_res, void* dx, void* dh, void* dgate, void* dpost, void* dpre,
+                              void* dscale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (gdr_status st = block_norm_check(shape)) return st;
+  if (!post_weight || !pre_weight || !dpost || !dpre || (scale && !dscale) ||
+      (shape->rows > 0 && (!x || !h || !dy || !dx || !dh || (gate && !dgate))))
+    return invalid("x, h, post_weight, pre_weight, dy, dx, dh, dpost, dpre (dgate with a gate, dscale with a scale) must be non-NULL");
+  const void* ptrs[] = {x, h, gate, post_weight, pre_weight, scale, dy, d_res, dx, dh, dgate, dpost, dpre, dscale};
+  if (!all_aligned(ptrs, esize(shape->dtype))) return invalid("device pointers must be aligned to their elements");
+  const void* outs[] = {dx, dh, dgate};
+  const void* ins[] = {x, h, gate, dy, d_res};
+  for (const void* o : outs)
+    for (const void* in : ins)
+      if (in_place(o, in)) return invalid("dx, dh and dgate must not overlap x, h, gate, dy and d_res");
+  if (!workspace || workspace_bytes < gdr_block_norm_bwd_workspace_size(shape))
+    return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_block_norm_bwd_workspace_size)");
+  if (!aligned(workspace, 16)) return invalid("workspace must be 16-byte aligned");
+  gdr::BlockNormParams p = block_norm_params(shape, x, gate, post_weight, pre_weight, scale);
+  p.h = h; p.dy = dy; p.dres = d_res;
+  p.dx = dx; p.dh = dh; p.dgate = dgate; p.dpost = dpost; p.dpre = dpre; p.dscale = dscale;
+  p.part = static_cast<float*>(workspace);
+  return done(gdr::launch_block_norm_bwd(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+gdr_status gdr_quantize_rows(const gdr_quantize_shape* shape, const void* x, int8_t* q, float* scales, void* stream) {
+  if (!shape) return invalid("shape is NULL");
+  if (shape->dtype != GDR_BF16 && shape->dtype != GDR_F32) return unsupported("dtype must be GDR_BF16 or GDR_F32");
+  if (shape->rows < 0 || shape->dim < 1) return invalid("rows must not be negative, dim positive");
+  if (shape->dim > 32768) return unsupported("dim must be at most 32768");
+  if (shape->rows > (kMaxThreads - 1024) / row_threads(shape->dim)) return unsupported("too many rows");
+  const int pad = (shape->dim + 15) / 16 * 16;
+  if ((shape->x_stride != 0 && shape->x_stride < shape->dim) || (shape->q_stride != 0 && shape->q_stride < pad))
+    return invalid("a row stride is smaller than its row");
+  if (shape->q_stride % 16 != 0) return invalid("q_stride must be a multiple of 16");
+  if (shape->rows > 0 && (!x || !q || !scales)) return invalid("x, q and scales must be non-NULL");
+  if (!aligned(x, esize(shape->dtype)) || !aligned(q, 16) || !aligned(scales, 4))
+    return invalid("x and scales must be aligned to their elements, q to 16 bytes");
+  if (shape->rows == 0) return GDR_OK;
+  gdr::QuantParams p = {};
+  p.rows = shape->rows; p.dim = shape->dim; p.pad = pad; p.x = x; p.q = q; p.scales = scales;
+  p.x_stride = shape->x_stride ? shape->x_stride : shape->dim;
+  p.q_stride = shape->q_stride ? shape->q_stride : pad;
+  return done(gdr::launch_quant_rows(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+}
+
+gdr_status gdr_matmul_i8(const gdr_matmul_i8_shape* shape, const int8_t* x, const float* x_scales, const int8_t* weight,
+                         const float* weight_scales, const float* bias, void* y, void* stream) {
+  if (!shape) return invalid("shape is NULL");
+  if (shape->dtype != GDR_BF16 && shape->dtype != GDR_F32) return unsupported("dtype must be GDR_BF16 or GDR_F32");
+  if (shape->M < 0 || shape->N < 1 || shape->K < 1) return invalid("M must not be negative, N and K positive");
+  if (shape->K > (1 << 17) - 1) return unsupported("K must be at most 2^17 - 1");
+  // row numbers plus a tile's fit an int, and a tile's rows lie within 2^31 bytes
+  if (shape->M > (1 << 30) || shape->N > (1 << 30)) return unsupported("M and N must be at most 2^30");
+  const int pad = (shape->K + 15) / 16 * 16;
+  const int64_t st[2] = {shape->x_stride, shape->w_stride};
+  for (int64_t s : st) {
+    if (s != 0 && s < shape->K) return invalid("a row stride is smaller than its row");
+    if (s % 16 != 0) return invalid("row strides must be multiples of 16");
+    if (s > (1 << 22)) return unsupported("a row stride is over 2^22");
+  }
+  if (!weight || !weight_scales || (shape->M > 0 && (!x || !x_scales || !y)))
+    return invalid("x, x_scales, weight, weight_scales and y must be non-NULL");
+  const void* f32[] = {x_scales, weight_scales, bias};
+  if (!aligned(x, 16) || !aligned(weight, 16)) return invalid("x and weight must be 16-byte aligned");
+  if (!all_aligned(f32, 4) || !aligned(y, esize(shape->dtype))) return invalid("device pointers must be aligned to their elements");
+  if ((shape->M / 128 + 1L) * (shape->N / 128 + 1L) > kMaxThreads / 512) return unsupported("too many rows times columns");
+  if (shape->M == 0) return GDR_OK;
+  gdr::I8Params p = {};
+  p.x = x; p.w = weight; p.xs = x_scales; p.ws = weight_scales; p.bias = bias; p.y = y;
+  p.x_stride = shape->x_stride ? shape->x_stride : pad;
+  p.w_stride = shape->w_stride ? shape->w_stride : pad;
+  p.M = shape->M; p.N = shape->N; p.K = shape->K;
+  return done(gdr::launch_i8_matmul(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

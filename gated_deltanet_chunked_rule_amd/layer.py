@@ -11,8 +11,14 @@ tensors; work is enqueued on the current stream of the tensors' device.
     Selective state space scan: prompts, one new token (inference).
 ``gdr_rms_norm_fwd`` / ``gdr_rms_norm_bwd``
     Root-mean-square norm with the residual's addition, a gate, an 8-bit output with scales.
-``causal_conv`` / ``rms_norm``
-    The convolution and the norm, differentiable through ``torch.autograd``.
+``gdr_linear_scan_fwd`` / ``gdr_linear_scan_bwd`` / ``gdr_linear_scan_step``
+    Gated linear recurrence of one decay per channel: prompts, gradient, one new token.
+``gdr_block_norm_fwd`` / ``gdr_block_norm_bwd``
+    The norm behind a block with its gate and scale, the residual's addition, and the norm before the next block.
+``gdr_quantize_rows`` / ``gdr_matmul_i8``
+    Rows in 8-bit integers with one scale each, and their product with such a weight (inference).
+``causal_conv`` / ``rms_norm`` / ``linear_scan`` / ``block_norm``
+    Differentiable through ``torch.autograd``.
 
 Operands called "strided" may be slices of a wider row, such as the parts of a
 fused projection's output.  ``cu_seqlens`` on the device is taken as it is (int32,
@@ -22,11 +28,11 @@ get zero rows.  ``slots`` name each row's state in the pool: a row whose slot is
 of range, or was named by an earlier row, is padding and gets a zero row.
 
 Where gradients are recorded, the entry points other than the ``_bwd`` ones refuse
-inputs that require one: ``causal_conv`` and ``rms_norm`` are the calls that give it.
-The ``_bwd`` ones return plain values.
+inputs that require one: ``causal_conv``, ``rms_norm``, ``linear_scan`` and
+``block_norm`` are the calls that give it.  The ``_bwd`` ones return plain values.
 
-``causal_conv`` and ``rms_norm`` can be captured with their backward, as any
-differentiable call of torch: on leaves that no eager graph alive was built from.
+These four can be captured with their backward, as any differentiable call of
+torch: on leaves that no eager graph alive was built from.
 """
 from __future__ import annotations
 
@@ -58,6 +64,24 @@ class _NormShape(ctypes.Structure):
                 ("g_inner", _i64)]
 
 
+class _LinearScanShape(ctypes.Structure):
+    _fields_ = [("B", _i32), ("T", _i32), ("D", _i32), ("num_seqs", _i32), ("dtype", ctypes.c_int), ("x_stride", _i64),
+                ("r_stride", _i64), ("i_stride", _i64)]
+
+
+class _BlockNormShape(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("dim", _i32), ("dtype", ctypes.c_int), ("eps", _f32), ("x_stride", _i64),
+                ("residual_stride", _i64), ("gate_stride", _i64)]
+
+
+class _QuantizeShape(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("dim", _i32), ("dtype", ctypes.c_int), ("x_stride", _i64), ("q_stride", _i64)]
+
+
+class _MatmulI8Shape(ctypes.Structure):
+    _fields_ = [("M", _i32), ("N", _i32), ("K", _i32), ("dtype", ctypes.c_int), ("x_stride", _i64), ("w_stride", _i64)]
+
+
 _SIGNATURES = {
     "gdr_causal_conv_fwd": (_ConvShape, 8),
     "gdr_causal_conv_bwd": (_ConvShape, 12, ctypes.c_size_t, 1),
@@ -70,6 +94,16 @@ _SIGNATURES = {
     "gdr_causal_conv_bwd_workspace_size": (_ConvShape,),
     "gdr_ssm_scan_fwd_workspace_size": (_SsmShape,),
     "gdr_rms_norm_bwd_workspace_size": (_NormShape,),
+    "gdr_linear_scan_fwd": (_LinearScanShape, 9, ctypes.c_size_t, 1),
+    "gdr_linear_scan_bwd": (_LinearScanShape, 14, ctypes.c_size_t, 1),
+    "gdr_linear_scan_step": (_LinearScanShape, 5, _i32, 3),
+    "gdr_block_norm_fwd": (_BlockNormShape, 9),
+    "gdr_block_norm_bwd": (_BlockNormShape, 15, ctypes.c_size_t, 1),
+    "gdr_quantize_rows": (_QuantizeShape, 4),
+    "gdr_matmul_i8": (_MatmulI8Shape, 7),
+    "gdr_linear_scan_fwd_workspace_size": (_LinearScanShape,),
+    "gdr_linear_scan_bwd_workspace_size": (_LinearScanShape,),
+    "gdr_block_norm_bwd_workspace_size": (_BlockNormShape,),
 }
 _entries = {}
 
@@ -514,3 +548,260 @@ class _NormFunction(torch.autograd.Function):
 def rms_norm(x, weight, residual: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, eps=1e-6):
     """High-level call: returns (y, h or None) with h = x + residual; differentiable."""
     return _NormFunction.apply(x, weight, residual, gate, eps)
+
+
+# ------------------------------------------------------- linear recurrence --
+def _linear_scan_args(x, r, i, A, cu_seqlens):
+    if x.dim() != 3:
+        raise GdrError("x must be [B, T, D]")
+    shape = tuple(x.shape)
+    B, T, D = shape
+    code, dev, ty = _code(x), x.get_device(), x.dtype
+    xp, xs = _rows_of(x, "x", shape, ty, dev, 2)
+    rp, rs = _rows_of(r, "r", shape, ty, dev, 2)
+    ip, ist = _rows_of(i, "i", shape, ty, dev, 2)
+    Ap = _dense(A, "A", (D,), torch.float32, dev)
+    cu, N = _offsets(cu_seqlens, B, T, x.device)
+    return _LinearScanShape(B, T, D, N, code, xs, rs, ist), (xp, rp, ip, Ap), cu, N, dev
+
+
+def gdr_linear_scan_fwd(x, r, i, A, initial_state=None, cu_seqlens=None, *, output_final_state=False, workspace=None):
+    """h = a h + sqrt(1 - a^2) sigmoid(i) x with a = exp(A sigmoid(r)), token by token: x, r, i [B, T, D] (strided), A [D]
+    fp32, initial_state [N, D] fp32.  Returns (y, final_state or None)."""
+    if _grad_enabled() and (x.requires_grad or r.requires_grad or i.requires_grad or A.requires_grad
+                            or (initial_state is not None and initial_state.requires_grad)):
+        _no_gradient("gdr_linear_scan_fwd", "linear_scan")
+    sh, ptrs, cu, N, dev = _linear_scan_args(x, r, i, A, cu_seqlens)
+    hp = _dense(initial_state, "initial_state", (N, sh.D), torch.float32, dev)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    ht = torch.empty((N, sh.D), device=dev, dtype=torch.float32) if output_final_state else None
+    ws = _workspace(workspace, _bytes("gdr_linear_scan_fwd_workspace_size", sh), dev)
+    _call(dev, _entry("gdr_linear_scan_fwd"), sh, *ptrs, hp, _ptr(cu), y.data_ptr(), _ptr(ht), ws.data_ptr(), ws.numel())
+    return y, ht
+
+
+def gdr_linear_scan_bwd(x, r, i, A, dy, initial_state=None, dht=None, cu_seqlens=None, *, workspace=None):
+    """Backward of gdr_linear_scan_fwd.  Returns (dx, dr, di, dA, dh0); dh0 is None without an initial state."""
+    sh, ptrs, cu, N, dev = _linear_scan_args(x, r, i, A, cu_seqlens)
+    hp = _dense(initial_state, "initial_state", (N, sh.D), torch.float32, dev)
+    dyp = _dense(dy, "dy", tuple(x.shape), x.dtype, dev)
+    dhp = _dense(dht, "dht", (N, sh.D), torch.float32, dev)
+    dx, dr, di = (torch.empty(x.shape, device=dev, dtype=x.dtype) for _ in range(3))
+    dA = torch.empty((sh.D,), device=dev, dtype=torch.float32)
+    dh0 = None if initial_state is None else torch.empty((N, sh.D), device=dev, dtype=torch.float32)
+    ws = _workspace(workspace, _bytes("gdr_linear_scan_bwd_workspace_size", sh), dev)
+    _call(dev, _entry("gdr_linear_scan_bwd"), sh, *ptrs, hp, _ptr(cu), dyp, dhp, dx.data_ptr(), dr.data_ptr(), di.data_ptr(),
+          dA.data_ptr(), _ptr(dh0), ws.data_ptr(), ws.numel())
+    return dx, dr, di, dA, dh0
+
+
+def gdr_linear_scan_step(x, r, i, A, state, *, slots=None):
+    """One new token per row: x, r, i [rows, D] (strided), A [D] fp32, state [slots, D] fp32, in place.  Returns y
+    [rows, D]."""
+    if x.dim() != 2:
+        raise GdrError("x must be [rows, D]")
+    if _grad_enabled() and (x.requires_grad or r.requires_grad or i.requires_grad or A.requires_grad or state.requires_grad):
+        _no_gradient("gdr_linear_scan_step")
+    shape = x.shape
+    rows, D = shape
+    code, dev, ty = _code(x), x.get_device(), x.dtype
+    xp, xs = _rows_of(x, "x", shape, ty, dev, 1)
+    rp, rs = _rows_of(r, "r", shape, ty, dev, 1)
+    ip, ist = _rows_of(i, "i", shape, ty, dev, 1)
+    Ap = _dense(A, "A", (D,), torch.float32, dev)
+    sp, n, lp = _pool(state, "state", (D,), torch.float32, dev, rows, slots)
+    y = torch.empty(rows, D, device=dev, dtype=ty) if xs else torch.empty_like(x)
+    if rows:
+        _call(dev, _entry("gdr_linear_scan_step"), _LinearScanShape(rows, 1, D, 0, code, xs, rs, ist), xp, rp, ip, Ap, sp, n, lp,
+              y.data_ptr())
+        _changed((state,))
+    return y
+
+
+class _LinearScanFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, i, A, initial_state, cu_seqlens, output_final_state):
+        cu, _ = _offsets(cu_seqlens, x.shape[0], x.shape[1], x.device) if x.dim() == 3 else (None, 0)
+        y, ht = gdr_linear_scan_fwd(x, r, i, A, initial_state, cu, output_final_state=output_final_state)
+        ctx.save_for_backward(x, r, i, A, initial_state, cu)
+        ctx.set_materialize_grads(False)
+        return y, ht
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dht):
+        x, r, i, A, h0, cu = ctx.saved_tensors
+        if dy is None and dht is None:
+            return (None,) * 7
+        dy = torch.zeros(x.shape, device=x.device, dtype=x.dtype) if dy is None else dy.contiguous()
+        dht = None if dht is None else dht.contiguous()
+        dx, dr, di, dA, dh0 = gdr_linear_scan_bwd(x, r, i, A, dy, h0, dht, cu)
+        return dx, dr, di, dA, dh0, None, None
+
+
+def linear_scan(x, r, i, A, initial_state=None, output_final_state=False, cu_seqlens=None):
+    """High-level call: returns (y, final_state or None); differentiable."""
+    return _LinearScanFunction.apply(x, r, i, A, initial_state, cu_seqlens, output_final_state)
+
+
+# ------------------------------------------------------- norms of a block --
+def _flat_rows(t, name, shape, dtype, index):
+    """(pointer, row stride) of [..., dim] rows that have one stride (0: dense)."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or index < 0:
+        _refuse(t, name, shape, dtype, index, False)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    st = t.stride()
+    if shape[-1] != 1 and st[-1] != 1:
+        raise GdrError(f"{name}: the values of a row must be contiguous")
+    stride = width = None
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, width = s, s * n
+        elif s != width:
+            raise GdrError(f"{name}: the leading dimensions must have one stride")
+        else:
+            width *= n
+    if stride is not None and stride < shape[-1]:
+        raise GdrError(f"{name}: rows overlap (expanded tensor): call .contiguous()")
+    return t.data_ptr(), stride or 0
+
+
+def _block_norm_args(x, post_weight, h, pre_weight, gate, scale, eps, h_name):
+    if x.dim() < 2:
+        raise GdrError("x must be [..., dim] with at least two dimensions")
+    shape = x.shape
+    dim = shape[-1]
+    rows = x.numel() // dim if dim else 0
+    code, dev, ty = _code(x), x.get_device(), x.dtype
+    xp, xs = _flat_rows(x, "x", shape, ty, dev)
+    hp, hs = _flat_rows(h, h_name, shape, ty, dev)
+    gp, gs = _flat_rows(gate, "gate", shape, ty, dev)
+    post = _dense(post_weight, "post_weight", (dim,), ty, dev)
+    pre = _dense(pre_weight, "pre_weight", (dim,), ty, dev)
+    sp = _dense(scale, "scale", (dim,), ty, dev)
+    return _BlockNormShape(rows, dim, code, eps, xs, hs, gs), (xp, hp, gp, post, pre, sp), dev
+
+
+def gdr_block_norm_fwd(x, post_weight, residual, pre_weight, gate=None, scale=None, *, eps=1e-6):
+    """h = residual + scale * rms_norm(x) * post_weight * silu(gate), y = rms_norm(h) * pre_weight, over the last dimension;
+    x, residual and gate [..., dim] (strided), weights and scale [dim].  Returns (y, h)."""
+    if _grad_enabled() and (x.requires_grad or post_weight.requires_grad or residual.requires_grad or pre_weight.requires_grad
+                            or (gate is not None and gate.requires_grad) or (scale is not None and scale.requires_grad)):
+        _no_gradient("gdr_block_norm_fwd", "block_norm")
+    sh, ptrs, dev = _block_norm_args(x, post_weight, residual, pre_weight, gate, scale, eps, "residual")
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    h = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    _call(dev, _entry("gdr_block_norm_fwd"), sh, *ptrs, y.data_ptr(), h.data_ptr())
+    return y, h
+
+
+def gdr_block_norm_bwd(x, post_weight, h, pre_weight, dy, gate=None, scale=None, dres=None, *, eps=1e-6, workspace=None):
+    """Backward of gdr_block_norm_fwd at its x and h; dres is the gradient of h from elsewhere.  Returns (dx, dh, dpost,
+    dpre, dgate, dscale); dh is the gradient of residual, dgate and dscale are None without a gate or scale."""
+    sh, ptrs, dev = _block_norm_args(x, post_weight, h, pre_weight, gate, scale, eps, "h")
+    shape, ty, dim = tuple(x.shape), x.dtype, sh.dim
+    dyp = _dense(dy, "dy", shape, ty, dev)
+    drp = _dense(dres, "dres", shape, ty, dev)
+    dx, dh = torch.empty(shape, device=dev, dtype=ty), torch.empty(shape, device=dev, dtype=ty)
+    dgate = None if gate is None else torch.empty(shape, device=dev, dtype=ty)
+    dpost, dpre = torch.empty((dim,), device=dev, dtype=ty), torch.empty((dim,), device=dev, dtype=ty)
+    dscale = None if scale is None else torch.empty((dim,), device=dev, dtype=ty)
+    ws = _workspace(workspace, _bytes("gdr_block_norm_bwd_workspace_size", sh), dev)
+    _call(dev, _entry("gdr_block_norm_bwd"), sh, *ptrs, dyp, drp, dx.data_ptr(), dh.data_ptr(), _ptr(dgate), dpost.data_ptr(),
+          dpre.data_ptr(), _ptr(dscale), ws.data_ptr(), ws.numel())
+    return dx, dh, dpost, dpre, dgate, dscale
+
+
+class _BlockNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, post_weight, residual, pre_weight, gate, scale, eps):
+        y, h = gdr_block_norm_fwd(x, post_weight, residual, pre_weight, gate, scale, eps=eps)
+        ctx.save_for_backward(x, post_weight, h, pre_weight, gate, scale)
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dres):
+        x, post, h, pre, gate, scale = ctx.saved_tensors
+        if dy is None and dres is None:
+            return (None,) * 7
+        dy = torch.zeros(x.shape, device=x.device, dtype=x.dtype) if dy is None else dy.contiguous()
+        dres = None if dres is None else dres.contiguous()
+        dx, dh, dpost, dpre, dgate, dscale = gdr_block_norm_bwd(x, post, h, pre, dy, gate, scale, dres, eps=ctx.eps)
+        return dx, dpost, dh, dpre, dgate, dscale, None
+
+
+def block_norm(x, post_weight, residual, pre_weight, gate: Optional[torch.Tensor] = None,
+               scale: Optional[torch.Tensor] = None, eps=1e-6):
+    """High-level call: returns (y, h); differentiable."""
+    return _BlockNormFunction.apply(x, post_weight, residual, pre_weight, gate, scale, eps)
+
+
+# ------------------------------------------------------ products in 8 bits --
+def gdr_quantize_rows(x):
+    """Rows of x [..., K] (strided) in 8-bit integers.  Returns (q, scales): q [..., K] int8, its rows at multiples of 16
+    bytes (a slice of a wider tensor where K is none), scales [...] fp32."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise GdrError("x must be [..., K] with K positive")
+    if _grad_enabled() and x.requires_grad:
+        _no_gradient("gdr_quantize_rows")
+    shape = x.shape
+    K = shape[-1]
+    code, dev = _code(x), x.get_device()
+    xp, xs = _flat_rows(x, "x", shape, x.dtype, dev)
+    pad = -(-K // 16) * 16
+    q = torch.empty((*shape[:-1], pad), device=dev, dtype=torch.int8)
+    scales = torch.empty(shape[:-1], device=dev, dtype=torch.float32)
+    _call(dev, _entry("gdr_quantize_rows"), _QuantizeShape(x.numel() // K, K, code, xs, pad), xp, q.data_ptr(), scales.data_ptr())
+    return (q if pad == K else q[..., :K]), scales
+
+
+def _i8_rows(t, name, shape, index):
+    """(pointer, row stride) of int8 rows at multiples of 16 bytes."""
+    ptr, stride = _flat_rows(t, name, shape, torch.int8, index)
+    K = shape[-1]
+    if K % 16 == 0:
+        return ptr, stride
+    pad = -(-K // 16) * 16
+    rows = t.numel() // K
+    if rows == 0:
+        return ptr, 0
+    if stride == 0 and rows > 1:
+        raise GdrError(f"{name}: rows of {K} values must be at multiples of 16 bytes (pad the rows and slice)")
+    stride = stride or pad
+    # the last row is read up to the end of its last 16 bytes
+    if t.storage_offset() + (rows - 1) * stride + pad > t.untyped_storage().nbytes():
+        raise GdrError(f"{name}: the last row's storage must reach to a multiple of 16 bytes")
+    return ptr, stride
+
+
+def gdr_matmul_i8(q, scales, weight, weight_scales, bias=None, *, dtype=torch.bfloat16):
+    """y[m, n] = (q[m] . weight[n]) scales[m] weight_scales[n] + bias[n]: q [..., K] and weight [N, K] int8 with rows at
+    multiples of 16 bytes, scales [...], weight_scales [N] and bias [N] fp32.  Returns y [..., N] of the dtype."""
+    if q.dim() < 1 or weight.dim() != 2:
+        raise GdrError("q must be [..., K] and weight [N, K]")
+    if _grad_enabled() and (scales.requires_grad or weight_scales.requires_grad or (bias is not None and bias.requires_grad)):
+        _no_gradient("gdr_matmul_i8")
+    shape = q.shape
+    N, K = weight.shape
+    if K < 1 or shape[-1] != K:
+        raise GdrError(f"shape mismatch: q is {tuple(shape)}, weight {tuple(weight.shape)}")
+    code = GDR_BF16 if dtype is torch.bfloat16 else GDR_F32 if dtype is torch.float32 else None
+    if code is None:
+        raise GdrError(f"unsupported dtype {dtype} (bfloat16 or float32)")
+    dev = q.get_device()
+    qp, qs = _i8_rows(q, "q", shape, dev)
+    wp, ws = _i8_rows(weight, "weight", weight.shape, dev)
+    sp = _dense(scales, "scales", shape[:-1], torch.float32, dev)
+    wsp = _dense(weight_scales, "weight_scales", (N,), torch.float32, dev)
+    bp = _dense(bias, "bias", (N,), torch.float32, dev)
+    y = torch.empty((*shape[:-1], N), device=dev, dtype=dtype)
+    _call(dev, _entry("gdr_matmul_i8"), _MatmulI8Shape(q.numel() // K, N, K, code, qs, ws), qp, sp, wp, wsp, bp, y.data_ptr())
+    return y

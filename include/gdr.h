@@ -373,6 +373,110 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const vo
                             const void* dy, const void* d_res, void* dh, void* dw, void* dgate, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* ---- gated linear recurrence -------------------------------------------------
+ *   e = sigmoid(r_t),  a = exp(A e),  b = sqrt(1 - a^2) sigmoid(i_t) x_t
+ *   h_t = a h_{t-1} + b,  y_t = h_t
+ * per channel; A <= 0 (a positive one gives NaN where a > 1).  States and sums
+ * are fp32; y is h rounded once. */
+typedef struct {
+  int32_t B, T;               /* as in gdr_shape */
+  int32_t D;                  /* channels, at most 2^30 */
+  int32_t num_seqs;           /* sequences in packed mode; ignored otherwise */
+  gdr_dtype dtype;            /* of x, r, i, y and their gradients */
+  int64_t x_stride, r_stride, i_stride;  /* elements between tokens (0: D) */
+} gdr_linear_scan_shape;
+
+/* Bytes of device workspace the forward needs (0 on invalid arguments). */
+size_t gdr_linear_scan_fwd_workspace_size(const gdr_linear_scan_shape* shape);
+
+/*   x, r, i                      [B, T, D], strided;  A [D] fp32
+ *   initial_state, final_state   [num_seqs or B, D] fp32, nullable
+ *   y                            [B, T, D] dense */
+gdr_status gdr_linear_scan_fwd(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
+                               const float* A, const float* initial_state, const int32_t* cu_seqlens, void* y,
+                               float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace the backward needs (0 on invalid arguments). */
+size_t gdr_linear_scan_bwd_workspace_size(const gdr_linear_scan_shape* shape);
+
+/* Gradients of <y, dy> + <final_state, dht>.  dy dense; dht nullable.  dx, dr,
+ * di [B, T, D] dense, in the call's dtype; dA [D] and dh0 [num_seqs or B, D]
+ * (nullable) fp32.  sqrt(1 - a^2) has no derivative where it is zero: that
+ * token adds nothing through it.  dA is added in a fixed order. */
+gdr_status gdr_linear_scan_bwd(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
+                               const float* A, const float* initial_state, const int32_t* cu_seqlens, const void* dy,
+                               const float* dht, void* dx, void* dr, void* di, float* dA, float* dh0, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* One new token per row (shape: B = rows, T = 1); state [num_slots, D] fp32, in
+ * place. */
+gdr_status gdr_linear_scan_step(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
+                                const float* A, float* state, int32_t num_slots, const int32_t* slots, void* y,
+                                void* stream);
+
+/* ---- norms around a block ----------------------------------------------------
+ *   p = x / rms(x) * post_weight (* gate sigmoid(gate)),  rms(v) = sqrt(mean(v^2) + eps)
+ *   h = residual + (scale *) p,  y = h / rms(h) * pre_weight
+ * over rows of dim values (dim <= 16384): the norm behind a block with its gate
+ * and scale, the residual's addition, and the norm before the next block.
+ * Statistics are fp32; y is made from the unrounded h. */
+typedef struct {
+  int64_t rows;
+  int32_t dim;
+  gdr_dtype dtype;            /* of all tensors and gradients */
+  float eps;                  /* >= 0 */
+  int64_t x_stride, residual_stride, gate_stride;  /* elements between rows (0: dim) */
+} gdr_block_norm_shape;
+
+/*   x, residual, gate           [rows, dim], strided; gate nullable
+ *   post_weight, pre_weight, scale  [dim]; scale nullable
+ *   y, h                        [rows, dim] dense; h may be residual itself where that is dense */
+gdr_status gdr_block_norm_fwd(const gdr_block_norm_shape* shape, const void* x, const void* residual, const void* gate,
+                              const void* post_weight, const void* pre_weight, const void* scale, void* y, void* h,
+                              void* stream);
+
+/* Bytes of device workspace gdr_block_norm_bwd needs (0 on invalid arguments). */
+size_t gdr_block_norm_bwd_workspace_size(const gdr_block_norm_shape* shape);
+
+/* Gradients of <y, dy> + <h, d_res> at x and h (the forward's h;
+ * residual_stride is its stride).  dy and d_res (nullable) dense; dx, dh (the
+ * gradient of residual) and dgate (with a gate) [rows, dim] dense; dpost, dpre
+ * and dscale (with a scale) [dim], added in a fixed order. */
+gdr_status gdr_block_norm_bwd(const gdr_block_norm_shape* shape, const void* x, const void* h, const void* gate,
+                              const void* post_weight, const void* pre_weight, const void* scale, const void* dy,
+                              const void* d_res, void* dx, void* dh, void* dgate, void* dpost, void* dpre,
+                              void* dscale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- products in 8-bit integers (inference) ----------------------------------
+ * Rows quantised with one scale each:
+ *   scale = max(max |x|, 2^-100) / 127,  q = the fp32 quotient x / scale rounded to an integer, ties to even
+ * A row with an infinity or a NaN gets the scale NaN and zeros. */
+typedef struct {
+  int64_t rows;
+  int32_t dim;                /* at most 32768 */
+  gdr_dtype dtype;            /* of x */
+  int64_t x_stride;           /* elements between rows (0: dim) */
+  int64_t q_stride;           /* bytes between rows of q, a multiple of 16 (0: dim rounded up to one) */
+} gdr_quantize_shape;
+
+/* x [rows, dim] strided; q [rows, dim] int8, 16-byte aligned; the bytes from
+ * dim up to the next multiple of 16 are set to zero.  scales [rows] fp32. */
+gdr_status gdr_quantize_rows(const gdr_quantize_shape* shape, const void* x, int8_t* q, float* scales, void* stream);
+
+/* y[m, n] = (sum over k of x[m, k] weight[n, k]) x_scales[m] weight_scales[n] + bias[n]
+ * x [M, K] and weight [N, K] int8, the sum exact; scales and bias (nullable)
+ * fp32; y [M, N] dense, in dtype, rounded once from fp32. */
+typedef struct {
+  int32_t M, N;
+  int32_t K;                  /* at most 2^17 - 1 */
+  gdr_dtype dtype;            /* of y */
+  int64_t x_stride, w_stride; /* bytes between rows, multiples of 16 (0: K rounded up to one), at most 2^22.  The rows'
+                               * starts are 16-byte aligned, and the last row's last 16-byte piece is readable whole
+                               * (what lies behind K in it does not matter). */
+} gdr_matmul_i8_shape;
+gdr_status gdr_matmul_i8(const gdr_matmul_i8_shape* shape, const int8_t* x, const float* x_scales, const int8_t* weight,
+                         const float* weight_scales, const float* bias, void* y, void* stream);
+
 /* ---- kernel timing (diagnostics) ------------------------------------------
  * When enabled, every kernel the library enqueues is bracketed by a pair of
  * HIP events recorded on the launch stream.  gdr_timing_collect() waits for
