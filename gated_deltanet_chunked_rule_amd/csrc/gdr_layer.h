@@ -82,6 +82,9 @@ struct LinParams {               // linear scan; the step: Ttot rows, ht the poo
   void *y, *dx, *dr, *di;
   float *ht, *dh0, *dA;
   float *P, *S, *Q, *part;       // [tiles][D] each
+  uint64_t* words;               // [tiles][D]: (P, S) of the tiles that are there, in one pass
+  uint32_t* ends;                // [groups][D]: states at the ends of groups of tiles
+  int* ticket;
   const int32_t* slots;
   long x_stride, r_stride, i_stride;
   int D, tiles, cols, num_slots; // tiles of tokens, columns of channels
@@ -134,9 +137,11 @@ hipError_t launch_ssm_scan(DType dt, const SsmParams& p, hipStream_t st);
 hipError_t launch_norm_fwd(DType dt, bool quant, const NormParams& p, hipStream_t st);
 hipError_t launch_norm_bwd(DType dt, const NormParams& p, hipStream_t st);
 int norm_bwd_blocks(long rows, int dim);
-int lin_tiles(int tokens);                  // tiles of the token axis
+int lin_tiles(DType dt, int tokens);        // tiles of the token axis
+int lin_bwd_tiles(int tokens);
 int lin_cols(int D);
-hipError_t launch_lin_fwd(DType dt, const LinParams& p, hipStream_t st);
+size_t lin_fwd_bytes(DType dt, int tokens, int D);
+hipError_t launch_lin_fwd(DType dt, const LinParams& p, void* workspace, hipStream_t st);
 hipError_t launch_lin_bwd(DType dt, const LinParams& p, hipStream_t st);
 hipError_t launch_lin_step(DType dt, const LinParams& p, hipStream_t st);
 hipError_t launch_block_norm_fwd(DType dt, const BlockNormParams& p, hipStream_t st);
@@ -209,6 +214,31 @@ template <> struct VecIO<float, 4> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = __builtin_bit_cast(uint32_t, f[i]);
     return r;
+  }
+};
+typedef uint32_t u32x2_u4 __attribute__((ext_vector_type(2), aligned(4)));
+template <> struct VecIO<float, 2> {
+  typedef u32x2_u4 raw;
+  static __device__ __forceinline__ void up(raw r, float (&f)[2]) {
+    const uint32_t u = r[0], v = r[1];
+    f[0] = __builtin_bit_cast(float, u);
+    f[1] = __builtin_bit_cast(float, v);
+  }
+  static __device__ __forceinline__ raw down(const float (&f)[2]) {
+    return raw{__builtin_bit_cast(uint32_t, f[0]), __builtin_bit_cast(uint32_t, f[1])};
+  }
+};
+typedef uint32_t u32x1_u2 __attribute__((ext_vector_type(1), aligned(2)));
+template <> struct VecIO<bf16, 2> {
+  typedef u32x1_u2 raw;
+  static __device__ __forceinline__ void up(raw r, float (&f)[2]) {
+    const uint32_t u = r[0];
+    f[0] = __builtin_bit_cast(float, u << 16);
+    f[1] = __builtin_bit_cast(float, u & 0xffff0000u);
+  }
+  static __device__ __forceinline__ raw down(const float (&f)[2]) {
+    const bf16x2 b = {static_cast<bf16>(f[0]), static_cast<bf16>(f[1])};
+    return raw{__builtin_bit_cast(uint32_t, b)};
   }
 };
 struct raw_f8 { u32x4_u4 a, b; };
@@ -321,10 +351,11 @@ struct SeqFinder {
 // What happens at the `count` (below 32) tokens from t0 on, as bits: first: the
 // token starts a run that does not go on from the tokens before t0; last: it
 // ends its sequence; gap: it belongs to none, or lies behind the last token.
-// A token that starts or ends a run finds a sequence, whatever the table (where
-// offsets decrease, a run's tokens may find different ones).
+// seq[k] is the sequence of a token that starts or ends one, in [0, N)
+// whatever the table (where offsets decrease, a run's tokens may find
+// different ones, or none: such a token ends nothing).
 struct TokenRuns { uint32_t first, last, gap; };
-__host__ __device__ __forceinline__ TokenRuns token_runs(const SeqFinder& sf, int t0, int count) {
+__host__ __device__ __forceinline__ TokenRuns token_runs(const SeqFinder& sf, int t0, int count, int* seq) {
   TokenRuns m = {0, 0, 0};
   const int t1 = t0 + count < sf.Ttot ? t0 + count : sf.Ttot;
   for (int t = t0; t < t1;) {
@@ -333,9 +364,16 @@ __host__ __device__ __forceinline__ TokenRuns token_runs(const SeqFinder& sf, in
     if (n < 0) {
       m.gap |= ((1u << (stop - t)) - 1u) << (t - t0);
     } else {
-      if (!SeqFinder::goes_on(t, t0, start)) m.first |= 1u << (t - t0);
       int s, e;
-      if (end <= t1 && sf.find(end - 1, s, e) >= 0) m.last |= 1u << (end - 1 - t0);
+      const int ends = end > t1 ? -1 : end == t + 1 ? n : sf.find(end - 1, s, e);
+      if (!SeqFinder::goes_on(t, t0, start)) {
+        m.first |= 1u << (t - t0);
+        seq[t - t0] = n;
+      }
+      if (ends >= 0) {
+        m.last |= 1u << (end - 1 - t0);
+        seq[end - 1 - t0] = ends;
+      }
     }
     t = stop;
   }

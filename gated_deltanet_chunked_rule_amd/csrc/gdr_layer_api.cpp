@@ -164,7 +164,7 @@ gdr_status lin_check(const gdr_linear_scan_shape* sh, bool packed) {
   const int64_t st[3] = {sh->x_stride, sh->r_stride, sh->i_stride};
   for (int64_t s : st)
     if (s != 0 && s < sh->D) return invalid("a token stride is smaller than its row");
-  if ((long)gdr::lin_tiles(sh->B * sh->T) * gdr::lin_cols(sh->D) > kMaxThreads / 512) return unsupported("too many tokens times channels");
+  if ((long)gdr::lin_bwd_tiles(sh->B * sh->T) * gdr::lin_cols(sh->D) > kMaxThreads / 512) return unsupported("too many tokens times channels");
   return GDR_OK;
 }
 gdr::LinParams lin_params(const gdr_linear_scan_shape* sh, const void* x, const void* r, const void* i, const float* A,
@@ -176,12 +176,12 @@ gdr::LinParams lin_params(const gdr_linear_scan_shape* sh, const void* x, const 
   p.r_stride = sh->r_stride ? sh->r_stride : sh->D;
   p.i_stride = sh->i_stride ? sh->i_stride : sh->D;
   p.D = sh->D;
-  p.tiles = gdr::lin_tiles(sh->B * sh->T);
+  p.tiles = gdr::lin_tiles(dtype_of(sh->dtype), sh->B * sh->T);
   p.cols = gdr::lin_cols(sh->D);
   return p;
 }
 // One row of D fp32 values for each tile of tokens.
-size_t lin_rows_bytes(const gdr_linear_scan_shape* sh) { return align_up((size_t)gdr::lin_tiles(sh->B * sh->T) * sh->D * 4); }
+size_t lin_rows_bytes(const gdr_linear_scan_shape* sh) { return align_up((size_t)gdr::lin_bwd_tiles(sh->B * sh->T) * sh->D * 4); }
 
 // ------------------------------------------------------ norms of a block --
 gdr_status block_norm_check(const gdr_block_norm_shape* sh) {
@@ -398,7 +398,7 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const vo
 
 size_t gdr_linear_scan_fwd_workspace_size(const gdr_linear_scan_shape* shape) {
   if (lin_check(shape, false) != GDR_OK) return 0;
-  return 2 * lin_rows_bytes(shape);
+  return align_up(gdr::lin_fwd_bytes(dtype_of(shape->dtype), shape->B * shape->T, shape->D));
 }
 
 gdr_status gdr_linear_scan_fwd(const gdr_linear_scan_shape* shape, const void* x, const void* r, const void* i,
@@ -411,14 +411,12 @@ gdr_status gdr_linear_scan_fwd(const gdr_linear_scan_shape* shape, const void* x
   if (!all_aligned(ptrs, esize(shape->dtype)) || !all_aligned(f32, 4)) return invalid("device pointers must be aligned to their elements");
   if (in_place(y, x) || in_place(y, r) || in_place(y, i) || in_place(final_state, initial_state))
     return invalid("y and final_state must not overlap x, r, i and initial_state");
-  if (!workspace || workspace_bytes < 2 * lin_rows_bytes(shape))
+  if (!workspace || workspace_bytes < gdr_linear_scan_fwd_workspace_size(shape))
     return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_linear_scan_fwd_workspace_size)");
   if (!aligned(workspace, 16)) return invalid("workspace must be 16-byte aligned");
   gdr::LinParams p = lin_params(shape, x, r, i, A, initial_state, cu_seqlens);
   p.y = y; p.ht = final_state;
-  p.P = static_cast<float*>(workspace);
-  p.S = reinterpret_cast<float*>(static_cast<char*>(workspace) + lin_rows_bytes(shape));
-  return done(gdr::launch_lin_fwd(dtype_of(shape->dtype), p, static_cast<hipStream_t>(stream)));
+  return done(gdr::launch_lin_fwd(dtype_of(shape->dtype), p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 size_t gdr_linear_scan_bwd_workspace_size(const gdr_linear_scan_shape* shape) {
@@ -444,6 +442,7 @@ gdr_status gdr_linear_scan_bwd(const gdr_linear_scan_shape* shape, const void* x
     return set_error(GDR_ERR_WORKSPACE, "workspace too small (see gdr_linear_scan_bwd_workspace_size)");
   if (!aligned(workspace, 16)) return invalid("workspace must be 16-byte aligned");
   gdr::LinParams p = lin_params(shape, x, r, i, A, initial_state, cu_seqlens);
+  p.tiles = gdr::lin_bwd_tiles(shape->B * shape->T);
   p.dy = dy; p.dht = dht; p.dx = dx; p.dr = dr; p.di = di; p.dA = dA; p.dh0 = dh0;
   float** rows[] = {&p.P, &p.S, &p.Q, &p.part};
   for (int k = 0; k < 4; ++k) *rows[k] = reinterpret_cast<float*>(static_cast<char*>(workspace) + k * lin_rows_bytes(shape));

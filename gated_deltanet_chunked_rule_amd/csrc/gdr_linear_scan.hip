@@ -16,219 +16,400 @@
 namespace gdr {
 
 constexpr float kFresh = -1.f;   // in the place of a product of decays: the end does not depend on the start
-constexpr int kLinVec = 4;       // channels a lane
+constexpr int kLinVec = 2;       // channels a lane
 constexpr int kLinCh = 64 * kLinVec;
+typedef float lin_v __attribute__((ext_vector_type(kLinVec)));
 
-// sqrt(1 - a^2) with a = exp(s), s = s2 ln 2: 1 - a^2 = -expm1(2 s).  Near zero
-// the difference would lose all bits: below 2 |s| = 1/4 the Taylor series up to
-// z^6 / 720 (the next term is 4.8e-8 of the first); above it 1 - a^2 >= 0.22.
-// A positive s gives a NaN.
-__device__ __forceinline__ float lin_factor(float s2, float a) {
+// 1 - a^2 with a = exp(s), s = s2 ln 2: -expm1(2 s).  Near zero the difference
+// would lose all bits: below 2 |s| = 1/4 the Taylor series up to z^6 / 720 (the
+// next term is 4.8e-8 of the first); above it 1 - a^2 >= 0.22.  A positive s
+// gives a negative value, and a NaN as its root.
+__device__ __forceinline__ float lin_factor2(float s2, float a) {
   const float z = s2 * 1.3862943611198906f;
   float q = fmaf(z, 1.f / 720.f, 1.f / 120.f);
   q = fmaf(q, z, 1.f / 24.f);
   q = fmaf(q, z, 1.f / 6.f);
   q = fmaf(q, z, 0.5f);
   q = fmaf(q, z, 1.f);
-  return __builtin_amdgcn_sqrtf(z > -0.25f ? -z * q : fmaf(-a, a, 1.f));
+  return z > -0.25f ? -z * q : fmaf(-a, a, 1.f);
 }
 // a and b of one value; A2 = A log2(e)
 __device__ __forceinline__ void lin_gates(float x, float r, float i, float A2, float& a, float& b) {
   const float s2 = A2 * sigmoid_f(r);
   a = __builtin_amdgcn_exp2f(s2);
-  b = lin_factor(s2, a) * sigmoid_f(i) * x;
+  b = __builtin_amdgcn_sqrtf(lin_factor2(s2, a)) * sigmoid_f(i) * x;
 }
 // sigmoid(x) and 1 - sigmoid(x), both to a few ulps on either side of zero
+// (below -16 the latter is one; e^-x overflows from -88 on, and 1 / (1 + it) is
+// zero then).
 __device__ __forceinline__ void sigmoid_both(float x, float& e, float& ne) {
-  const float t = exp_f(-fabsf(x)), big = __builtin_amdgcn_rcpf(1.f + t), small = t * big;
-  e = x >= 0.f ? big : small;
-  ne = x >= 0.f ? small : big;
+  const float t = exp_f(-x);
+  e = __builtin_amdgcn_rcpf(1.f + t);
+  ne = x < -16.f ? 1.f : t * e;
 }
 
-// The runs of a wave's TT tokens, in scalar registers.
+// The runs of a wave's TT tokens, in scalar registers; seq: the wave's place in LDS.
 template <int TT>
-__device__ __forceinline__ TokenRuns lin_runs(const SeqFinder& sf, int t0) {
-  TokenRuns m = token_runs(sf, t0, TT);
+__device__ __forceinline__ TokenRuns lin_runs(const SeqFinder& sf, int t0, int* seq) {
+  TokenRuns m = token_runs(sf, t0, TT, seq);
   m.first = __builtin_amdgcn_readfirstlane(m.first);
   m.last = __builtin_amdgcn_readfirstlane(m.last);
   m.gap = __builtin_amdgcn_readfirstlane(m.gap);
   return m;
 }
-__device__ __forceinline__ int lin_seq_at(const SeqFinder& sf, int t) {
-  int start, end;
-  return __builtin_amdgcn_readfirstlane(sf.find(t, start, end));
+__device__ __forceinline__ int lin_seq(const int* seq, int k) { return __builtin_amdgcn_readfirstlane(seq[k]); }
+// The same pointer, to global memory, in scalar registers (it is equal across the wave).
+#define GDR_GLOBAL __attribute__((address_space(1)))
+__device__ __forceinline__ GDR_GLOBAL char* lin_uniform(const void* p) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return (GDR_GLOBAL char*)(uintptr_t)((uint64_t)hi << 32 | lo);
 }
 
-// TT tokens of a strided operand from token t0 on, four channels a lane; rows
-// behind the last are the last one.
-template <typename T, int TT>
-__device__ __forceinline__ void lin_load(const void* base, long stride, int t0, int Ttot, int d, int nd, bool full,
+// Channels of a lane: four from lin_base on.  A column's last lanes are moved
+// back onto the last four channels, which they share with the lane before:
+// they compute and store the same values, and no access needs a mask.  Fewer
+// than four channels (NARROW) are all held by every lane.
+__device__ __forceinline__ int lin_base(int first, int D) { return max(0, min(first, D - kLinVec)); }
+template <bool NARROW, typename T>
+__device__ __forceinline__ typename VecIO<T, kLinVec>::raw lin_read(const void* row, int d, int D) {
+  GDR_GLOBAL char* at = lin_uniform(row) + (uint32_t)d * (uint32_t)sizeof(T);   // a scalar row address and one offset in a register
+  if constexpr (NARROW) return vec_raw<T, kLinVec>((const T*)at, D);
+  else return *(const GDR_GLOBAL typename VecIO<T, kLinVec>::raw*)at;
+}
+template <bool NARROW, typename T>
+__device__ __forceinline__ void lin_write(void* row, int d, int D, const float (&f)[kLinVec]) {
+  GDR_GLOBAL char* at = lin_uniform(row) + (uint32_t)d * (uint32_t)sizeof(T);
+  if constexpr (NARROW) vec_store<T, kLinVec>((T*)at, D, f);
+  else *(GDR_GLOBAL typename VecIO<T, kLinVec>::raw*)at = VecIO<T, kLinVec>::down(f);
+}
+template <bool NARROW>
+__device__ __forceinline__ void lin_floats(const float* row, int d, int D, float (&f)[kLinVec]) {
+  VecIO<float, kLinVec>::up(lin_read<NARROW, float>(row, d, D), f);
+}
+
+// TT tokens of an operand from token t0 on; tokens behind the last are the last one.
+template <bool NARROW, typename T, int TT>
+__device__ __forceinline__ void lin_load(const void* base, long stride, int t0, int Ttot, int d, int D,
                                          typename VecIO<T, kLinVec>::raw (&out)[TT]) {
-  const T* p = static_cast<const T*>(base) + d;
-  if (full) {
 #pragma unroll
-    for (int k = 0; k < TT; ++k)
-      out[k] = *reinterpret_cast<const typename VecIO<T, kLinVec>::raw*>(p + (long)min(t0 + k, Ttot - 1) * stride);
-  } else {
-#pragma unroll
-    for (int k = 0; k < TT; ++k) out[k] = vec_raw<T, kLinVec>(p + (long)min(t0 + k, Ttot - 1) * stride, max(0, nd));
-  }
+  for (int k = 0; k < TT; ++k)
+    out[k] = lin_read<NARROW, T>(static_cast<const char*>(base) + (long)min(t0 + k, Ttot - 1) * stride * (long)sizeof(T), d, D);
 }
 
 // Sequences without a token: their final state is their initial state (the
 // gradient of that one the gradient of the final state).  Each tile of tokens
 // takes its share of the sequences.
 __device__ __forceinline__ void lin_empty(const SeqFinder& sf, const float* from, float* to, int tile, int tiles, int d, int D) {
+  if (!to || d >= D) return;
   for (int n = tile; n < sf.N; n += tiles)
-    if (sf.at(n + 1) <= sf.at(n) && d < D) to[(long)n * D + d] = from ? from[(long)n * D + d] : 0.f;
+    if (sf.at(n + 1) <= sf.at(n)) to[(long)n * D + d] = from ? from[(long)n * D + d] : 0.f;
 }
+// The channel that value c of a column's lanes stands for.
+__device__ __forceinline__ int lin_channel(int col, int c, int D) { return lin_base(col * kLinCh + (c & ~(kLinVec - 1)), D) + (c & (kLinVec - 1)); }
 
-struct LinAgg { f32x4 p[8][64], s[8][64]; };
+// What the waves of a tile do to the state.
+struct LinAgg {
+  lin_v p[8][64], s[8][64];
+  int seq[8][32];   // of the waves' tokens that start or end a sequence
+};
 
-// OUT false: what each tile does to the state (P, S).  OUT true: the states
-// from the tiles' entry states, and the outputs.
-template <typename T, int NW, int TT, bool OUT>
-__global__ __launch_bounds__(64 * NW) void k_lin_fwd(LinParams p) {
-  constexpr int TOK = NW * TT;
-  __shared__ int32_t cu_lds[kCuLds];
-  __shared__ LinAgg agg;
-  const int tile = blockIdx.x / p.cols, col = blockIdx.x - tile * p.cols;
-  const int w = wave_id(), l = lane_id(), t0 = tile * TOK + w * TT;
-  const int d = col * kLinCh + l * kLinVec, nd = min(kLinVec, p.D - d);
-  const bool full = (col + 1) * kLinCh <= p.D;
-  typename VecIO<T, kLinVec>::raw xr[TT], rr[TT], ir[TT];
-  if (t0 < p.s.Ttot) {
-    lin_load<T, TT>(p.r, p.r_stride, t0, p.s.Ttot, d, nd, full, rr);
-    lin_load<T, TT>(p.i, p.i_stride, t0, p.s.Ttot, d, nd, full, ir);
-    lin_load<T, TT>(p.x, p.x_stride, t0, p.s.Ttot, d, nd, full, xr);
+// a and b of a lane's tokens.
+template <typename T, int TT>
+__device__ __forceinline__ void lin_values(const float (&A2)[kLinVec], const typename VecIO<T, kLinVec>::raw (&xr)[TT],
+                                           const typename VecIO<T, kLinVec>::raw (&rr)[TT], const typename VecIO<T, kLinVec>::raw (&ir)[TT],
+                                           float (&a)[TT][kLinVec], float (&b)[TT][kLinVec]) {
+#pragma unroll
+  for (int k = 0; k < TT; ++k) {
+    float x[kLinVec], r[kLinVec], i[kLinVec];
+    VecIO<T, kLinVec>::up(rr[k], r);
+    VecIO<T, kLinVec>::up(ir[k], i);
+    VecIO<T, kLinVec>::up(xr[k], x);
+#pragma unroll
+    for (int c = 0; c < kLinVec; ++c) lin_gates(x[c], r[c], i[c], A2[c], a[k][c], b[k][c]);
   }
-  float A2[kLinVec], h[kLinVec];
-  vec_load<float, kLinVec>(p.A + d, max(0, nd), A2);
-  if (OUT && tile > 0) vec_load<float, kLinVec>(p.S + (long)(tile - 1) * p.D + d, max(0, nd), h);
-  else
+}
+// The initial state of the sequence that starts at the wave's token k.
+template <bool NARROW>
+__device__ __forceinline__ void lin_initial(const LinParams& p, const int* seq, int k, int d, float (&h)[kLinVec]) {
+  if (p.h0) {
+    lin_floats<NARROW>(p.h0 + (long)lin_seq(seq, k) * p.D, d, p.D, h);
+  } else {
 #pragma unroll
     for (int c = 0; c < kLinVec; ++c) h[c] = 0.f;
-#pragma unroll
-  for (int c = 0; c < kLinVec; ++c) A2[c] *= 1.4426950408889634f;
-  const SeqFinder sf = seq_finder(p.s, cu_lds);
-  const TokenRuns run = lin_runs<TT>(sf, t0);
-  float a[TT][kLinVec], b[TT][kLinVec];
-  f32x4 P = f32x4{1.f, 1.f, 1.f, 1.f}, S = zero4();
-  if (t0 < p.s.Ttot) {
+  }
+}
+// The state behind each token from the state h before them; then(k, h) takes it.
+template <bool NARROW, int TT, typename F>
+__device__ __forceinline__ void lin_states(const LinParams& p, const int* seq, const TokenRuns& run, int t0, int d,
+                                           const float (&a)[TT][kLinVec], const float (&b)[TT][kLinVec], float (&h)[kLinVec], F then) {
+  if ((run.first | run.gap | run.last) == 0) {
 #pragma unroll
     for (int k = 0; k < TT; ++k) {
-      float x[kLinVec], r[kLinVec], i[kLinVec];
-      VecIO<T, kLinVec>::up(rr[k], r);
-      VecIO<T, kLinVec>::up(ir[k], i);
-      VecIO<T, kLinVec>::up(xr[k], x);
 #pragma unroll
-      for (int c = 0; c < kLinVec; ++c) lin_gates(x[c], r[c], i[c], A2[c], a[k][c], b[k][c]);
-      if (run.first >> k & 1) {   // h_t = a h_0 + b
-        if (p.h0) {
-          float h0[kLinVec];
-          vec_load<float, kLinVec>(p.h0 + (long)lin_seq_at(sf, t0 + k) * p.D + d, max(0, nd), h0);
-#pragma unroll
-          for (int c = 0; c < kLinVec; ++c) b[k][c] = fmaf(a[k][c], h0[c], b[k][c]);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kLinVec; ++c) {
-        P[c] *= a[k][c];
-        S[c] = run.gap >> k & 1 ? 0.f : run.first >> k & 1 ? b[k][c] : fmaf(a[k][c], S[c], b[k][c]);
-      }
-    }
-  }
-  if (run.first | run.gap) P = f32x4{kFresh, kFresh, kFresh, kFresh};
-  agg.p[w][l] = P;
-  agg.s[w][l] = S;
-  __syncthreads();
-  if constexpr (!OUT) {
-    for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) {
-      if (col * kLinCh + c >= p.D) break;
-      float q = 1.f, s = 0.f;
-#pragma unroll
-      for (int u = 0; u < NW; ++u) {
-        const float pu = agg.p[u][c / 4][c % 4], su = agg.s[u][c / 4][c % 4];
-        s = pu == kFresh ? su : fmaf(pu, s, su);
-        q = pu == kFresh || q == kFresh ? kFresh : q * pu;
-      }
-      p.P[(long)tile * p.D + col * kLinCh + c] = q;
-      p.S[(long)tile * p.D + col * kLinCh + c] = s;
+      for (int c = 0; c < kLinVec; ++c) h[c] = fmaf(a[k][c], h[c], b[k][c]);
+      then(k, h);
     }
     return;
   }
-  for (int u = 0; u < w; ++u) {
-    const f32x4 pu = agg.p[u][l], su = agg.s[u][l];
-#pragma unroll
-    for (int c = 0; c < kLinVec; ++c) h[c] = pu[c] == kFresh ? su[c] : fmaf(pu[c], h[c], su[c]);
-  }
-  T* y = static_cast<T*>(p.y) + d;
 #pragma unroll
   for (int k = 0; k < TT; ++k) {
-    if (t0 + k >= p.s.Ttot) break;
+    if (run.first >> k & 1) lin_initial<NARROW>(p, seq, k, d, h);
 #pragma unroll
-    for (int c = 0; c < kLinVec; ++c) h[c] = run.gap >> k & 1 ? 0.f : run.first >> k & 1 ? b[k][c] : fmaf(a[k][c], h[c], b[k][c]);
-    if (nd > 0) vec_store<T, kLinVec>(y + (long)(t0 + k) * p.D, nd, h);
-    if (p.ht && (run.last >> k & 1)) {
-      const int n = lin_seq_at(sf, t0 + k);
-      if (nd > 0) vec_store<float, kLinVec>(p.ht + (long)n * p.D + d, nd, h);
-    }
+    for (int c = 0; c < kLinVec; ++c) h[c] = run.gap >> k & 1 ? 0.f : fmaf(a[k][c], h[c], b[k][c]);
+    if (t0 + k < p.s.Ttot) then(k, h);
   }
-  if (p.ht) {
-    for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) lin_empty(sf, p.h0, p.ht, tile, p.tiles, col * kLinCh + c, p.D);
+}
+// What the tokens do to the state: (P, S).
+template <bool NARROW, int TT>
+__device__ __forceinline__ void lin_effect(const LinParams& p, const int* seq, const TokenRuns& run, int t0, int d,
+                                           const float (&a)[TT][kLinVec], const float (&b)[TT][kLinVec], lin_v& P, lin_v& S) {
+  float h[kLinVec] = {};
+  lin_states<NARROW, TT>(p, seq, run, t0, d, a, b, h, [](int, const float (&)[kLinVec]) {});
+#pragma unroll
+  for (int c = 0; c < kLinVec; ++c) {
+    S[c] = h[c];
+    P[c] = 1.f;
+#pragma unroll
+    for (int k = 0; k < TT; ++k) P[c] *= a[k][c];
+    if (run.first | run.gap) P[c] = kFresh;
+  }
+}
+// The outputs of a lane's tokens from the state h before them.
+template <bool NARROW, typename T, int TT>
+__device__ __forceinline__ void lin_leave(const LinParams& p, const int* seq, const TokenRuns& run, int t0, int d,
+                                          const float (&a)[TT][kLinVec], const float (&b)[TT][kLinVec], float (&h)[kLinVec]) {
+  lin_states<NARROW, TT>(p, seq, run, t0, d, a, b, h, [&](int k, const float (&h)[kLinVec]) {
+    lin_write<NARROW, T>(static_cast<char*>(p.y) + (long)(t0 + k) * p.D * (long)sizeof(T), d, p.D, h);
+    if (p.ht && (run.last >> k & 1)) lin_write<NARROW, float>(p.ht + (long)lin_seq(seq, k) * p.D, d, p.D, h);
+  });
+}
+// One run behind another.
+__device__ __forceinline__ void lin_join(float& P, float& S, float p2, float s2) {
+  S = p2 == kFresh ? s2 : fmaf(p2, S, s2);
+  P = p2 == kFresh || P == kFresh ? kFresh : P * p2;
+}
+__device__ __forceinline__ float lin_after(float h, float P, float S) { return P == kFresh ? S : fmaf(P, h, S); }
+
+// What tiles leave for those behind them: a word of (P, S) for each tile and
+// channel, and the state at the end of each group of kLinGroup tiles.  The
+// words are written and read whole, past the caches that the XCDs do not
+// share, so that a word that is there needs no flag and no order with others;
+// kLinEmpty stands in those that are not there yet (never in one that is: a
+// NaN is written as kLinNan).
+constexpr int kLinGroup = 16;
+constexpr int kLinLine = 32;   // between the counters of two columns, so that they share no cache line
+constexpr uint32_t kLinEmpty = 0xffffffffu, kLinNan = 0x7fc00000u;
+// How often a wait looks.  Every wait ends long before that, as the tiles are
+// handed out in order and a tile leaves its own word before it waits for
+// those before it.  Only if another call clears the words meanwhile (two
+// calls that share a workspace) is it reached: the state is NaN then.
+constexpr int kLinLooks = 1 << 18;
+__device__ __forceinline__ uint32_t lin_bits(float x) { return x != x ? kLinNan : __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ void lin_put(uint64_t* at, float P, float S) {
+  __hip_atomic_store(at, (uint64_t)lin_bits(S) << 32 | lin_bits(P), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t lin_get(const char* row, uint32_t off) {
+  return __hip_atomic_load((const GDR_GLOBAL uint64_t*)(lin_uniform(row) + off), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ __launch_bounds__(256) void k_lin_clear(LinParams p) {
+  const long n = (long)p.tiles * p.D, words = n * 2 + (long)(p.tiles / kLinGroup + 1) * p.D;   // of 32 bits
+  uint32_t* w = reinterpret_cast<uint32_t*>(p.words);
+  for (long i = ((long)blockIdx.x * 256 + threadIdx.x) * 4; i < words; i += (long)gridDim.x * 1024) {
+    if (i + 4 <= words) *reinterpret_cast<u32x4_u4*>(w + i) = u32x4_u4{kLinEmpty, kLinEmpty, kLinEmpty, kLinEmpty};
+    else
+      for (long j = i; j < words; ++j) w[j] = kLinEmpty;
+  }
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.cols; i += 256) p.ticket[i * kLinLine] = 0;
+}
+
+// One pass: persistent workgroups take the tiles of a column of channels in
+// order, and a tile's entry state comes from the words of the tiles of its
+// group and the state at the end of the group before.  Every wait ends: a
+// workgroup finishes its tiles in the order in which it took them, and of all
+// tiles taken and not yet finished the one taken first waits for finished ones
+// only (none is taken by a workgroup that does not run).
+//
+// 8192 x 4096 in bf16: 80 us (3.3 TB/s), 65536 x 2560 362 (3.7); without the
+// waits 65 and 288.  Two passes (the tiles' words, a join, the outputs) took 111
+// and 477, as the values are made twice; tiles of 64 tokens 88 and 447, which
+// wait more often; one counter for all columns 93 and 383 (512 workgroups that
+// draw their first tile from one word: 13 us); the next tile's loads ahead of
+// the waits 95 and 425, as a word's load is not there before data asked for
+// earlier.
+template <typename T, int NW, int TT, bool NARROW>
+__global__ __launch_bounds__(64 * NW, 4) void k_lin_one(LinParams p) {
+  constexpr int TOK = NW * TT, SHARE = 64 * NW / kLinCh, EACH = kLinGroup / SHARE;   // lanes that look back for a channel, words for each
+  __shared__ int32_t cu_lds[kCuLds];
+  __shared__ LinAgg aggs[2];
+  __shared__ float half_p[SHARE][kLinCh], half_s[SHARE][kLinCh], entry[kLinCh], before[kLinCh];
+  __shared__ int ticket;
+  // a workgroup stays with its column of channels
+  const int w = wave_id(), l = lane_id(), col = blockIdx.x % p.cols, d = lin_base(col * kLinCh + l * kLinVec, p.D);
+  const int hf = w / (kLinCh / 64), c = 64 * (w - kLinCh / 64 * hf) + l;
+  const uint32_t dc = lin_channel(col, c, p.D);
+  int* tickets = p.ticket + col * kLinLine;
+  if (threadIdx.x == 0) ticket = atomicAdd(tickets, 1);
+  float A2[kLinVec];
+  lin_floats<NARROW>(p.A, d, p.D, A2);
+#pragma unroll
+  for (int e = 0; e < kLinVec; ++e) A2[e] *= 1.4426950408889634f;
+  const SeqFinder sf = seq_finder(p.s, cu_lds);
+  __syncthreads();
+  int tile = __builtin_amdgcn_readfirstlane(ticket);
+  for (int par = 0; tile < p.tiles; par ^= 1) {
+    const int t0 = tile * TOK + w * TT;
+    LinAgg& agg = aggs[par];
+    typename VecIO<T, kLinVec>::raw xr[TT], rr[TT], ir[TT];
+    lin_load<NARROW, T, TT>(p.r, p.r_stride, t0, p.s.Ttot, d, p.D, rr);
+    lin_load<NARROW, T, TT>(p.i, p.i_stride, t0, p.s.Ttot, d, p.D, ir);
+    lin_load<NARROW, T, TT>(p.x, p.x_stride, t0, p.s.Ttot, d, p.D, xr);
+    int next = 0;
+    if (threadIdx.x == 0) next = atomicAdd(tickets, 1);
+    const TokenRuns run = lin_runs<TT>(sf, t0, agg.seq[w]);
+    float a[TT][kLinVec], b[TT][kLinVec];
+    lin_values<T, TT>(A2, xr, rr, ir, a, b);
+    lin_v P, S;
+    lin_effect<NARROW, TT>(p, agg.seq[w], run, t0, d, a, b, P, S);
+    agg.p[w][l] = P;
+    agg.s[w][l] = S;
+    lds_barrier();
+    float tp = 1.f, ts = 0.f;
+    if (hf == 0) {
+#pragma unroll
+      for (int u = 0; u < NW; ++u) lin_join(tp, ts, agg.p[u][c / kLinVec][c % kLinVec], agg.s[u][c / kLinVec][c % kLinVec]);
+      lin_put(p.words + (long)tile * p.D + dc, tp, ts);
+    }
+    const int grp = tile / kLinGroup, in = tile - grp * kLinGroup, n = max(0, min(EACH, in - EACH * hf));
+    const bool reach = hf == SHARE - 1 && grp > 0;   // the state at the end of the group before
+    const char* words = reinterpret_cast<const char*>(p.words + (long)(grp * kLinGroup + EACH * hf) * p.D);
+    const char* end = reinterpret_cast<const char*>(p.ends + (long)(grp - 1) * p.D);
+    float bp = 1.f, bs = 0.f;
+    uint32_t ve = 0;
+    if (n > 0 || reach) {
+      uint64_t v[EACH];
+      for (int looks = 0;; ++looks) {
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) v[k] = k < n ? lin_get(words + (long)k * p.D * 8, 8 * dc) : 0;
+        if (reach) ve = __hip_atomic_load((const GDR_GLOBAL uint32_t*)(lin_uniform(end) + 4 * dc), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        bool all = ve != kLinEmpty;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) all &= (uint32_t)v[k] != kLinEmpty;
+        if (all || looks >= kLinLooks) break;
+        __builtin_amdgcn_s_sleep(2);
+      }
+#pragma unroll
+      for (int k = 0; k < EACH; ++k)
+        if (k < n) lin_join(bp, bs, __builtin_bit_cast(float, (uint32_t)v[k]), __builtin_bit_cast(float, (uint32_t)(v[k] >> 32)));
+    }
+    half_p[hf][c] = bp;
+    half_s[hf][c] = bs;
+    if (hf == SHARE - 1) before[c] = __builtin_bit_cast(float, ve);
+    if (threadIdx.x == 0) ticket = next;
+    lds_barrier();
+    if (hf == 0) {
+      float h = before[c];
+#pragma unroll
+      for (int u = 0; u < SHARE; ++u) h = lin_after(h, half_p[u][c], half_s[u][c]);
+      entry[c] = h;
+      if (in == kLinGroup - 1)
+        __hip_atomic_store(p.ends + (long)grp * p.D + dc, lin_bits(lin_after(h, tp, ts)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    lds_barrier();
+    const int done = tile;
+    tile = __builtin_amdgcn_readfirstlane(ticket);
+    float h[kLinVec];
+#pragma unroll
+    for (int e = 0; e < kLinVec; ++e) h[e] = entry[l * kLinVec + e];
+    for (int u = 0; u < w; ++u) {
+      const lin_v pu = agg.p[u][l], su = agg.s[u][l];
+#pragma unroll
+      for (int e = 0; e < kLinVec; ++e) h[e] = lin_after(h[e], pu[e], su[e]);
+    }
+    lin_leave<NARROW, T, TT>(p, agg.seq[w], run, t0, d, a, b, h);
+    if (hf == 0) lin_empty(sf, p.h0, p.ht, done, p.tiles, col * kLinCh + c, p.D);
   }
 }
 
-// The tiles' (P, S) turned into the states at their ends, and, for the
-// gradient, Q (what a tile hands on to the tile before it of the gradient of
-// the state, from zero) into what it hands on: 64 channels by 16 strands of
-// consecutive tiles a workgroup.
-template <bool BWD>
+// Prompts of one tile: nothing to look back for, and nothing to clear.
+template <typename T, int NW, int TT, bool NARROW>
+__global__ __launch_bounds__(64 * NW, 4) void k_lin_tile(LinParams p) {
+  __shared__ int32_t cu_lds[kCuLds];
+  __shared__ LinAgg agg;
+  const int w = wave_id(), l = lane_id(), t0 = w * TT, col = blockIdx.x;
+  const int d = lin_base(col * kLinCh + l * kLinVec, p.D);
+  float a[TT][kLinVec], b[TT][kLinVec], h[kLinVec] = {};
+  if (p.s.Ttot > 0) {
+    typename VecIO<T, kLinVec>::raw xr[TT], rr[TT], ir[TT];
+    lin_load<NARROW, T, TT>(p.r, p.r_stride, t0, p.s.Ttot, d, p.D, rr);
+    lin_load<NARROW, T, TT>(p.i, p.i_stride, t0, p.s.Ttot, d, p.D, ir);
+    lin_load<NARROW, T, TT>(p.x, p.x_stride, t0, p.s.Ttot, d, p.D, xr);
+    float A2[kLinVec];
+    lin_floats<NARROW>(p.A, d, p.D, A2);
+#pragma unroll
+    for (int c = 0; c < kLinVec; ++c) A2[c] *= 1.4426950408889634f;
+    lin_values<T, TT>(A2, xr, rr, ir, a, b);
+  }
+  const SeqFinder sf = seq_finder(p.s, cu_lds);
+  const TokenRuns run = lin_runs<TT>(sf, t0, agg.seq[w]);
+  lin_v P, S;
+  lin_effect<NARROW, TT>(p, agg.seq[w], run, t0, d, a, b, P, S);
+  agg.p[w][l] = P;
+  agg.s[w][l] = S;
+  lds_barrier();
+  for (int u = 0; u < w; ++u) {
+    const lin_v pu = agg.p[u][l], su = agg.s[u][l];
+#pragma unroll
+    for (int c = 0; c < kLinVec; ++c) h[c] = lin_after(h[c], pu[c], su[c]);
+  }
+  lin_leave<NARROW, T, TT>(p, agg.seq[w], run, t0, d, a, b, h);
+  for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) lin_empty(sf, p.h0, p.ht, 0, 1, col * kLinCh + c, p.D);
+}
+
+// The tiles' (P, S) turned into the states at their ends, and Q into what the
+// tiles hand on: 16 channels by 64 strands of consecutive tiles a workgroup, so
+// that a strand's loads are few and all compute units take part (171 tiles of
+// 1024 channels with 64 channels by 16 strands: 12 us, so 9.5).
 __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
-  __shared__ float lp[16][64], ls[16][64], lq[16][64];
-  const int c = threadIdx.x & 63, u = threadIdx.x >> 6, d = blockIdx.x * 64 + c;
-  const int per = (p.tiles + 15) / 16, j0 = min(u * per, p.tiles), j1 = min(j0 + per, p.tiles);
+  constexpr int CH = 16, ST = 1024 / CH;
+  __shared__ float lp[ST][CH], ls[ST][CH], lq[ST][CH];
+  const int c = threadIdx.x % CH, u = threadIdx.x / CH, d = blockIdx.x * CH + c;
+  const int per = (p.tiles + ST - 1) / ST, j0 = min(u * per, p.tiles), j1 = min(j0 + per, p.tiles);
   const bool live = d < p.D;
   const float* P = p.P + d;
-  float* S = p.S + d;
-  float* Q = BWD ? p.Q + d : nullptr;
+  float *S = p.S + d, *Q = p.Q + d;
   float q = 1.f, s = 0.f, g = 0.f;
   if (live) {
-#pragma unroll 8
+#pragma unroll 4
     for (int j = j0; j < j1; ++j) {
-      const float pj = P[(long)j * p.D], sj = S[(long)j * p.D];
-      s = pj == kFresh ? sj : fmaf(pj, s, sj);
-      q = pj == kFresh || q == kFresh ? kFresh : q * pj;
+      const float pj = P[(long)j * p.D];
+      // what a later run hands on goes through this one's decays (kFresh: not at all)
+      g = q == kFresh ? g : fmaf(q, Q[(long)j * p.D], g);
+      lin_join(q, s, pj, S[(long)j * p.D]);
     }
-    if (BWD)
-#pragma unroll 8
-      for (int j = j1 - 1; j >= j0; --j) {
-        const float pj = P[(long)j * p.D], qj = Q[(long)j * p.D];
-        g = pj == kFresh ? qj : fmaf(pj, g, qj);
-      }
   }
   lp[u][c] = q;
   ls[u][c] = s;
   lq[u][c] = g;
   __syncthreads();
-  if (!live) return;
+  if (!live || j0 == j1) return;
   float h = 0.f;
-  for (int v = 0; v < u; ++v) h = lp[v][c] == kFresh ? ls[v][c] : fmaf(lp[v][c], h, ls[v][c]);
-#pragma unroll 8
+#pragma unroll 4
+  for (int v = 0; v < u; ++v) h = lin_after(h, lp[v][c], ls[v][c]);
+#pragma unroll 4
   for (int j = j0; j < j1; ++j) {
-    const float pj = P[(long)j * p.D], sj = S[(long)j * p.D];
-    h = pj == kFresh ? sj : fmaf(pj, h, sj);
+    h = lin_after(h, P[(long)j * p.D], S[(long)j * p.D]);
     S[(long)j * p.D] = h;
   }
-  if (BWD) {
-    g = 0.f;
-    for (int v = 15; v > u; --v) g = lp[v][c] == kFresh ? lq[v][c] : fmaf(lp[v][c], g, lq[v][c]);
-#pragma unroll 8
-    for (int j = j1 - 1; j >= j0; --j) {
-      const float pj = P[(long)j * p.D], qj = Q[(long)j * p.D];
-      g = pj == kFresh ? qj : fmaf(pj, g, qj);
-      Q[(long)j * p.D] = g;
-    }
+  g = 0.f;
+#pragma unroll 4
+  for (int v = ST - 1; v > u; --v) g = lin_after(g, lp[v][c], lq[v][c]);
+#pragma unroll 4
+  for (int j = j1 - 1; j >= j0; --j) {
+    g = lin_after(g, P[(long)j * p.D], Q[(long)j * p.D]);
+    Q[(long)j * p.D] = g;
   }
 }
 
@@ -236,188 +417,183 @@ __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
 //   g_t = dy_t + a_{t+1} g_{t+1}  (+ dht at a sequence's last token)
 //   dx = g m sigmoid(i),  di = g b (1 - sigmoid(i))
 //   ds = g (a h_{t-1} - a^2 / m sigmoid(i) x),  dr = ds A e (1 - e),  dA = sum of ds e
-// (s = A e; where m is zero its term is left out).  A lane walks its TT tokens
-// three times: for the run's P, S and Q, forwards for the states before each
-// token, which take the place of b, and backwards for the gradients.
-template <typename T, int NW, int TT, bool OUT>
-__global__ __launch_bounds__(64 * NW) void k_lin_bwd(LinParams p) {
+// (s = A e; where m is zero its term is left out).  What does not depend on h
+// and g is made once (seven values), the states turn it into five factors of g
+// forwards, and the gradients come backwards.
+//
+// OUT false: what each tile does to the state (P, S) and to its gradient (P, Q:
+// what it hands on to the tile before it, from zero).  Both directions cannot
+// be had in one pass, as tiles would wait for each other.  32768 x 4096 in bf16:
+// 236 us (4.5 TB/s), the join 34, this pass 378 (5.0 TB/s), dA 11.  With eight
+// tokens a wave one workgroup of 152 registers is resident and not two (475); in
+// workgroups of four waves 355, and the shorter tiles' joins take that again.
+// Values made again for the walk backwards instead of held took 643.
+template <typename T, int NW, int TT, bool OUT, bool NARROW>
+__global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
   constexpr int TOK = NW * TT;
   __shared__ int32_t cu_lds[kCuLds];
   __shared__ LinAgg agg;
-  __shared__ f32x4 back[NW][64];
-  const int tile = blockIdx.x / p.cols, col = blockIdx.x - tile * p.cols;
+  __shared__ lin_v back[NW][64];
+  // the second pass starts with what the first one read last
+  const int id = OUT ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x, tile = id / p.cols, col = id - tile * p.cols;
   const int w = wave_id(), l = lane_id(), t0 = tile * TOK + w * TT;
-  const int d = col * kLinCh + l * kLinVec, nd = min(kLinVec, p.D - d);
-  const bool full = (col + 1) * kLinCh <= p.D;
-  typename VecIO<T, kLinVec>::raw xr[TT], rr[TT], ir[TT], gr[TT];
-  if (t0 < p.s.Ttot) {
-    lin_load<T, TT>(p.r, p.r_stride, t0, p.s.Ttot, d, nd, full, rr);
-    lin_load<T, TT>(p.i, p.i_stride, t0, p.s.Ttot, d, nd, full, ir);
-    lin_load<T, TT>(p.x, p.x_stride, t0, p.s.Ttot, d, nd, full, xr);
-    lin_load<T, TT>(p.dy, p.D, t0, p.s.Ttot, d, nd, full, gr);
-  }
-  float A[kLinVec], h[kLinVec], g[kLinVec];
-  vec_load<float, kLinVec>(p.A + d, max(0, nd), A);
-#pragma unroll
-  for (int c = 0; c < kLinVec; ++c) h[c] = g[c] = 0.f;
-  if (OUT && tile > 0) vec_load<float, kLinVec>(p.S + (long)(tile - 1) * p.D + d, max(0, nd), h);
-  if (OUT && tile + 1 < p.tiles) vec_load<float, kLinVec>(p.Q + (long)(tile + 1) * p.D + d, max(0, nd), g);
+  const int d = lin_base(col * kLinCh + l * kLinVec, p.D);
+  float a[TT][kLinVec], b[TT][kLinVec], g0[TT][kLinVec], h[kLinVec] = {}, g[kLinVec] = {};
+  float mj[TT][kLinVec], fi[TT][kLinVec], u[TT][kLinVec], e[TT][kLinVec], q[TT][kLinVec];   // OUT
   const SeqFinder sf = seq_finder(p.s, cu_lds);
-  const TokenRuns run = lin_runs<TT>(sf, t0);
-  float a[TT][kLinVec], b[TT][kLinVec];
-  f32x4 P = f32x4{1.f, 1.f, 1.f, 1.f}, S = zero4(), Q = zero4();
-  auto dy_at = [&](int k, float (&f)[kLinVec]) __attribute__((always_inline)) {
-    VecIO<T, kLinVec>::up(gr[k], f);
-    if (p.dht && (run.last >> k & 1)) {
-      float e[kLinVec];
-      vec_load<float, kLinVec>(p.dht + (long)lin_seq_at(sf, t0 + k) * p.D + d, max(0, nd), e);
+  const TokenRuns run = lin_runs<TT>(sf, t0, agg.seq[w]);
+  if (p.s.Ttot > 0) {
+    typename VecIO<T, kLinVec>::raw xr[TT], rr[TT], ir[TT], gr[TT];
+    lin_load<NARROW, T, TT>(p.r, p.r_stride, t0, p.s.Ttot, d, p.D, rr);
+    lin_load<NARROW, T, TT>(p.i, p.i_stride, t0, p.s.Ttot, d, p.D, ir);
+    lin_load<NARROW, T, TT>(p.x, p.x_stride, t0, p.s.Ttot, d, p.D, xr);
+    lin_load<NARROW, T, TT>(p.dy, p.D, t0, p.s.Ttot, d, p.D, gr);
+    float A[kLinVec], A2[kLinVec];
+    lin_floats<NARROW>(p.A, d, p.D, A);
 #pragma unroll
-      for (int c = 0; c < kLinVec; ++c) f[c] += e[c];
-    }
-  };
-  auto h0_at = [&](int k, float (&f)[kLinVec]) __attribute__((always_inline)) {
-    if (p.h0) vec_load<float, kLinVec>(p.h0 + (long)lin_seq_at(sf, t0 + k) * p.D + d, max(0, nd), f);
-    else
+    for (int c = 0; c < kLinVec; ++c) A2[c] = A[c] * 1.4426950408889634f;
+    if (OUT && tile > 0) lin_floats<NARROW>(p.S + (long)(tile - 1) * p.D, d, p.D, h);
+    if (OUT && tile + 1 < p.tiles) lin_floats<NARROW>(p.Q + (long)(tile + 1) * p.D, d, p.D, g);
+    if constexpr (!OUT) {
+      lin_values<T, TT>(A2, xr, rr, ir, a, b);
+    } else {
 #pragma unroll
-      for (int c = 0; c < kLinVec; ++c) f[c] = 0.f;
-  };
-  if (t0 < p.s.Ttot) {
+      for (int k = 0; k < TT; ++k) {
+        float x[kLinVec], r[kLinVec], i[kLinVec];
+        VecIO<T, kLinVec>::up(rr[k], r);
+        VecIO<T, kLinVec>::up(ir[k], i);
+        VecIO<T, kLinVec>::up(xr[k], x);
 #pragma unroll
-    for (int k = 0; k < TT; ++k) {
-      float x[kLinVec], r[kLinVec], i[kLinVec];
-      VecIO<T, kLinVec>::up(rr[k], r);
-      VecIO<T, kLinVec>::up(ir[k], i);
-      VecIO<T, kLinVec>::up(xr[k], x);
-#pragma unroll
-      for (int c = 0; c < kLinVec; ++c) lin_gates(x[c], r[c], i[c], A[c] * 1.4426950408889634f, a[k][c], b[k][c]);
-      if (run.first >> k & 1) {
-        float h0[kLinVec];
-        h0_at(k, h0);
-#pragma unroll
-        for (int c = 0; c < kLinVec; ++c) S[c] = fmaf(a[k][c], h0[c], b[k][c]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kLinVec; ++c) S[c] = run.gap >> k & 1 ? 0.f : fmaf(a[k][c], S[c], b[k][c]);
+        for (int c = 0; c < kLinVec; ++c) {
+          float ne, j, nj;
+          sigmoid_both(r[c], e[k][c], ne);
+          sigmoid_both(i[c], j, nj);
+          const float s2 = A2[c] * e[k][c], ak = __builtin_amdgcn_exp2f(s2), m2 = lin_factor2(s2, ak);
+          const float rm = m2 == 0.f ? 0.f : __builtin_amdgcn_rsqf(m2);
+          a[k][c] = ak;
+          mj[k][c] = m2 * rm * j;
+          b[k][c] = mj[k][c] * x[c];
+          fi[k][c] = b[k][c] * nj;
+          u[k][c] = ak * rm * (ak * rm) * b[k][c];   // a^2 / m sigmoid(i) x
+          q[k][c] = A[c] * ne;
+        }
       }
-#pragma unroll
-      for (int c = 0; c < kLinVec; ++c) P[c] *= a[k][c];
     }
 #pragma unroll
-    for (int k = TT - 1; k >= 0; --k) {
-      float f[kLinVec];
-      dy_at(k, f);
-#pragma unroll
-      for (int c = 0; c < kLinVec; ++c) Q[c] = (run.first | run.gap) >> k & 1 ? 0.f : a[k][c] * (f[c] + Q[c]);
-    }
+    for (int k = 0; k < TT; ++k) VecIO<T, kLinVec>::up(gr[k], g0[k]);
   }
-  if (run.first | run.gap) P = f32x4{kFresh, kFresh, kFresh, kFresh};
+  if (p.dht && run.last) {
+#pragma unroll
+    for (int k = 0; k < TT; ++k)
+      if (run.last >> k & 1) {
+        float f[kLinVec];
+        lin_floats<NARROW>(p.dht + (long)lin_seq(agg.seq[w], k) * p.D, d, p.D, f);
+#pragma unroll
+        for (int c = 0; c < kLinVec; ++c) g0[k][c] += f[c];
+      }
+  }
+  // the gradient that token k hands on to the one before it
+  const uint32_t cut = run.first | run.gap;
+  lin_v P, S, Q;
+  lin_effect<NARROW, TT>(p, agg.seq[w], run, t0, d, a, b, P, S);
+#pragma unroll
+  for (int c = 0; c < kLinVec; ++c) Q[c] = 0.f;
+#pragma unroll
+  for (int k = TT - 1; k >= 0; --k) {
+#pragma unroll
+    for (int c = 0; c < kLinVec; ++c) Q[c] = a[k][c] * (g0[k][c] + Q[c]);
+    if (cut >> k & 1)
+#pragma unroll
+      for (int c = 0; c < kLinVec; ++c) Q[c] = 0.f;
+  }
   agg.p[w][l] = P;
   agg.s[w][l] = S;
   back[w][l] = Q;
-  __syncthreads();
+  lds_barrier();
   if constexpr (!OUT) {
     for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) {
-      if (col * kLinCh + c >= p.D) break;
-      float q = 1.f, s = 0.f, b = 0.f;
+      const int dc = lin_channel(col, c, p.D);
+      if (dc >= p.D) break;
+      float tp = 1.f, ts = 0.f, tq = 0.f;
 #pragma unroll
-      for (int u = 0; u < NW; ++u) {
-        const float pu = agg.p[u][c / 4][c % 4], su = agg.s[u][c / 4][c % 4];
-        s = pu == kFresh ? su : fmaf(pu, s, su);
-        q = pu == kFresh || q == kFresh ? kFresh : q * pu;
-      }
+      for (int v = 0; v < NW; ++v) lin_join(tp, ts, agg.p[v][c / kLinVec][c % kLinVec], agg.s[v][c / kLinVec][c % kLinVec]);
 #pragma unroll
-      for (int u = NW - 1; u >= 0; --u) {
-        const float pu = agg.p[u][c / 4][c % 4], qu = back[u][c / 4][c % 4];
-        b = pu == kFresh ? qu : fmaf(pu, b, qu);
-      }
-      p.P[(long)tile * p.D + col * kLinCh + c] = q;
-      p.S[(long)tile * p.D + col * kLinCh + c] = s;
-      p.Q[(long)tile * p.D + col * kLinCh + c] = b;
+      for (int v = NW - 1; v >= 0; --v) tq = lin_after(tq, agg.p[v][c / kLinVec][c % kLinVec], back[v][c / kLinVec][c % kLinVec]);
+      p.P[(long)tile * p.D + dc] = tp;
+      p.S[(long)tile * p.D + dc] = ts;
+      p.Q[(long)tile * p.D + dc] = tq;
     }
     return;
   }
-  for (int u = 0; u < w; ++u) {
-    const f32x4 pu = agg.p[u][l], su = agg.s[u][l];
+  for (int v = 0; v < w; ++v) {
+    const lin_v pv = agg.p[v][l], sv = agg.s[v][l];
 #pragma unroll
-    for (int c = 0; c < kLinVec; ++c) h[c] = pu[c] == kFresh ? su[c] : fmaf(pu[c], h[c], su[c]);
+    for (int c = 0; c < kLinVec; ++c) h[c] = lin_after(h[c], pv[c], sv[c]);
   }
-  for (int u = NW - 1; u > w; --u) {
-    const f32x4 pu = agg.p[u][l], qu = back[u][l];
+  for (int v = NW - 1; v > w; --v) {
+    const lin_v pv = agg.p[v][l], qv = back[v][l];
 #pragma unroll
-    for (int c = 0; c < kLinVec; ++c) g[c] = pu[c] == kFresh ? qu[c] : fmaf(pu[c], g[c], qu[c]);
+    for (int c = 0; c < kLinVec; ++c) g[c] = lin_after(g[c], pv[c], qv[c]);
   }
-  // forwards: the state before each token in the place of b
 #pragma unroll
   for (int k = 0; k < TT; ++k) {
-    if (run.first >> k & 1) h0_at(k, h);
+    if (run.first >> k & 1) lin_initial<NARROW>(p, agg.seq[w], k, d, h);
 #pragma unroll
     for (int c = 0; c < kLinVec; ++c) {
-      const float old = h[c];
-      h[c] = run.gap >> k & 1 ? 0.f : fmaf(a[k][c], old, b[k][c]);
-      b[k][c] = old;
+      const float f = fmaf(a[k][c], h[c], -u[k][c]) * e[k][c];   // ds e / g
+      u[k][c] = f;
+      q[k][c] *= f;
+      h[c] = fmaf(a[k][c], h[c], b[k][c]);
     }
+    if (run.gap >> k & 1)
+#pragma unroll
+      for (int c = 0; c < kLinVec; ++c) a[k][c] = g0[k][c] = mj[k][c] = fi[k][c] = u[k][c] = q[k][c] = h[c] = 0.f;
   }
-  f32x4 dA = zero4();
-  T *dx = static_cast<T*>(p.dx) + d, *dr = static_cast<T*>(p.dr) + d, *di = static_cast<T*>(p.di) + d;
+  lin_v dA;
+#pragma unroll
+  for (int c = 0; c < kLinVec; ++c) dA[c] = 0.f;
 #pragma unroll
   for (int k = TT - 1; k >= 0; --k) {
-    const long at = (long)(t0 + k) * p.D;
-    if (run.gap >> k & 1) {
+    float ox[kLinVec], orr[kLinVec], oi[kLinVec];
+    if (run.gap >> k & 1)
 #pragma unroll
       for (int c = 0; c < kLinVec; ++c) g[c] = 0.f;
-      if (t0 + k < p.s.Ttot && nd > 0) {
-        vec_store<T, kLinVec>(dx + at, nd, g);
-        vec_store<T, kLinVec>(dr + at, nd, g);
-        vec_store<T, kLinVec>(di + at, nd, g);
-      }
-      continue;
-    }
-    float x[kLinVec], r[kLinVec], i[kLinVec], f[kLinVec], ox[kLinVec], orr[kLinVec], oi[kLinVec];
-    dy_at(k, f);
-    VecIO<T, kLinVec>::up(rr[k], r);
-    VecIO<T, kLinVec>::up(ir[k], i);
-    VecIO<T, kLinVec>::up(xr[k], x);
 #pragma unroll
     for (int c = 0; c < kLinVec; ++c) {
-      const float gt = f[c] + g[c], at = a[k][c];
-      float e, ne, j, nj;
-      sigmoid_both(r[c], e, ne);
-      sigmoid_both(i[c], j, nj);
-      const float m = lin_factor(A[c] * 1.4426950408889634f * e, at);
-      const float jx = j * x[c];
-      const float dm = m > 0.f ? at * at * __builtin_amdgcn_rcpf(m) : (m == 0.f ? 0.f : m);
-      const float ds = gt * (at * b[k][c] - dm * jx);
-      ox[c] = gt * m * j;
-      oi[c] = gt * m * jx * nj;
-      orr[c] = ds * A[c] * e * ne;
-      dA[c] = fmaf(ds, e, dA[c]);
-      g[c] = at * gt;
+      const float gt = g0[k][c] + g[c];
+      ox[c] = gt * mj[k][c];
+      oi[c] = gt * fi[k][c];
+      orr[c] = gt * q[k][c];
+      dA[c] = fmaf(gt, u[k][c], dA[c]);
+      g[c] = a[k][c] * gt;
     }
-    if (nd > 0) {
-      vec_store<T, kLinVec>(dx + at, nd, ox);
-      vec_store<T, kLinVec>(dr + at, nd, orr);
-      vec_store<T, kLinVec>(di + at, nd, oi);
+    if (t0 + k < p.s.Ttot) {
+      const long row = (long)(t0 + k) * p.D * (long)sizeof(T);
+      lin_write<NARROW, T>(static_cast<char*>(p.dx) + row, d, p.D, ox);
+      lin_write<NARROW, T>(static_cast<char*>(p.dr) + row, d, p.D, orr);
+      lin_write<NARROW, T>(static_cast<char*>(p.di) + row, d, p.D, oi);
     }
     if (run.first >> k & 1) {
-      if (p.dh0 && nd > 0) vec_store<float, kLinVec>(p.dh0 + (long)lin_seq_at(sf, t0 + k) * p.D + d, nd, g);
+      if (p.dh0) lin_write<NARROW, float>(p.dh0 + (long)lin_seq(agg.seq[w], k) * p.D, d, p.D, g);
 #pragma unroll
       for (int c = 0; c < kLinVec; ++c) g[c] = 0.f;
     }
   }
-  __syncthreads();   // every wave has read the others' runs
+  lds_barrier();   // every wave has read the others' runs
   back[w][l] = dA;
-  __syncthreads();
+  lds_barrier();
   for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) {
-    if (p.dh0) lin_empty(sf, p.dht, p.dh0, tile, p.tiles, col * kLinCh + c, p.D);
-    if (col * kLinCh + c >= p.D) continue;
+    lin_empty(sf, p.dht, p.dh0, tile, p.tiles, col * kLinCh + c, p.D);
+    const int dc = lin_channel(col, c, p.D);
+    if (dc >= p.D) break;
     float s = 0.f;
 #pragma unroll
-    for (int u = 0; u < NW; ++u) s += back[u][c / 4][c % 4];
-    p.part[(long)tile * p.D + col * kLinCh + c] = s;
+    for (int v = 0; v < NW; ++v) s += back[v][c / kLinVec][c % kLinVec];
+    p.part[(long)tile * p.D + dc] = s;
   }
 }
 
-// One new token per row; a wave takes 256 channels of one row.
+// One new token per row; a wave takes 128 channels of one row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_step(LinParams p) {
   const long unit = (long)blockIdx.x * (blockDim.x >> 6) + wave_id();
@@ -427,7 +603,7 @@ __global__ __launch_bounds__(256) void k_lin_step(LinParams p) {
   const int slot = step_slot(p.slots, row, p.num_slots);
   if (nd <= 0) return;
   T* y = static_cast<T*>(p.y) + (long)row * p.D + d;
-  float h[kLinVec] = {0.f, 0.f, 0.f, 0.f};
+  float h[kLinVec] = {};
   if (slot >= 0) {
     float x[kLinVec], r[kLinVec], i[kLinVec], A[kLinVec];
     float* state = p.ht + (long)slot * p.D + d;
@@ -447,11 +623,15 @@ __global__ __launch_bounds__(256) void k_lin_step(LinParams p) {
   vec_store<T, kLinVec>(y, nd, h);
 }
 
-constexpr int kLinWaves = 8, kLinTok = 8;   // waves a tile, tokens a wave
-int lin_tiles(int tokens) {
-  const int n = (tokens + kLinWaves * kLinTok - 1) / (kLinWaves * kLinTok);
+// Waves a tile, and tokens a wave (by the size of the type: a lane holds them all).
+constexpr int kLinWaves = 8, kLinTok16 = 16, kLinTok32 = 8;
+constexpr int kLinBwdWaves = 8, kLinBwdTok = 6;   // waves a tile, tokens a wave
+static int lin_tiles_of(int tokens, int tile) {
+  const int n = (tokens + tile - 1) / tile;
   return n > 0 ? n : 1;
 }
+int lin_tiles(DType dt, int tokens) { return lin_tiles_of(tokens, kLinWaves * (dt == DType::BF16 ? kLinTok16 : kLinTok32)); }
+int lin_bwd_tiles(int tokens) { return lin_tiles_of(tokens, kLinBwdWaves * kLinBwdTok); }
 int lin_cols(int D) { return (D + kLinCh - 1) / kLinCh; }
 
 template <typename K>
@@ -463,27 +643,40 @@ static hipError_t lin_launch(const char* name, K kernel, dim3 grid, dim3 block, 
   return e;
 }
 
+// Bytes of the words, the groups' states and the ticket; 32-bit values.
+static long lin_words(int tiles, int D) { return (long)tiles * D * 2 + (long)(tiles / kLinGroup + 1) * D + (long)lin_cols(D) * kLinLine; }
+size_t lin_fwd_bytes(DType dt, int tokens, int D) { return (size_t)lin_words(lin_tiles(dt, tokens), D) * 4; }
+
 template <typename T>
-static hipError_t lin_fwd(const LinParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)(p.tiles * p.cols)), block(64 * kLinWaves);
-  if (p.tiles > 1) {
-    if (hipError_t e = lin_launch("linear_scan_parts", k_lin_fwd<T, kLinWaves, kLinTok, false>, grid, block, p, st)) return e;
-    if (hipError_t e = lin_launch("linear_scan_join", k_lin_join<false>, dim3((p.D + 63) / 64), dim3(1024), p, st)) return e;
-  }
-  return lin_launch("linear_scan_out", k_lin_fwd<T, kLinWaves, kLinTok, true>, grid, block, p, st);
+static hipError_t lin_fwd(LinParams p, void* workspace, hipStream_t st) {
+  constexpr int TT = sizeof(T) == 2 ? kLinTok16 : kLinTok32;
+  const dim3 block(64 * kLinWaves);
+#define CALL(K) (p.D < kLinVec ? K<T, kLinWaves, TT, true> : K<T, kLinWaves, TT, false>)
+  if (p.tiles == 1) return lin_launch("linear_scan", CALL(k_lin_tile), dim3(p.cols), block, p, st);
+  p.words = static_cast<uint64_t*>(workspace);
+  p.ends = reinterpret_cast<uint32_t*>(p.words + (long)p.tiles * p.D);
+  p.ticket = reinterpret_cast<int*>(p.ends + (long)(p.tiles / kLinGroup + 1) * p.D);
+  const long blocks = (lin_words(p.tiles, p.D) + 4095) / 4096;
+  if (hipError_t e = lin_launch("linear_scan_clear", k_lin_clear, dim3(blocks < 4 * kComputeUnits ? blocks : 4 * kComputeUnits), dim3(256), p, st)) return e;
+  // as many workgroups a column as are resident at once
+  const int resident = 2 * kComputeUnits / p.cols;
+  return lin_launch("linear_scan", CALL(k_lin_one), dim3(p.cols * (resident < 1 ? 1 : resident < p.tiles ? resident : p.tiles)), block, p, st);
+#undef CALL
 }
-hipError_t launch_lin_fwd(DType dt, const LinParams& p, hipStream_t st) {
-  return dt == DType::BF16 ? lin_fwd<bf16>(p, st) : lin_fwd<float>(p, st);
+hipError_t launch_lin_fwd(DType dt, const LinParams& p, void* workspace, hipStream_t st) {
+  return dt == DType::BF16 ? lin_fwd<bf16>(p, workspace, st) : lin_fwd<float>(p, workspace, st);
 }
 
 template <typename T>
 static hipError_t lin_bwd(const LinParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)(p.tiles * p.cols)), block(64 * kLinWaves);
+  const dim3 grid((unsigned)(p.tiles * p.cols)), block(64 * kLinBwdWaves);
+#define CALL(OUT) (p.D < kLinVec ? k_lin_bwd<T, kLinBwdWaves, kLinBwdTok, OUT, true> : k_lin_bwd<T, kLinBwdWaves, kLinBwdTok, OUT, false>)
   if (p.tiles > 1) {
-    if (hipError_t e = lin_launch("linear_scan_bwd_parts", k_lin_bwd<T, kLinWaves, kLinTok, false>, grid, block, p, st)) return e;
-    if (hipError_t e = lin_launch("linear_scan_bwd_join", k_lin_join<true>, dim3((p.D + 63) / 64), dim3(1024), p, st)) return e;
+    if (hipError_t e = lin_launch("linear_scan_bwd_parts", CALL(false), grid, block, p, st)) return e;
+    if (hipError_t e = lin_launch("linear_scan_bwd_join", k_lin_join, dim3((p.D + 15) / 16), dim3(1024), p, st)) return e;
   }
-  if (hipError_t e = lin_launch("linear_scan_bwd", k_lin_bwd<T, kLinWaves, kLinTok, true>, grid, block, p, st)) return e;
+  if (hipError_t e = lin_launch("linear_scan_bwd", CALL(true), grid, block, p, st)) return e;
+#undef CALL
   RowsSum s = {};
   s.part = p.part;
   s.rows = p.tiles;

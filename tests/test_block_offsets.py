@@ -14,15 +14,21 @@ RUNS = r"""
 extern "C" int runs(const int32_t* cu, int N, int T, int Ttot, int t0, int count, uint32_t* out) {
   gdr::SeqFinder f;
   f.cu = cu; f.N = N; f.T = T; f.Ttot = Ttot; f.packed = cu != nullptr;
-  const gdr::TokenRuns m = gdr::token_runs(f, t0, count);
+  int seq[32];
+  for (int& n : seq) n = -1;
+  const gdr::TokenRuns m = gdr::token_runs(f, t0, count, seq);
   out[0] = m.first; out[1] = m.last; out[2] = m.gap;
-  for (int k = 0; k < count; ++k) {   // what a run's ends index: a row of the states
-    if (!((m.first | m.last) >> k & 1)) continue;
-    int start, end;
-    if (t0 + k >= Ttot) return 1;
-    const int n = f.find(t0 + k, start, end);
-    if (n < 0 || n >= N) return 2;
+  for (int k = 0; k < 32; ++k) {   // what a run's ends index: a row of the states
+    if (k < count && ((m.first | m.last) >> k & 1)) {
+      if (t0 + k >= Ttot) return 1;
+      if (seq[k] < 0 || seq[k] >= N) return 2;
+      if (cu && f.at(seq[k]) > t0 + k) return 3;
+      if (!cu && seq[k] != (t0 + k) / T) return 4;
+    } else if (seq[k] != -1) {
+      return 5;
+    }
   }
+  for (int k = 0; k < count; ++k) out[3 + k] = (uint32_t)seq[k];
   return 0;
 }
 """
@@ -39,13 +45,13 @@ def lib(tmp_path_factory):
 
 
 def runs(lib, cu, N, T, total, t0, count):
-    table, out = None if cu is None else (ctypes.c_int32 * len(cu))(*cu), (ctypes.c_uint32 * 3)()
+    table, out = None if cu is None else (ctypes.c_int32 * len(cu))(*cu), (ctypes.c_uint32 * 38)()
     assert lib.runs(table, N, T, total, t0, count, out) == 0, (cu, total, t0)
-    first, last, gap = out
+    first, last, gap = out[:3]
     mask = (1 << count) - 1
     assert first & gap == 0 and (first | last) & ~mask == 0
     assert t0 > 0 or count == 0 or (first | gap) & 1      # token 0 goes on from nothing
-    return first, last, gap & mask
+    return first, last, gap & mask, out[3:3 + count]
 
 
 def test_any_table_stays_inside_the_buffers(lib):
@@ -70,10 +76,12 @@ def test_tables_that_do_not_decrease(lib, count):
             cu, total = sorted(rng.randint(0, T) for _ in range(rng.randint(2, 9))), T
             table = cu
         for t0 in range(0, total, count):
-            first, last, gap = runs(lib, table, len(cu) - 1, T, total, t0, count)
+            first, last, gap, seq = runs(lib, table, len(cu) - 1, T, total, t0, count)
             for k in range(count):
                 t, bit = t0 + k, lambda m: m >> k & 1
                 inside = any(a <= t < b for a, b in zip(cu, cu[1:]))
                 starts = any(a == t < b for a, b in zip(cu, cu[1:]))
                 ends = any(a <= t == b - 1 for a, b in zip(cu, cu[1:]))
+                if starts or ends:
+                    assert cu[seq[k]] <= t < cu[seq[k] + 1]
                 assert (bit(first), bit(last), bit(gap)) == (starts, ends, not inside), (cu, t0, k)
