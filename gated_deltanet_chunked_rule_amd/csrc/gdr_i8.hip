@@ -104,100 +104,138 @@ __device__ __forceinline__ i32x4 i8_head(i32x4 f, int k, int K) {
 }
 __device__ __forceinline__ i32x4 i8_mma(i32x4 a, i32x4 b, i32x4 c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }
 
-// y of N consecutive n from n0 on of row m
-template <typename T, int N>
-__device__ __forceinline__ void i8_leave(const I8Params& p, int m, int n0, const int (&acc)[N], float xs, const float (&ws)[N], const float (&bias)[N]) {
-  const int nd = min(N, p.N - n0);
-  if (m >= p.M || nd <= 0) return;
-  float f[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) f[e] = (float)acc[e] * xs * ws[e] + bias[e];
-  T* y = static_cast<T*>(p.y) + (long)m * p.N + n0;
-#pragma unroll
-  for (int e = 0; e < N; e += 4) {
-    float g[4] = {f[e], f[e + 1], f[e + 2], f[e + 3]};
-    if (nd > e) vec_store<T, 4>(y + e, nd - e, g);
-  }
-}
-
-// Few rows of x: the weight is streamed once from memory into registers, and
-// nothing is staged.  A workgroup takes 16 NT rows of the weight and 16 MT of
-// x; its waves share k in pieces of 64 U bytes and add up in LDS.
-template <typename T, int MT, int NT, int U, int NW>
-__global__ __launch_bounds__(64 * NW) void k_i8_few(I8Params p) {
-  constexpr int TILES = MT * NT;
-  __shared__ i32x4 part[NW][TILES][64];
-  const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
-  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
-  const rsrc_t rw = make_rsrc_u(p.w + (long)n0 * p.w_stride, i8_range(min(16 * NT, p.N - n0), p.w_stride, p.K));
-  const rsrc_t rx = make_rsrc_u(p.x + (long)m0 * p.x_stride, i8_range(min(16 * MT, p.M - m0), p.x_stride, p.K));
-  const uint32_t ow = (uint32_t)(c * p.w_stride) + 16 * g, ox = (uint32_t)(c * p.x_stride) + 16 * g;
-  const uint32_t sw = (uint32_t)(16 * p.w_stride), sx = (uint32_t)(16 * p.x_stride);
-  i32x4 acc[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  for (int k0 = w * 64 * U; k0 < p.K; k0 += NW * 64 * U) {
-    i32x4 fw[U][NT], fx[U][MT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i) fw[u][i] = __builtin_bit_cast(i32x4, buf_load16(rw, ow + i * sw + k0 + 64 * u));
-#pragma unroll
-      for (int j = 0; j < MT; ++j) fx[u][j] = __builtin_bit_cast(i32x4, buf_load16(rx, ox + j * sx + k0 + 64 * u));
-    }
-    if (k0 + 64 * U > p.K) {   // wave-uniform
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) fw[u][i] = i8_head(fw[u][i], k0 + 64 * u + 16 * g, p.K);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) acc[i][j] = i8_mma(fw[u][i], fx[u][j], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) part[w][i * MT + j][l] = acc[i][j];
-  __syncthreads();
+// The waves' sums of a workgroup's tiles ([wave][tile][lane], tile = MT i + j),
+// added and left in y.
+template <typename T, int MT, int TILES, int NW>
+__device__ __forceinline__ void i8_finish(const I8Params& p, const i32x4* part, int m0, int n0, int w) {
+  const int l = lane_id(), c = l & 15, g = l >> 4;
   for (int tile = w; tile < TILES; tile += NW) {
-    i32x4 s = part[0][tile][l];
+    i32x4 s = part[tile * 64 + l];
 #pragma unroll
-    for (int u = 1; u < NW; ++u) s += part[u][tile][l];
+    for (int u = 1; u < NW; ++u) s += part[(u * TILES + tile) * 64 + l];
     const int i = tile / MT, j = tile - i * MT, m = m0 + 16 * j + c, n = n0 + 16 * i + 4 * g;
     if (m >= p.M || n >= p.N) continue;
     float ws[4], bias[4] = {0.f, 0.f, 0.f, 0.f};
     vec_load<float, 4>(p.ws + n, p.N - n, ws);
     if (p.bias) vec_load<float, 4>(p.bias + n, p.N - n, bias);
-    const int a[4] = {s[0], s[1], s[2], s[3]};
-    i8_leave<T, 4>(p, m, n, a, p.xs[m], ws, bias);
+    const float xs = p.xs[m];
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = (float)s[e] * xs * ws[e] + bias[e];
+    vec_store<T, 4>(static_cast<T*>(p.y) + (long)m * p.N + n, p.N - n, f);
   }
 }
 
+// The s_waitcnt that lets N of the wave's copies be under way.
+template <int N>
+__device__ __forceinline__ void i8_landed() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
+// Some rows: 16 NT rows of the weight by 16 MT of x a workgroup, in steps of 256
+// bytes of k of which each of the four waves multiplies 64.  Direct copies of
+// whole rows bring the steps into LDS, ST - 1 ahead; nothing in LDS is read
+// twice, and the waves' sums meet at the end.  Row r's 16-byte piece c stands
+// at c ^ stage_swz<16>(r % 16).  Bound by the copies, of the weight from memory
+// and, from 100 rows on, of x from the cache: 4096 -> 8192, 1 row 8.9 us (floor
+// 6.5), 100 rows 12.3, 256 rows 17.4.  Operands read straight into registers
+// took 8.8, 19.4 and 41 (a lane's 16 bytes of 16 rows are 64 requests).
+template <typename T, int MT, int NT, int ST>
+__global__ __launch_bounds__(256) void k_i8_some(I8Params p) {
+  constexpr int NW = 4, KS = 64 * NW, R = 16 * (MT + NT), C = R / 4 / NW, TILES = MT * NT;   // C: 1 KB copies a wave and step
+  static_assert(C * 4 * NW == R, "whole copies for each wave");
+  constexpr int STAGE = R * KS, PART = NW * TILES * 1024;
+  __shared__ __align__(1024) int8_t lds[ST * STAGE > PART ? ST * STAGE : PART];
+  const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
+  const int bn = (p.N + 16 * NT - 1) / (16 * NT), bm = blockIdx.x / bn;
+  const int n0 = (blockIdx.x - bm * bn) * 16 * NT, m0 = bm * 16 * MT;
+  const i32x4v rw = rsrc_words(p.w + (long)n0 * p.w_stride, i8_range(min(16 * NT, p.N - n0), p.w_stride, p.K));
+  const i32x4v rx = rsrc_words(p.x + (long)m0 * p.x_stride, i8_range(min(16 * MT, p.M - m0), p.x_stride, p.K));
+  // rows of the weight first; a copy's four rows are all of one operand
+  uint32_t off[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int first = (j * NW + w) * 4, r = first + (l >> 4);
+    off[j] = (uint32_t)(first < 16 * NT ? r * p.w_stride : (r - 16 * NT) * p.x_stride) + 16 * ((l & 15) ^ stage_swz<16>(r & 15));
+  }
+  const int steps = (p.K + KS - 1) / KS;
+  // steps behind the last are copied from behind the descriptors' ranges: zeros
+  auto copy = [&](int s, int buf) __attribute__((always_inline)) {
+    const uint32_t k0 = s < steps ? (uint32_t)(s * KS) : 0x80000000u;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int first = (j * NW + w) * 4;
+      lds_copy16(first < 16 * NT ? rw : rx, off[j] + k0, lds_addr(&lds[buf * STAGE + first * KS]));
+    }
+  };
+  i32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) copy(s, s);
+  const int at = c * KS + 16 * ((4 * w + g) ^ stage_swz<16>(c));
+  int buf = 0;
+  for (int s = 0; s < steps; ++s) {
+    i8_landed<(ST - 2) * C>();   // of step s, this wave's copies
+    lds_barrier();               // and everybody's; the buffer of step s - 1 is free
+    copy(s + ST - 1, buf == 0 ? ST - 1 : buf - 1);
+    i32x4 fw[NT], fx[MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) fw[i] = *reinterpret_cast<const i32x4*>(&lds[buf * STAGE + at + i * 16 * KS]);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) fx[j] = *reinterpret_cast<const i32x4*>(&lds[buf * STAGE + at + (NT + j) * 16 * KS]);
+    if ((s + 1) * KS > p.K) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) fw[i] = i8_head(fw[i], s * KS + 64 * w + 16 * g, p.K);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = i8_mma(fw[i], fx[j], acc[i][j]);
+    buf = buf == ST - 1 ? 0 : buf + 1;
+  }
+  i8_landed<0>();
+  lds_barrier();   // the stages' place is free for the sums
+  i32x4* part = reinterpret_cast<i32x4*>(lds);
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[(w * TILES + i * MT + j) * 64 + l] = acc[i][j];
+  lds_barrier();
+  i8_finish<T, MT, TILES, NW>(p, part, m0, n0, w);
+}
+
 // Many rows: BN rows of the weight by BM rows of x a workgroup, in steps of 128
-// bytes of k that direct copies bring into two LDS buffers.  Row r's 16-byte
-// piece c stands at c ^ (r % 8).  Row r of a wave's 16 NT weight rows in LDS is
-// n = 4 NT ((r % 16) / 4) + 4 (r / 16) + r % 4, so that a lane's values of one
-// m over its NT tiles are 4 NT consecutive n.
+// bytes of k that direct copies bring into two LDS buffers.  A step is two
+// products of 64 k; the operands of the next one are read into a second set of
+// registers while a product runs.  Row r's 16-byte piece c stands at c ^
+// stage_swz<8>(r % 16).  Row r of a wave's 16 NT weight rows in LDS is n = 4 NT
+// ((r % 16) / 4) + 4 (r / 16) + r % 4, so that a lane's values of one m over its
+// NT tiles are 4 NT consecutive n.
+//
+// 8192 x 4096 -> 8192: 249 us (2.2e15 operations a second), 8192^3 431 (2.55e15),
+// where the clock gives way under the load; a tile's first copies and its
+// outputs are the rest.  With the operands read where they are used 304; steps of
+// 64 k in four buffers 346 (rows of 64 bytes are read at half the rate); copies
+// between the products, or behind an earlier second barrier, 273 and 265;
+// persistent workgroups with the next tile's first copies ahead of the outputs
+// 272; waves of 64 x 128 288.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
   constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16, KS = 128;
-  constexpr int CW = BN / 8 / NW, CX = BM / 8 / NW;   // 1 KB copies a wave
+  constexpr int CW = BN / 8 / NW, CX = BM / 8 / NW, C = CW + CX;   // 1 KB copies a wave and step
   static_assert(CW * 8 * NW == BN && CX * 8 * NW == BM, "whole copies for each wave");
   __shared__ __align__(1024) int8_t lds[2][(BM + BN) * KS];
   const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
   const int id = xcd_remap(blockIdx.x, p.tiles);
   if (id >= p.tiles) return;
-  // groups of p.group rows of tiles, column by column, so that the tiles that
-  // run at once on an XCD share rows of both operands
-  const int per = p.group * p.tn, grp = id / per, in = id - grp * per;
-  const int gm = min(p.group, p.tm - grp * p.group);
-  const int m0 = (grp * p.group + in % gm) * BM, n0 = in / gm * BN;
+  // groups of four rows of tiles, column by column, so that the tiles that run
+  // at once on an XCD share rows of both operands
+  const int per = 4 * p.tn, grp = id / per, in = id - grp * per, gm = min(4, p.tm - grp * 4);
+  const int m0 = (grp * 4 + in % gm) * BM, n0 = in / gm * BN;
   const i32x4v rw = rsrc_words(p.w + (long)n0 * p.w_stride, i8_range(min(BN, p.N - n0), p.w_stride, p.K));
   const i32x4v rx = rsrc_words(p.x + (long)m0 * p.x_stride, i8_range(min(BM, p.M - m0), p.x_stride, p.K));
   uint32_t ow[CW], ox[CX];
@@ -205,82 +243,99 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
   for (int j = 0; j < CW; ++j) {
     const int r = (w * CW + j) * 8 + (l >> 3), in_wave = r % (16 * NT);
     const int n = r - in_wave + 4 * NT * (in_wave % 16 / 4) + 4 * (in_wave / 16) + in_wave % 4;
-    ow[j] = (uint32_t)(n * p.w_stride) + 16 * ((l & 7) ^ (r & 7));
+    ow[j] = (uint32_t)(n * p.w_stride) + 16 * ((l & 7) ^ stage_swz<8>(r & 15));
   }
 #pragma unroll
   for (int j = 0; j < CX; ++j) {
     const int r = (w * CX + j) * 8 + (l >> 3);
-    ox[j] = (uint32_t)(r * p.x_stride) + 16 * ((l & 7) ^ (r & 7));
+    ox[j] = (uint32_t)(r * p.x_stride) + 16 * ((l & 7) ^ stage_swz<8>(r & 15));
   }
-  auto copy = [&](int k0, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < CW; ++j) lds_copy16(rw, ow[j] + k0, lds_addr(&lds[buf][(w * CW + j) * 8 * KS]));
-#pragma unroll
-    for (int j = 0; j < CX; ++j) lds_copy16(rx, ox[j] + k0, lds_addr(&lds[buf][(BN + (w * CX + j) * 8) * KS]));
+  const int steps = (p.K + KS - 1) / KS;
+  // steps behind the last are copied from behind the descriptors' ranges: zeros
+  auto copy_one = [&](int j, uint32_t k0, int buf) __attribute__((always_inline)) {
+    if (j < CW) lds_copy16(rw, ow[j < CW ? j : 0] + k0, lds_addr(&lds[buf][(w * CW + j) * 8 * KS]));
+    else lds_copy16(rx, ox[j < CW ? 0 : j - CW] + k0, lds_addr(&lds[buf][(BN + (w * CX + j - CW) * 8) * KS]));
   };
+  auto copy_at = [&](int s) { return s < steps ? (uint32_t)(s * KS) : 0x80000000u; };
   const int wm = w % WM, wn = w / WM;
   const int aw = (wn * 16 * NT + c) * KS, ax = (BN + wm * 16 * MT + c) * KS;
-  i32x4 acc[NT][MT];
+  i32x4 acc[NT][MT], fw[2][NT], fx[2][MT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  auto products = [&](int k0, int buf, auto tail) __attribute__((always_inline)) {
+  auto read = [&](int buf, auto half) __attribute__((always_inline)) {
+    constexpr int H = decltype(half)::value;
+    const int at = 16 * ((4 * H + g) ^ stage_swz<8>(c));
 #pragma unroll
-    for (int kk = 0; kk < KS / 64; ++kk) {
-      const int at = 16 * ((4 * kk + g) ^ (c & 7));
-      i32x4 fw[NT], fx[MT];
+    for (int i = 0; i < NT; ++i) fw[H][i] = *reinterpret_cast<const i32x4*>(&lds[buf][aw + i * 16 * KS + at]);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) fw[i] = *reinterpret_cast<const i32x4*>(&lds[buf][aw + i * 16 * KS + at]);
+    for (int j = 0; j < MT; ++j) fx[H][j] = *reinterpret_cast<const i32x4*>(&lds[buf][ax + j * 16 * KS + at]);
+  };
+  // Products FROM .. TO of the NT x MT of a half step.
+  auto products = [&](auto half, auto from, auto to) __attribute__((always_inline)) {
+    constexpr int H = decltype(half)::value;
 #pragma unroll
-      for (int j = 0; j < MT; ++j) fx[j] = *reinterpret_cast<const i32x4*>(&lds[buf][ax + j * 16 * KS + at]);
-      if constexpr (decltype(tail)::value) {
+    for (int k = decltype(from)::value; k < decltype(to)::value; ++k) acc[k / MT][k % MT] = i8_mma(fw[H][k / MT], fx[H][k % MT], acc[k / MT][k % MT]);
+  };
+  constexpr int ALL = NT * MT, EARLY = ALL / 4;
+  auto copy = [&](int s, int buf) __attribute__((always_inline)) {
+    const uint32_t k0 = copy_at(s);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) fw[i] = i8_head(fw[i], k0 + 64 * kk + 16 * g, p.K);
-      }
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) acc[i][j] = i8_mma(fw[i], fx[j], acc[i][j]);
-    }
+    for (int j = 0; j < C; ++j) copy_one(j, k0, buf);
   };
   copy(0, 0);
-  int buf = 0, k0 = 0;
-  for (; k0 + KS < p.K; k0 += KS, buf ^= 1) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's copies have landed
-    lds_barrier();                        // and everybody's; the other buffer is free
-    copy(k0 + KS, buf ^ 1);
-    products(k0, buf, std::false_type{});
-  }
-  __builtin_amdgcn_s_waitcnt(0x0F70);
+  copy(1, 1);
+  i8_landed<C>();
   lds_barrier();
-  if (k0 + KS > p.K) products(k0, buf, std::true_type{});
-  else products(k0, buf, std::false_type{});
-  const int n = n0 + wn * 16 * NT + 4 * NT * g;
-  float ws[4 * NT], bias[4 * NT];
+  read(0, ic<0>{});
+  int buf = 0;
+  for (int s = 0; s + 1 < steps; ++s) {
+    read(buf, ic<1>{});
+    products(ic<0>{}, ic<0>{}, ic<ALL>{});
+    i8_landed<0>();    // of the next step, this wave's copies; and its reads of this one are done
+    lds_barrier();     // and everybody's
+    copy(s + 2, buf);
+    buf ^= 1;
+    read(buf, ic<0>{});
+    products(ic<1>{}, ic<0>{}, ic<ALL>{});
+  }
+  read(buf, ic<1>{});
+  if (steps * KS > p.K) {
 #pragma unroll
-  for (int e = 0; e < 4 * NT; e += 4) {
-    float f[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (n + e < p.N) {
-      vec_load<float, 4>(p.ws + n + e, p.N - n - e, f);
-      if (p.bias) vec_load<float, 4>(p.bias + n + e, p.N - n - e, b);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ws[e + i] = f[i];
-      bias[e + i] = b[i];
+    for (int i = 0; i < NT; ++i) {
+      fw[0][i] = i8_head(fw[0][i], (steps - 1) * KS + 16 * g, p.K);
+      fw[1][i] = i8_head(fw[1][i], (steps - 1) * KS + 64 + 16 * g, p.K);
     }
   }
+  products(ic<0>{}, ic<0>{}, ic<ALL>{});
+  products(ic<1>{}, ic<0>{}, ic<ALL>{});
+  i8_landed<0>();   // no copy outlives the wave
+  constexpr int V = sizeof(T) == 2 ? 8 : 4;   // 16 bytes of y
+  auto leave = [&](auto all) __attribute__((always_inline)) {
+    constexpr bool WHOLE = decltype(all)::value;   // every n of the tile is there
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int m = m0 + wm * 16 * MT + 16 * j + c;
-    int a[4 * NT];
+    for (int e = 0; e < 4 * NT; e += V) {
+      const int n = n0 + wn * 16 * NT + 4 * NT * g + e, nd = WHOLE ? V : max(0, p.N - n);
+      float ws[V], bias[V];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < V; ++i) bias[i] = 0.f;
+      vec_load<float, V>(p.ws + n, nd, ws);
+      if (p.bias) vec_load<float, V>(p.bias + n, nd, bias);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[4 * i + e] = acc[i][j][e];
-    i8_leave<T, 4 * NT>(p, m, n, a, m < p.M ? p.xs[m] : 0.f, ws, bias);
-  }
+      for (int j = 0; j < MT; ++j) {
+        const int m = m0 + wm * 16 * MT + 16 * j + c;
+        if (m >= p.M) continue;
+        const float xs = p.xs[m];
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = (float)acc[(e + i) / 4][j][i % 4] * xs * ws[i] + bias[i];
+        vec_store<T, V>(static_cast<T*>(p.y) + (long)m * p.N + n, nd, f);
+      }
+    }
+  };
+  if (n0 + BN <= p.N) leave(std::true_type{});
+  else leave(std::false_type{});
 }
 
 #define QUANT_DISPATCH(CALL)                   \
@@ -311,28 +366,49 @@ hipError_t launch_quant_rows(DType dt, const QuantParams& p, hipStream_t st) {
   return dt == DType::BF16 ? quant_rows<bf16>(p, st) : quant_rows<float>(p, st);
 }
 
-template <typename T, int MT, int NT, int U>
-static void i8_few(const I8Params& p, hipStream_t st) {
-  hipLaunchKernelGGL((k_i8_few<T, MT, NT, U, 8>), dim3((p.N + 16 * NT - 1) / (16 * NT), (p.M + 16 * MT - 1) / (16 * MT)), dim3(512), 0, st, p);
+template <typename T, int MT, int NT, int ST>
+static void i8_some(const I8Params& p, hipStream_t st) {
+  hipLaunchKernelGGL((k_i8_some<T, MT, NT, ST>), dim3((unsigned)(((p.N + 16L * NT - 1) / (16 * NT)) * ((p.M + 16L * MT - 1) / (16 * MT)))), dim3(256), 0, st, p);
 }
 template <typename T, int BM, int BN, int WM, int WN>
 static void i8_many(I8Params p, hipStream_t st) {
   p.tm = (p.M + BM - 1) / BM;
   p.tn = (p.N + BN - 1) / BN;
   p.tiles = p.tm * p.tn;
-  p.group = 4;
   hipLaunchKernelGGL((k_i8_many<T, BM, BN, WM, WN>), dim3((p.tiles + 7) / 8 * 8), dim3(64 * WM * WN), 0, st, p);
 }
+// The variant with the shortest rounds: workgroups over compute units, rounded
+// up, times what a round takes (k = 4096, bf16, us beside the launch, which is
+// some 3 for all):
+//   x rows by weight rows    32 x 32   64 x 32   128 x 32   128 x 64   128 x 128   256 x 256
+//   a round                     6         7         8         12.5        20           57
+// Measured, us a call, 4096 -> 8192: 17 rows 9.3 (64 x 32: 9.8), 40 rows 10.0 (32
+// x 32: 14, 128 x 32: 11.3), 100 rows 12.5 (64 x 32: 17.4, 128 x 64: 16.5), 256
+// rows 18.1 (128 x 32: 26, 128 x 128: 24.9), 512 rows 27.8 (128 x 64: 33.5, 256 x
+// 256: 46), 1024 rows 41 (48), 2048 rows 62 (128 x 128: 80); 4096 -> 2048: 256
+// rows 7.8 (128 x 32: 11.3), 1024 rows 17.3 (64 x 32: 26, 128 x 128: 25).
 template <typename T>
 static hipError_t i8_matmul(const I8Params& p, hipStream_t st) {
   timing_before("matmul_i8", st);
-  auto tiles = [&](long bm, long bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
-  if (p.M <= 16) i8_few<T, 1, 1, 4>(p, st);
-  else if (p.M <= 32) i8_few<T, 2, 1, 4>(p, st);
-  else if (p.M <= 64) i8_few<T, 4, 1, 2>(p, st);
-  else if (p.M <= 128 || tiles(128, 128) < kComputeUnits) i8_few<T, 8, 2, 1>(p, st);
-  else if (tiles(256, 256) < kComputeUnits) i8_many<T, 128, 128, 2, 2>(p, st);
-  else i8_many<T, 256, 256, 2, 4>(p, st);
+  const struct { int bm, bn; float round; } kinds[] = {{32, 32, 6.f}, {64, 32, 7.f}, {128, 32, 8.f}, {128, 64, 12.5f}, {128, 128, 20.f}, {256, 256, 57.f}};
+  int best = 0;
+  float least = 0.f;
+  for (int k = 0; k < 6; ++k) {
+    const long tiles = ((p.M + kinds[k].bm - 1L) / kinds[k].bm) * ((p.N + kinds[k].bn - 1L) / kinds[k].bn);
+    const float cost = (float)((tiles + kComputeUnits - 1) / kComputeUnits) * kinds[k].round;
+    if (k == 0 || cost < least) {
+      best = k;
+      least = cost;
+    }
+  }
+  switch (best) {
+    case 0: i8_some<T, 2, 2, 6>(p, st); break;
+    case 1: i8_some<T, 4, 2, 4>(p, st); break;
+    case 2: i8_some<T, 8, 2, 3>(p, st); break;
+    case 3: i8_some<T, 8, 4, 3>(p, st); break;
+    case 4: i8_many<T, 128, 128, 2, 2>(p, st); break;
+    default: i8_many<T, 256, 256, 2, 4>(p, st);
+  }
   const hipError_t e = hipGetLastError();
   timing_after(st);
   return e;

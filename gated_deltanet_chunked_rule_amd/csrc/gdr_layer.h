@@ -123,7 +123,7 @@ struct I8Params {
   void* y;
   long x_stride, w_stride;
   int M, N, K;
-  int tm, tn, tiles, group;      // tiles of x and the weight, rows of tiles that are walked together
+  int tm, tn, tiles;             // tiles of x and the weight
 };
 
 hipError_t launch_conv_fwd(DType dt, int W, const ConvParams& p, hipStream_t st);

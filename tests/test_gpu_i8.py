@@ -61,6 +61,13 @@ PRODUCTS = [
     (1025, 4097, 100, F32, True),
     (2100, 2050, 500, F32, False),
     (4096, 4096, 200, BF, True),        # tiles of 256
+    # each shape of a workgroup's tile with ends in it
+    (40, 8150, 70, BF, True),
+    (100, 8100, 200, F32, False),
+    (250, 8150, 130, BF, False),
+    (500, 8100, 257, F32, True),
+    (4000, 4090, 300, BF, True),
+    (3990, 4085, 129, F32, False),
     (4100, 4099, 130, F32, True),
 ]
 
