@@ -203,7 +203,8 @@ constexpr uint32_t kLinEmpty = 0xffffffffu, kLinNan = 0x7fc00000u;
 // How often a wait looks.  Every wait ends long before that, as the tiles are
 // handed out in order and a tile leaves its own word before it waits for
 // those before it.  Only if another call clears the words meanwhile (two
-// calls that share a workspace) is it reached: the state is NaN then.
+// calls that share a workspace) is it reached, once a wave: the state is NaN
+// then.
 constexpr int kLinLooks = 1 << 18;
 __device__ __forceinline__ uint32_t lin_bits(float x) { return x != x ? kLinNan : __builtin_bit_cast(uint32_t, x); }
 __device__ __forceinline__ void lin_put(uint64_t* at, float P, float S) {
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_one(LinParams p) {
   for (int e = 0; e < kLinVec; ++e) A2[e] *= 1.4426950408889634f;
   const SeqFinder sf = seq_finder(p.s, cu_lds);
   __syncthreads();
-  int tile = __builtin_amdgcn_readfirstlane(ticket);
+  int tile = __builtin_amdgcn_readfirstlane(ticket), most = kLinLooks;
   for (int par = 0; tile < p.tiles; par ^= 1) {
     const int t0 = tile * TOK + w * TT;
     LinAgg& agg = aggs[par];
@@ -297,7 +298,11 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_one(LinParams p) {
         bool all = ve != kLinEmpty;
 #pragma unroll
         for (int k = 0; k < EACH; ++k) all &= (uint32_t)v[k] != kLinEmpty;
-        if (all || looks >= kLinLooks) break;
+        if (all) break;
+        if (looks >= most) {   // never again as long
+          most = 0;
+          break;
+        }
         __builtin_amdgcn_s_sleep(2);
       }
 #pragma unroll
@@ -469,7 +474,8 @@ __global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
           sigmoid_both(r[c], e[k][c], ne);
           sigmoid_both(i[c], j, nj);
           const float s2 = A2[c] * e[k][c], ak = __builtin_amdgcn_exp2f(s2), m2 = lin_factor2(s2, ak);
-          const float rm = m2 == 0.f ? 0.f : __builtin_amdgcn_rsqf(m2);
+          // 1 / m; none where m is zero or its square below the normal numbers, which the instruction takes as zero
+          const float rm = fabsf(m2) < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(m2);
           a[k][c] = ak;
           mj[k][c] = m2 * rm * j;
           b[k][c] = mj[k][c] * x[c];

@@ -380,13 +380,15 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const vo
  * are fp32; y is h rounded once. */
 typedef struct {
   int32_t B, T;               /* as in gdr_shape */
-  int32_t D;                  /* channels, at most 2^30 */
+  int32_t D;                  /* channels, at most 2^28 */
   int32_t num_seqs;           /* sequences in packed mode; ignored otherwise */
   gdr_dtype dtype;            /* of x, r, i, y and their gradients */
   int64_t x_stride, r_stride, i_stride;  /* elements between tokens (0: D) */
 } gdr_linear_scan_shape;
 
-/* Bytes of device workspace the forward needs (0 on invalid arguments). */
+/* Bytes of device workspace the forward needs (0 on invalid arguments).  Calls
+ * that overlap in time need workspaces of their own, as everywhere: tiles of one
+ * prompt tell each other through it how far they are. */
 size_t gdr_linear_scan_fwd_workspace_size(const gdr_linear_scan_shape* shape);
 
 /*   x, r, i                      [B, T, D], strided;  A [D] fp32

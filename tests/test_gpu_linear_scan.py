@@ -227,3 +227,51 @@ def test_two_streams_and_another_current_stream():
             got.append([gdr.gdr_linear_scan_fwd(x, r, i, A)[0] for _ in range(4)])
     torch.cuda.synchronize()
     assert all(torch.equal(t, want) for ts in got for t in ts)
+
+
+def test_no_tokens():
+    g = gen(15)
+    D = 40
+    for B, cu in ((3, None), (1, [0, 0, 0])):
+        N = B if cu is None else len(cu) - 1
+        e = torch.empty(B, 0, D, device="cuda")
+        A, h0, dht = cuda(-torch.rand(D, generator=g)), cuda(randn(g, N, D)), cuda(randn(g, N, D))
+        y, ht = gdr.gdr_linear_scan_fwd(e, e, e, A, h0, cu, output_final_state=True)
+        assert y.shape == e.shape and torch.equal(ht, h0)
+        dx, dr, di, dA, dh0 = gdr.gdr_linear_scan_bwd(e, e, e, A, e, h0, dht, cu)
+        assert dx.shape == dr.shape == di.shape == e.shape and not dA.any() and torch.equal(dh0, dht)
+        assert not gdr.gdr_linear_scan_fwd(e, e, e, A, None, cu, output_final_state=True)[1].any()
+
+
+def test_squares_below_the_normal_numbers():
+    """1 - a^2 of 2e-39 and less: the factor counts as zero, and no gradient becomes infinite."""
+    g = gen(16)
+    x, i, dy = (randn(g, 1, 40, 12) for _ in range(3))
+    r = torch.full((1, 40, 12), -21.0)
+    for rate in (-1e-30, -1e-38, -1e-25):
+        A = torch.full((12,), rate)
+        got = gdr.gdr_linear_scan_fwd(*(cuda(t) for t in (x, r, i, A)))[0], *gdr.gdr_linear_scan_bwd(*(cuda(t) for t in (x, r, i, A)), cuda(dy))[:4]
+        assert all(bool(torch.isfinite(t).all()) for t in got), rate
+        assert float(got[0].abs().max()) <= 1e-15 and float(got[1].abs().max()) <= 1e-14
+
+
+@pytest.mark.parametrize("dtype,T,D", [(BF, 3000, 300), (F32, 1300, 514), (BF, 9000, 32)])
+def test_a_workspace_of_any_content_serves_call_after_call(dtype, T, D):
+    g = gen(17)
+    shape = gdr.layer._LinearScanShape(1, T, D, 1, 0 if dtype == BF else 1, 0, 0, 0)
+    n = [gdr.layer._bytes(f"gdr_linear_scan_{k}_workspace_size", shape) for k in ("fwd", "bwd")]
+    kept = [torch.randint(0, 256, (m,), dtype=torch.uint8, device="cuda") for m in n]
+    A = cuda(-torch.rand(D, generator=g))
+    for k in range(8):
+        x, r, i, dy = (cuda(randn(gen(100 * k + j), 1, T, D, dtype=dtype)) for j in range(4))
+        y, ht = gdr.gdr_linear_scan_fwd(x, r, i, A, output_final_state=True, workspace=kept[0])
+        grads = gdr.gdr_linear_scan_bwd(x, r, i, A, dy, workspace=kept[1])
+        fresh = [torch.full((m,), 255 * (k % 2), dtype=torch.uint8, device="cuda") for m in n]
+        want = gdr.gdr_linear_scan_fwd(x, r, i, A, output_final_state=True, workspace=fresh[0])
+        assert torch.equal(y, want[0]) and torch.equal(ht, want[1])
+        for a, b in zip(grads[:4], gdr.gdr_linear_scan_bwd(x, r, i, A, dy, workspace=fresh[1])):
+            assert torch.equal(a, b)
+    cpu = [t.cpu() for t in (x, r, i)]
+    ry, rye, rh, rhe, _, _ = ref.linear_scan(*(t[..., :8] for t in cpu), A.cpu()[:8])
+    check(y[..., :8].contiguous(), ry, rye, "y")
+    check(ht[:, :8].contiguous(), rh, rhe, "final state")
