@@ -19,6 +19,7 @@ constexpr float kFresh = -1.f;   // in the place of a product of decays: the end
 constexpr int kLinVec = 2;       // channels a lane
 constexpr int kLinCh = 64 * kLinVec;
 typedef float lin_v __attribute__((ext_vector_type(kLinVec)));
+constexpr int kLinJoinCh = 16;
 
 // 1 - a^2 with a = exp(s), s = s2 ln 2: -expm1(2 s).  Near zero the difference
 // would lose all bits: below 2 |s| = 1/4 the Taylor series up to z^6 / 720 (the
@@ -374,13 +375,15 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_tile(LinParams p) {
 }
 
 // The tiles' (P, S) turned into the states at their ends, and Q into what the
-// tiles hand on: 16 channels by 64 strands of consecutive tiles a workgroup, so
-// that a strand's loads are few and all compute units take part (171 tiles of
-// 1024 channels with 64 channels by 16 strands: 12 us, so 9.5).
+// tiles hand on: 16 channels by 64 strands of consecutive tiles a workgroup, and
+// the two workgroups that share cache lines on one XCD (683 tiles of 4096
+// channels: 21 us; on two XCDs 34, 32 channels by 32 strands 27, and with a
+// strand's tiles kept in registers between its walks 36).
 __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
-  constexpr int CH = 16, ST = 1024 / CH;
+  constexpr int CH = kLinJoinCh, ST = 1024 / CH;
   __shared__ float lp[ST][CH], ls[ST][CH], lq[ST][CH];
-  const int c = threadIdx.x % CH, u = threadIdx.x / CH, d = blockIdx.x * CH + c;
+  const int c = threadIdx.x % CH, u = threadIdx.x / CH;
+  const int y = blockIdx.x >> 3, d = ((y >> 1) * 16 + (blockIdx.x & 7) * 2 + (y & 1)) * CH + c;
   const int per = (p.tiles + ST - 1) / ST, j0 = min(u * per, p.tiles), j1 = min(j0 + per, p.tiles);
   const bool live = d < p.D;
   const float* P = p.P + d;
@@ -429,7 +432,7 @@ __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
 // OUT false: what each tile does to the state (P, S) and to its gradient (P, Q:
 // what it hands on to the tile before it, from zero).  Both directions cannot
 // be had in one pass, as tiles would wait for each other.  32768 x 4096 in bf16:
-// 236 us (4.5 TB/s), the join 34, this pass 378 (5.0 TB/s), dA 11.  With eight
+// 236 us (4.5 TB/s), the join 21, this pass 380 (4.9 TB/s), dA 11.  With eight
 // tokens a wave one workgroup of 152 registers is resident and not two (475); in
 // workgroups of four waves 355, and the shorter tiles' joins take that again.
 // Values made again for the walk backwards instead of held took 643.
@@ -679,7 +682,7 @@ static hipError_t lin_bwd(const LinParams& p, hipStream_t st) {
 #define CALL(OUT) (p.D < kLinVec ? k_lin_bwd<T, kLinBwdWaves, kLinBwdTok, OUT, true> : k_lin_bwd<T, kLinBwdWaves, kLinBwdTok, OUT, false>)
   if (p.tiles > 1) {
     if (hipError_t e = lin_launch("linear_scan_bwd_parts", CALL(false), grid, block, p, st)) return e;
-    if (hipError_t e = lin_launch("linear_scan_bwd_join", k_lin_join, dim3((p.D + 15) / 16), dim3(1024), p, st)) return e;
+    if (hipError_t e = lin_launch("linear_scan_bwd_join", k_lin_join, dim3((p.D + 16 * kLinJoinCh - 1) / (16 * kLinJoinCh) * 16), dim3(1024), p, st)) return e;
   }
   if (hipError_t e = lin_launch("linear_scan_bwd", CALL(true), grid, block, p, st)) return e;
 #undef CALL
