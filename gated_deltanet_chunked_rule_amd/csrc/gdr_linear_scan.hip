@@ -392,10 +392,10 @@ __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
   if (live) {
 #pragma unroll 4
     for (int j = j0; j < j1; ++j) {
-      const float pj = P[(long)j * p.D];
+      const float pj = P[(long)j * p.D], sj = S[(long)j * p.D], gj = Q[(long)j * p.D];
       // what a later run hands on goes through this one's decays (kFresh: not at all)
-      g = q == kFresh ? g : fmaf(q, Q[(long)j * p.D], g);
-      lin_join(q, s, pj, S[(long)j * p.D]);
+      g = q == kFresh ? g : fmaf(q, gj, g);
+      lin_join(q, s, pj, sj);
     }
   }
   lp[u][c] = q;
@@ -408,7 +408,8 @@ __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
   for (int v = 0; v < u; ++v) h = lin_after(h, lp[v][c], ls[v][c]);
 #pragma unroll 4
   for (int j = j0; j < j1; ++j) {
-    h = lin_after(h, P[(long)j * p.D], S[(long)j * p.D]);
+    const float pj = P[(long)j * p.D], sj = S[(long)j * p.D];
+    h = lin_after(h, pj, sj);
     S[(long)j * p.D] = h;
   }
   g = 0.f;
@@ -416,7 +417,8 @@ __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
   for (int v = ST - 1; v > u; --v) g = lin_after(g, lp[v][c], lq[v][c]);
 #pragma unroll 4
   for (int j = j1 - 1; j >= j0; --j) {
-    g = lin_after(g, P[(long)j * p.D], Q[(long)j * p.D]);
+    const float pj = P[(long)j * p.D], gj = Q[(long)j * p.D];
+    g = lin_after(g, pj, gj);
     Q[(long)j * p.D] = g;
   }
 }
