@@ -216,13 +216,13 @@ __global__ __launch_bounds__(256) void k_i8_some(I8Params p) {
 // ((r % 16) / 4) + 4 (r / 16) + r % 4, so that a lane's values of one m over its
 // NT tiles are 4 NT consecutive n.
 //
-// 8192 x 4096 -> 8192: 249 us (2.2e15 operations a second), 8192^3 431 (2.55e15),
-// where the clock gives way under the load; a tile's first copies and its
-// outputs are the rest.  With the operands read where they are used 304; steps of
-// 64 k in four buffers 346 (rows of 64 bytes are read at half the rate); copies
-// between the products, or behind an earlier second barrier, 273 and 265;
-// persistent workgroups with the next tile's first copies ahead of the outputs
-// 272; waves of 64 x 128 288.
+// 8192 x 4096 -> 8192: 235 us (2.35e15 operations a second), 8192^3 420 (2.6e15);
+// a tile's first copies and its outputs are the rest.  Of its variants, where
+// this loop took 249: operands read where they are used 304; steps of 64 k in
+// four buffers 346 (rows of 64 bytes are read at half the rate); copies between
+// the products, or behind an earlier second barrier, 273 and 265; persistent
+// workgroups with the next tile's first copies ahead of the outputs 272; waves of
+// 64 x 128 288.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
   constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16, KS = 128;
@@ -311,26 +311,35 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
   products(ic<0>{}, ic<0>{}, ic<ALL>{});
   products(ic<1>{}, ic<0>{}, ic<ALL>{});
   i8_landed<0>();   // no copy outlives the wave
+  // a lane's 4 NT values of a row one after another, so that cache lines fill at
+  // once (in two turns of 16 bytes each was written twice: 267 MB for 134)
   constexpr int V = sizeof(T) == 2 ? 8 : 4;   // 16 bytes of y
   auto leave = [&](auto all) __attribute__((always_inline)) {
     constexpr bool WHOLE = decltype(all)::value;   // every n of the tile is there
+    const int n = n0 + wn * 16 * NT + 4 * NT * g;
+    float ws[4 * NT], bias[4 * NT];
 #pragma unroll
-    for (int e = 0; e < 4 * NT; e += V) {
-      const int n = n0 + wn * 16 * NT + 4 * NT * g + e, nd = WHOLE ? V : max(0, p.N - n);
-      float ws[V], bias[V];
+    for (int e = 0; e < 4 * NT; e += 4) {
+      float f[4], h[4] = {0.f, 0.f, 0.f, 0.f};
+      vec_load<float, 4>(p.ws + n + e, WHOLE ? 4 : max(0, p.N - n - e), f);
+      if (p.bias) vec_load<float, 4>(p.bias + n + e, WHOLE ? 4 : max(0, p.N - n - e), h);
 #pragma unroll
-      for (int i = 0; i < V; ++i) bias[i] = 0.f;
-      vec_load<float, V>(p.ws + n, nd, ws);
-      if (p.bias) vec_load<float, V>(p.bias + n, nd, bias);
+      for (int i = 0; i < 4; ++i) {
+        ws[e + i] = f[i];
+        bias[e + i] = h[i];
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const int m = m0 + wm * 16 * MT + 16 * j + c;
-        if (m >= p.M) continue;
-        const float xs = p.xs[m];
+    for (int j = 0; j < MT; ++j) {
+      const int m = m0 + wm * 16 * MT + 16 * j + c;
+      if (m >= p.M) continue;
+      const float xs = p.xs[m];
+#pragma unroll
+      for (int e = 0; e < 4 * NT; e += V) {
         float f[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = (float)acc[(e + i) / 4][j][i % 4] * xs * ws[i] + bias[i];
-        vec_store<T, V>(static_cast<T*>(p.y) + (long)m * p.N + n, nd, f);
+        for (int i = 0; i < V; ++i) f[i] = (float)acc[(e + i) / 4][j][i % 4] * xs * ws[e + i] + bias[e + i];
+        vec_store<T, V>(static_cast<T*>(p.y) + (long)m * p.N + n + e, WHOLE ? V : p.N - n - e, f);
       }
     }
   };
