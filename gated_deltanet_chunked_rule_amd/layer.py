@@ -573,8 +573,8 @@ def gdr_linear_scan_fwd(x, r, i, A, initial_state=None, cu_seqlens=None, *, outp
         _no_gradient("gdr_linear_scan_fwd", "linear_scan")
     sh, ptrs, cu, N, dev = _linear_scan_args(x, r, i, A, cu_seqlens)
     hp = _dense(initial_state, "initial_state", (N, sh.D), torch.float32, dev)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
-    ht = torch.empty((N, sh.D), device=dev, dtype=torch.float32) if output_final_state else None
+    y = torch.empty(*x.shape, device=dev, dtype=x.dtype)
+    ht = torch.empty(N, sh.D, device=dev, dtype=torch.float32) if output_final_state else None
     ws = _workspace(workspace, _bytes("gdr_linear_scan_fwd_workspace_size", sh), dev)
     _call(dev, _entry("gdr_linear_scan_fwd"), sh, *ptrs, hp, _ptr(cu), y.data_ptr(), _ptr(ht), ws.data_ptr(), ws.numel())
     return y, ht
@@ -694,8 +694,8 @@ def gdr_block_norm_fwd(x, post_weight, residual, pre_weight, gate=None, scale=No
                             or (gate is not None and gate.requires_grad) or (scale is not None and scale.requires_grad)):
         _no_gradient("gdr_block_norm_fwd", "block_norm")
     sh, ptrs, dev = _block_norm_args(x, post_weight, residual, pre_weight, gate, scale, eps, "residual")
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
-    h = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    y = torch.empty(*x.shape, device=dev, dtype=x.dtype)
+    h = torch.empty_like(y)
     _call(dev, _entry("gdr_block_norm_fwd"), sh, *ptrs, y.data_ptr(), h.data_ptr())
     return y, h
 
@@ -757,8 +757,8 @@ def gdr_quantize_rows(x):
     code, dev = _code(x), x.get_device()
     xp, xs = _flat_rows(x, "x", shape, x.dtype, dev)
     pad = -(-K // 16) * 16
-    q = torch.empty((*shape[:-1], pad), device=dev, dtype=torch.int8)
-    scales = torch.empty(shape[:-1], device=dev, dtype=torch.float32)
+    q = torch.empty(*shape[:-1], pad, device=dev, dtype=torch.int8)
+    scales = torch.empty(*shape[:-1], device=dev, dtype=torch.float32) if x.dim() > 1 else torch.empty((), device=dev)
     _call(dev, _entry("gdr_quantize_rows"), _QuantizeShape(x.numel() // K, K, code, xs, pad), xp, q.data_ptr(), scales.data_ptr())
     return (q if pad == K else q[..., :K]), scales
 
@@ -802,6 +802,6 @@ def gdr_matmul_i8(q, scales, weight, weight_scales, bias=None, *, dtype=torch.bf
     sp = _dense(scales, "scales", shape[:-1], torch.float32, dev)
     wsp = _dense(weight_scales, "weight_scales", (N,), torch.float32, dev)
     bp = _dense(bias, "bias", (N,), torch.float32, dev)
-    y = torch.empty((*shape[:-1], N), device=dev, dtype=dtype)
+    y = torch.empty(*shape[:-1], N, device=dev, dtype=dtype)
     _call(dev, _entry("gdr_matmul_i8"), _MatmulI8Shape(q.numel() // K, N, K, code, qs, ws), qp, sp, wp, wsp, bp, y.data_ptr())
     return y

@@ -125,6 +125,16 @@ def test_leading_dimensions_no_rows_and_strided_rows():
     assert gdr.gdr_matmul_i8(q, s, w, ws).shape == (0, 3, 50)
 
 
+def test_one_row_without_a_leading_dimension():
+    g = gen(8)
+    x, (w, ws) = cuda(randn(g, 100)), gdr.gdr_quantize_rows(cuda(randn(g, 30, 100)))
+    q, s = gdr.gdr_quantize_rows(x)
+    assert q.shape == (100,) and s.shape == () and s.dtype == F32
+    y = gdr.gdr_matmul_i8(q, s, w, ws, dtype=F32)
+    q2, s2 = gdr.gdr_quantize_rows(x[None])
+    assert y.shape == (30,) and torch.equal(y, gdr.gdr_matmul_i8(q2, s2, w, ws, dtype=F32)[0])
+
+
 def test_captured_projection_replays():
     g = gen(7)
     x, W = cuda(randn(g, 40, 512, dtype=BF)), cuda(randn(g, 300, 512, dtype=BF))
