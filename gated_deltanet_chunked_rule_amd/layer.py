@@ -758,7 +758,7 @@ def gdr_quantize_rows(x):
     xp, xs = _flat_rows(x, "x", shape, x.dtype, dev)
     pad = -(-K // 16) * 16
     q = torch.empty(*shape[:-1], pad, device=dev, dtype=torch.int8)
-    scales = torch.empty(*shape[:-1], device=dev, dtype=torch.float32) if x.dim() > 1 else torch.empty((), device=dev)
+    scales = torch.empty(shape[:-1], device=dev, dtype=torch.float32)
     _call(dev, _entry("gdr_quantize_rows"), _QuantizeShape(x.numel() // K, K, code, xs, pad), xp, q.data_ptr(), scales.data_ptr())
     return (q if pad == K else q[..., :K]), scales
 

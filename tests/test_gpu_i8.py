@@ -135,6 +135,18 @@ def test_one_row_without_a_leading_dimension():
     assert y.shape == (30,) and torch.equal(y, gdr.gdr_matmul_i8(q2, s2, w, ws, dtype=F32)[0])
 
 
+def test_scales_are_fp32_whatever_the_default_type():
+    x = cuda(randn(gen(9), 100, dtype=BF))
+    q, s = gdr.gdr_quantize_rows(x)
+    torch.set_default_dtype(torch.float64)
+    try:
+        for v in (x, x[None]):
+            q1, s1 = gdr.gdr_quantize_rows(v)
+            assert s1.dtype == F32 and torch.equal(q1.flatten(), q) and torch.equal(s1.flatten()[0], s)
+    finally:
+        torch.set_default_dtype(torch.float32)
+
+
 def test_captured_projection_replays():
     g = gen(7)
     x, W = cuda(randn(g, 40, 512, dtype=BF)), cuda(randn(g, 300, 512, dtype=BF))
