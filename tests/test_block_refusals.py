@@ -197,3 +197,19 @@ def test_row_strides():
     raises("multiples of 16", layer._i8_rows, on_device(torch.zeros(5, 33, dtype=torch.int8)), "q", (5, 33), 0)
     short = on_device(torch.zeros(4 * 48 + 33, dtype=torch.int8).as_strided((5, 33), (48, 1)))
     raises("storage must reach", layer._i8_rows, short, "q", (5, 33), 0)
+
+
+def test_sizes_that_32_bits_cannot_hold():
+    m = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="meta").as_subclass(OnDevice)  # noqa: E731
+    n = 2 ** 32 + 8                                     # its low 32 bits are a size that would be taken
+    x, A = m(1, n, 8), m(8, dtype=torch.float32)
+    raises("T must be below", gdr.gdr_linear_scan_fwd, x, x, x, A)
+    raises("T must be below", gdr.gdr_linear_scan_bwd, x, x, x, A, x)
+    raises("rows must be below", gdr.gdr_linear_scan_step, x[0], x[0], x[0], A, m(n, 8, dtype=torch.float32))
+    x, w = m(2, n), m(n)
+    raises("dim must be below", gdr.gdr_block_norm_fwd, x, w, x, w)
+    raises("dim must be below", gdr.gdr_block_norm_bwd, x, w, x, w, x)
+    raises("K must be below", gdr.gdr_quantize_rows, x)
+    q, s, w = m(n, 16, dtype=torch.int8), m(n, dtype=torch.float32), m(8, 16, dtype=torch.int8)
+    raises("M must be below", gdr.gdr_matmul_i8, q, s, w, m(8, dtype=torch.float32))
+    raises("N must be below", gdr.gdr_matmul_i8, w, m(8, dtype=torch.float32), q, s)
