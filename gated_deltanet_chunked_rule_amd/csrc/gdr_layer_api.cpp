@@ -160,7 +160,8 @@ gdr_status lin_check(const gdr_linear_scan_shape* sh, bool packed) {
   if (!sh) return invalid("shape is NULL");
   if (gdr_status st = check_tokens(sh->B, sh->T, packed, sh->num_seqs, sh->dtype)) return st;
   if (sh->D < 1) return invalid("D must be positive");
-  if (sh->D > (1 << 28)) return unsupported("D must be at most 2^28");   // a row of 64-bit words lies within 2^32 bytes
+  // the gradient's join starts 64 threads a channel, and a row of 64-bit words lies within 2^32 bytes
+  if (sh->D > (1 << 25)) return unsupported("D must be at most 2^25");
   const int64_t st[3] = {sh->x_stride, sh->r_stride, sh->i_stride};
   for (int64_t s : st)
     if (s != 0 && s < sh->D) return invalid("a token stride is smaller than its row");

@@ -380,7 +380,7 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const vo
  * are fp32; y is h rounded once. */
 typedef struct {
   int32_t B, T;               /* as in gdr_shape */
-  int32_t D;                  /* channels, at most 2^28 */
+  int32_t D;                  /* channels, at most 2^25 */
   int32_t num_seqs;           /* sequences in packed mode; ignored otherwise */
   gdr_dtype dtype;            /* of x, r, i, y and their gradients */
   int64_t x_stride, r_stride, i_stride;  /* elements between tokens (0: D) */

@@ -25,7 +25,7 @@ BWD = [P[0], P[1], P[2], P[3], None, None, P[4], None, P[5], P[6], P[7], P[8], N
 
 @pytest.mark.parametrize("kw,rc,msg", [
     (dict(B=0), -1, "B must be positive"), (dict(T=-1), -1, "T not negative"), (dict(D=0), -1, "D must be positive"),
-    (dict(D=2 ** 28 + 1), -2, "2^28"), (dict(dtype=2), -2, "dtype"), (dict(xs=15), -1, "smaller"), (dict(rs=-16), -1, "smaller"),
+    (dict(D=2 ** 25 + 1), -2, "2^25"), (dict(dtype=2), -2, "dtype"), (dict(xs=15), -1, "smaller"), (dict(rs=-16), -1, "smaller"),
     (dict(ist=1), -1, "smaller"), (dict(T=2 ** 31 - 1), -2, "too many tokens"), (dict(T=2 ** 24, D=2 ** 20), -2, "too many tokens times channels"),
 ])
 def test_linear_scan_refuses(kw, rc, msg):

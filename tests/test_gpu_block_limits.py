@@ -43,6 +43,22 @@ def test_linear_scan_beyond_32_bits():
         check(some(t), value, bound)
 
 
+def test_linear_scan_of_the_most_channels():
+    T, D = 50, 2 ** 25
+    x = big(T, D, 7)[None]
+    A = torch.full((D,), -0.5, device="cuda")
+    cols = torch.tensor([0, 1, 2 ** 24 + 77, D - 1], device="cuda")
+    some = lambda t: t[..., cols]  # noqa: E731
+    y, _ = gdr.gdr_linear_scan_fwd(x, x, x, A)
+    v, a = some(x).cpu(), some(A).cpu()
+    ry, rye, _, _, _, _ = ref.linear_scan(v, v, v, a)
+    check(some(y), ry, rye, "y")
+    del y
+    grads = gdr.gdr_linear_scan_bwd(x, x, x, A, x)
+    for t, (value, bound) in zip(grads[:4], ref.linear_scan_bwd(v, v, v, a, v)):
+        check(some(t), value, bound)
+
+
 def test_block_norm_beyond_32_bits():
     rows, dim = 131200, 16384                # 2.15e9 values
     x = big(rows, dim, 3)
