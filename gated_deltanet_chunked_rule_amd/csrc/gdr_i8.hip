@@ -395,17 +395,18 @@ static void i8_many(I8Params p, hipStream_t st) {
 // x 32: 14, 128 x 32: 11.3), 100 rows 12.5 (64 x 32: 17.4, 128 x 64: 16.5), 256
 // rows 18.1 (128 x 32: 26, 128 x 128: 24.9), 512 rows 27.8 (128 x 64: 33.5, 256 x
 // 256: 46), 1024 rows 41 (48), 2048 rows 62 (128 x 128: 80); 4096 -> 2048: 256
-// rows 7.8 (128 x 32: 11.3), 1024 rows 17.3 (64 x 32: 26, 128 x 128: 25).
+// rows 7.8 (128 x 32: 11.3), 1024 rows 17.3 (64 x 32: 26, 128 x 128: 25).  A
+// launch is below 2^32 threads: from 2^29 columns on small tiles are none.
 template <typename T>
 static hipError_t i8_matmul(const I8Params& p, hipStream_t st) {
   timing_before("matmul_i8", st);
   const struct { int bm, bn; float round; } kinds[] = {{32, 32, 6.f}, {64, 32, 7.f}, {128, 32, 8.f}, {128, 64, 12.5f}, {128, 128, 20.f}, {256, 256, 57.f}};
-  int best = 0;
-  float least = 0.f;
+  int best = 5;
+  float least = __builtin_inff();
   for (int k = 0; k < 6; ++k) {
     const long tiles = ((p.M + kinds[k].bm - 1L) / kinds[k].bm) * ((p.N + kinds[k].bn - 1L) / kinds[k].bn);
     const float cost = (float)((tiles + kComputeUnits - 1) / kComputeUnits) * kinds[k].round;
-    if (k == 0 || cost < least) {
+    if (tiles * 256 < 1L << 32 && cost < least) {
       best = k;
       least = cost;
     }

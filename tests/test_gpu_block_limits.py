@@ -90,6 +90,16 @@ def test_product_beyond_32_bits():
     assert torch.equal(qx[-2:].cpu(), rq) and torch.equal(sx[-2:].cpu(), rs)
 
 
+def test_product_of_the_most_columns():
+    N, K = 2 ** 29, 16
+    g = torch.Generator(device="cuda").manual_seed(8)
+    w = torch.randint(-128, 128, (N // 8, K * 8), generator=g, device="cuda", dtype=torch.int8).view(N, K)
+    q, s, ws = w[5:6], torch.full((1,), 0.25, device="cuda"), torch.full((N,), 0.5, device="cuda")
+    y = gdr.gdr_matmul_i8(q, s, w, ws)
+    for at in (slice(0, 300), slice(2 ** 28 - 9, 2 ** 28 + 9), slice(N - 300, N)):
+        check(y[:, at], *ref.matmul_i8(q, s, w[at], ws[at]))
+
+
 def test_h_takes_the_residuals_place():
     g = gen(6)
     for rows, dim in ((37, 100), (9, 4096), (300, 128)):

@@ -57,10 +57,10 @@ PRODUCTS = [
     (100, 1000, 600, F32, True),
     (129, 300, 257, BF, True),
     (300, 64, 1024, BF, False),
-    (1000, 2100, 384, BF, True),        # tiles of 128
+    (1000, 2100, 384, BF, True),
     (1025, 4097, 100, F32, True),
     (2100, 2050, 500, F32, False),
-    (4096, 4096, 200, BF, True),        # tiles of 256
+    (4096, 4096, 200, BF, True),
     # each shape of a workgroup's tile with ends in it
     (40, 8150, 70, BF, True),
     (100, 8100, 200, F32, False),
