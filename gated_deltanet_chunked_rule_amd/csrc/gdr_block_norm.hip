@@ -9,12 +9,16 @@
 // 8 values each), so every operand is read once and the row's two sums need
 // nothing from memory.  Sums are fp32 over unrounded values; y is made from the
 // unrounded h.
+//
+// 16384 x 4096 in bf16 with gate and scale: 121 us (5.5 TB/s; a copy moves 5.2),
+// the gradient 208 (5.2) with its sums of partial rows 9; 64 rows 8.5 a call.
 #include "gdr_layer.h"
 
 namespace gdr {
 
-// Sums of N values over the TPR lanes of a row (a power of two, 16 to 1024),
-// the same on every lane; rows of more than a wave meet in LDS.
+// Sums of N values over the lanes of a row, the same on every lane: TPR lanes up
+// to 256 (a power of two), the whole workgroup (of up to TPR lanes) from 512 on.
+// Rows of more than a wave meet in LDS.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&a)[N], float (*lds)[N]) {
 #pragma unroll
@@ -29,23 +33,38 @@ __device__ __forceinline__ void row_sums(float (&a)[N], float (*lds)[N]) {
 #pragma unroll
       for (int i = 0; i < N; ++i) lds[w][i] = a[i];
     lds_barrier();
-    const int first = (threadIdx.x / TPR) * (TPR / 64);
+    if constexpr (TPR > 256) {
+      const int u = threadIdx.x & 15;   // up to 16 waves: one a lane
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      a[i] = 0.f;
+      for (int i = 0; i < N; ++i) a[i] = row16_sum(u < (int)(blockDim.x >> 6) ? lds[u][i] : 0.f);
+    } else {
+      const int first = (threadIdx.x / TPR) * (TPR / 64);
 #pragma unroll
-      for (int j = 0; j < TPR / 64; ++j) a[i] += lds[first + j][i];
+      for (int i = 0; i < N; ++i) {
+        a[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < TPR / 64; ++j) a[i] += lds[first + j][i];
+      }
     }
   }
 }
+// Values from d on: one 32-bit offset in a register for all rows.
+template <typename T, typename V> __device__ __forceinline__ T* values_at(V* row, int d) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
+  return reinterpret_cast<T*>(reinterpret_cast<byte*>(row) + (uint32_t)d * (uint32_t)sizeof(T));
+}
+// A thread's place in its row, its row in the workgroup, and the lanes of a row.
+template <int TPR> __device__ __forceinline__ int row_lane() { return TPR > 256 ? threadIdx.x : threadIdx.x & (TPR - 1); }
+template <int TPR> __device__ __forceinline__ int row_sub() { return TPR > 256 ? 0 : threadIdx.x / TPR; }
+template <int TPR> __device__ __forceinline__ int row_lanes() { return TPR > 256 ? blockDim.x : TPR; }
 
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockNormParams p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
   typedef typename VecIO<T, 8>::raw raw_t;
   __shared__ float red[2][NT / 64][1];
-  const int t = threadIdx.x & (TPR - 1);
-  const long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
+  const int t = row_lane<TPR>(), lanes = row_lanes<TPR>();
+  const long row = (long)blockIdx.x * RPB + row_sub<TPR>();
   const bool live = row < p.rows;   // rows behind the last read row 0 and write nothing
   const long rr = live ? row : 0;
   const T* x = static_cast<const T*>(p.x) + rr * p.x_stride;
@@ -54,7 +73,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockN
   raw_t xr[NV], sr[NV], zr[NV], wr[NV], cr[NV], vr[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int d = (v * TPR + t) * 8, nd = max(0, p.dim - d);
+    const int d = (v * lanes + t) * 8, nd = max(0, p.dim - d);
     xr[v] = vec_raw<T, 8>(x + d, nd);
     sr[v] = vec_raw<T, 8>(res + d, nd);
     if (p.gate) zr[v] = vec_raw<T, 8>(gate + d, nd);
@@ -101,7 +120,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockN
   const float rh = __builtin_amdgcn_rsqf(fmaf(ss[0], p.inv_dim, p.eps));
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+    const int d = (v * lanes + t) * 8, nd = min(8, p.dim - d);
     if (!live || nd <= 0) continue;
     float w[8];
     VecIO<T, 8>::up(vr[v], w);
@@ -119,6 +138,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockN
 //   dw_pre = sum dy n,  dw_post = sum dp q,  dscale = sum dh q w_post c
 // Persistent workgroups keep the three vectors' sums in registers and leave one
 // partial row of each.
+// Values as they were loaded: what was made of them before is made again and not
+// held in registers.
+__device__ __forceinline__ void as_loaded(VecIO<bf16, 8>::raw& r) { asm volatile("" : "+v"(r)); }
+__device__ __forceinline__ void as_loaded(VecIO<float, 8>::raw& r) { asm volatile("" : "+v"(r.a), "+v"(r.b)); }
+
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockNormParams p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
@@ -126,41 +150,69 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
   __shared__ float red3[2][NT / 64][3];
   __shared__ float red1[2][NT / 64][1];
   __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NV * 8 : 1];
-  const int t = threadIdx.x & (TPR - 1), sub = threadIdx.x / TPR;
+  // From 8193 values on a lane has 128 registers.  LDS holds the sums of two of
+  // the vectors, and row and vectors are read again (from L2) where they are used
+  // a second time: 4096 x 16384 in bf16 411 us, 1516 with all of it in registers
+  // (736 bytes a lane spilled), 2048 x 16384 in fp32 336 and 805.
+  constexpr bool BIG = TPR == 1024;
+  __shared__ f32x4 far[BIG ? 2 * NV : 1][2][BIG ? TPR : 1];   // [sum and vector][half][lane]
+  const int t = row_lane<TPR>(), sub = row_sub<TPR>(), lanes = row_lanes<TPR>();
   const bool gate = p.gate != nullptr, scale = p.scale != nullptr, dres = p.dres != nullptr;
   raw_t post[NV], pre[NV], sc[NV];
   float dpost[NV][8], dpre[NV][8], dsc[NV][8];
+  auto vectors = [&](int v) __attribute__((always_inline)) {
+    const int d = (v * lanes + t) * 8, nd = max(0, p.dim - d);
+    post[v] = vec_raw<T, 8>(values_at<const T>(p.post, d), nd);
+    pre[v] = vec_raw<T, 8>(values_at<const T>(p.pre, d), nd);
+    sc[v] = vec_raw<T, 8>(values_at<const T>(p.scale, d), scale ? nd : 0);
+  };
+  // sums of a lane's own columns: no other lane reads or writes them
+  auto far_sum = [&](int k, const float (&f)[8]) __attribute__((always_inline)) {
+    far[k][0][t] += f32x4{f[0], f[1], f[2], f[3]};
+    far[k][1][t] += f32x4{f[4], f[5], f[6], f[7]};
+  };
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int d = (v * TPR + t) * 8, nd = max(0, p.dim - d);
-    post[v] = vec_raw<T, 8>(static_cast<const T*>(p.post) + d, nd);
-    pre[v] = vec_raw<T, 8>(static_cast<const T*>(p.pre) + d, nd);
-    if (scale) sc[v] = vec_raw<T, 8>(static_cast<const T*>(p.scale) + d, nd);
+    if constexpr (BIG) far[2 * v][0][t] = far[2 * v][1][t] = far[2 * v + 1][0][t] = far[2 * v + 1][1][t] = zero4();
+    else vectors(v);
 #pragma unroll
     for (int c = 0; c < 8; ++c) dpost[v][c] = dpre[v][c] = dsc[v][c] = 0.f;
   }
   int buf = 0;
   // every thread of the workgroup makes the same number of steps (barriers)
   for (long base = (long)blockIdx.x * RPB; base < p.rows; base += (long)gridDim.x * RPB, buf ^= 1) {
-    const long row = base + sub;
+    // a row of its own for the workgroup: in scalar registers, and not as one
+    // running address of 64 bits a lane for each tensor and vector
+    const long row = RPB == 1 ? (long)__builtin_amdgcn_readfirstlane((int)base) : base + sub;
     const bool live = row < p.rows;
     const long rr = live ? row : 0;
     const T* x = static_cast<const T*>(p.x) + rr * p.x_stride;
     const T* hh = static_cast<const T*>(p.h) + rr * p.r_stride;
     const T* z = static_cast<const T*>(p.gate) + rr * p.g_stride;
     raw_t xr[NV], hr[NV], yr[NV], zr[NV], sr[NV];
+    auto sums_of = [&](int v) __attribute__((always_inline)) {   // what the first sums take
+      const int d = (v * lanes + t) * 8, nd = max(0, p.dim - d);
+      hr[v] = vec_raw<T, 8>(values_at<const T>(hh, d), nd);
+      yr[v] = vec_raw<T, 8>(values_at<const T>(static_cast<const T*>(p.dy) + rr * p.dim, d), nd);
+      xr[v] = vec_raw<T, 8>(values_at<const T>(x, d), nd);
+    };
+    auto others = [&](int v) __attribute__((always_inline)) {
+      const int d = (v * lanes + t) * 8, nd = max(0, p.dim - d);
+      zr[v] = vec_raw<T, 8>(values_at<const T>(z, d), gate ? nd : 0);
+      sr[v] = vec_raw<T, 8>(values_at<const T>(static_cast<const T*>(p.dres) + rr * p.dim, d), dres ? nd : 0);
+    };
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int d = (v * TPR + t) * 8, nd = max(0, p.dim - d);
-      hr[v] = vec_raw<T, 8>(hh + d, nd);
-      yr[v] = vec_raw<T, 8>(static_cast<const T*>(p.dy) + rr * p.dim + d, nd);
-      xr[v] = vec_raw<T, 8>(x + d, nd);
-      if (gate) zr[v] = vec_raw<T, 8>(z + d, nd);
-      if (dres) sr[v] = vec_raw<T, 8>(static_cast<const T*>(p.dres) + rr * p.dim + d, nd);
+      sums_of(v);
+      if constexpr (!BIG) others(v);
     }
     float s3[3] = {0.f, 0.f, 0.f};   // h^2, u h, x^2
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      if constexpr (BIG) {
+        asm volatile("" ::: "memory");
+        vectors(v);
+      }
       float h[8], g[8], w[8], q[8];
       VecIO<T, 8>::up(hr[v], h);
       VecIO<T, 8>::up(yr[v], g);
@@ -179,54 +231,68 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
     float dh[NV][8], s1[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
-      float h[8], g[8], w[8], q[8], wp[8], s[8], k[8], zz[8];
+      const int d = (v * lanes + t) * 8, nd = min(8, p.dim - d);
+      if constexpr (BIG) vectors(v);
+      if constexpr (BIG) {
+        asm volatile("" ::: "memory");   // a second read, and not registers that hold the first
+        sums_of(v);
+        others(v);
+      } else if constexpr (TPR > 256) {
+        as_loaded(xr[v]);
+        as_loaded(hr[v]);
+        as_loaded(yr[v]);
+      }
+      float h[8], g[8], w[8], q[8], wp[8], s[8], k[8], z[8];
       VecIO<T, 8>::up(hr[v], h);
       VecIO<T, 8>::up(yr[v], g);
       VecIO<T, 8>::up(pre[v], w);
       VecIO<T, 8>::up(xr[v], q);
       VecIO<T, 8>::up(post[v], wp);
-      if (dres) VecIO<T, 8>::up(sr[v], s);
+      VecIO<T, 8>::up(sr[v], s);
+      VecIO<T, 8>::up(sc[v], k);
+      VecIO<T, 8>::up(zr[v], z);
+      float dz[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float n = h[c] * rh;
-        dh[v][c] = rh * (g[c] * w[c] - n * mh) + (dres ? s[c] : 0.f);
-        dpre[v][c] += live ? g[c] * n : 0.f;
-        q[c] *= rx;
+        // an absent vector counts as what leaves the others as they are, so that nothing here branches
+        const float n = h[c] * rh, qc = q[c] * rx, e = sigmoid_f(z[c]), kc = scale ? k[c] : 1.f, act = gate ? z[c] * e : 1.f;
+        const float f = rh * (g[c] * w[c] - n * mh) + s[c], qw = qc * wp[c], fq = f * qw;
+        dz[c] = fq * kc * (e * fmaf(z[c], 1.f - e, 1.f));
+        const float dp = f * act * kc;
+        dh[v][c] = f;
+        dpre[v][c] = (BIG ? 0.f : dpre[v][c]) + (live ? g[c] * n : 0.f);
+        dpost[v][c] = (BIG ? 0.f : dpost[v][c]) + (live ? dp * qc : 0.f);
+        dsc[v][c] += live ? fq * act : 0.f;
+        h[c] = dp * wp[c];                                  // the gradient of q
+        s1[0] = fmaf(h[c], qc, s1[0]);
       }
-      if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dh) + row * p.dim + d, nd, dh[v]);
-      if (scale) VecIO<T, 8>::up(sc[v], k);
-      if (gate) {
-        float dz[8];
-        VecIO<T, 8>::up(zr[v], zz);
+      if constexpr (BIG) {
+        far_sum(2 * v, dpre[v]);
+        far_sum(2 * v + 1, dpost[v]);
+      }
+      if (live && nd > 0) {
+        vec_store<T, 8>(values_at<T>(static_cast<T*>(p.dh) + row * p.dim, d), nd, dh[v]);
+        if (gate) vec_store<T, 8>(values_at<T>(static_cast<T*>(p.dgate) + row * p.dim, d), nd, dz);
+      }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float e = sigmoid_f(zz[c]), cc = scale ? dh[v][c] * k[c] : dh[v][c];
-          dz[c] = cc * q[c] * wp[c] * (e * fmaf(zz[c], 1.f - e, 1.f));
-          zz[c] *= e;
-        }
-        if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dgate) + row * p.dim + d, nd, dz);
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float act = gate ? dh[v][c] * zz[c] : dh[v][c];   // dh silu(gate)
-        if (scale) dsc[v][c] += live ? act * q[c] * wp[c] : 0.f;
-        const float dp = scale ? act * k[c] : act;
-        dpost[v][c] += live ? dp * q[c] : 0.f;
-        dh[v][c] = dp * wp[c];                                  // the gradient of q
-        s1[0] = fmaf(dh[v][c], q[c], s1[0]);
-      }
+      for (int c = 0; c < 8; ++c) dh[v][c] = h[c];
     }
     row_sums<TPR, 1>(s1, red1[buf]);
     const float mx = s1[0] * p.inv_dim;
+    if constexpr (TPR > 256)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (BIG) xr[v] = vec_raw<T, 8>(values_at<const T>(x, (v * lanes + t) * 8), max(0, p.dim - (v * lanes + t) * 8));
+        else as_loaded(xr[v]);
+      }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+      const int d = (v * lanes + t) * 8, nd = min(8, p.dim - d);
       float q[8];
       VecIO<T, 8>::up(xr[v], q);
 #pragma unroll
       for (int c = 0; c < 8; ++c) q[c] = rx * (dh[v][c] - q[c] * rx * mx);
-      if (live && nd > 0) vec_store<T, 8>(static_cast<T*>(p.dx) + row * p.dim + d, nd, q);
+      if (live && nd > 0) vec_store<T, 8>(values_at<T>(static_cast<T*>(p.dx) + row * p.dim, d), nd, q);
     }
   }
   auto leave = [&](const float (&sum)[NV][8], float* part) __attribute__((always_inline)) {
@@ -235,7 +301,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) fold[sub][(v * TPR + t) * 8 + c] = sum[v][c];
+        for (int c = 0; c < 8; ++c) fold[sub][(v * lanes + t) * 8 + c] = sum[v][c];
       __syncthreads();
       for (int d = threadIdx.x; d < p.dim; d += NT) {
         float s = 0.f;
@@ -246,11 +312,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
+        const int d = (v * lanes + t) * 8, nd = min(8, p.dim - d);
         if (nd > 0) vec_store<float, 8>(part + d, nd, sum[v]);
       }
     }
   };
+  if constexpr (BIG) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        dpre[v][c] = far[2 * v][c / 4][t][c % 4];
+        dpost[v][c] = far[2 * v + 1][c / 4][t][c % 4];
+      }
+  }
   float* part = p.part + (long)blockIdx.x * (scale ? 3 : 2) * p.dim;
   leave(dpost, part);
   leave(dpre, part + p.dim);
@@ -258,7 +333,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
 }
 
 // Sums of partial rows, [rows][outputs][dim], in 64 strands of every 64th that
-// are then added in order; 32 columns a workgroup.
+// are then added in order; 32 columns a workgroup.  512 rows of 3 x 4096: 9 us (25
+// MB, from the last-level cache); bound by the few workgroups that so few columns
+// make, and by the launch.
 template <typename T>
 __global__ __launch_bounds__(512) void k_rows_sum(RowsSum p) {
   __shared__ f32x4 acc[64][8];
@@ -294,14 +371,21 @@ hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t 
   return e;
 }
 
-// Lanes per row and vectors per lane by the row's length.
+// Lanes per row and vectors per lane by the row's length; from 2049 values on as
+// many waves as its vectors need.  The gradient holds its registers for two
+// (two vectors) or three (one) waves a SIMD; measured in bf16, 2^26 values, us:
+// rows of 2304 347 in two, 458 in one, 4096 175 and 214, 5120 268 and 234, 6144
+// 239 and 204 (a few waves of two vectors leave SIMDs idle), 8192 208 in two.
+static bool block_norm_single(int dim) { return dim <= 2048 || (dim > 4096 && dim <= 6144); }
+static int block_norm_threads(int dim) { return dim <= 2048 ? 256 : block_norm_single(dim) ? (dim + 511) / 512 * 64 : (dim + 1023) / 1024 * 64; }
 #define BLOCK_NORM_DISPATCH(CALL)              \
   if (p.dim <= 128) { CALL(16, 1); }           \
   else if (p.dim <= 256) { CALL(32, 1); }      \
   else if (p.dim <= 512) { CALL(64, 1); }      \
   else if (p.dim <= 1024) { CALL(128, 1); }    \
   else if (p.dim <= 2048) { CALL(256, 1); }    \
-  else if (p.dim <= 4096) { CALL(256, 2); }    \
+  else if (p.dim <= 4096) { CALL(512, 2); }    \
+  else if (p.dim <= 6144) { CALL(768, 1); }    \
   else if (p.dim <= 8192) { CALL(512, 2); }    \
   else { CALL(1024, 2); }
 
@@ -311,7 +395,7 @@ static hipError_t block_norm_fwd(const BlockNormParams& p, hipStream_t st) {
 #define CALL(TPR, NV)                                                                                          \
   constexpr int NT = TPR < 256 ? 256 : TPR;                                                                    \
   hipLaunchKernelGGL((k_block_norm_fwd<T, TPR, NV>), dim3((unsigned)((p.rows + NT / TPR - 1) / (NT / TPR))),   \
-                     dim3(NT), 0, st, p)
+                     dim3(block_norm_threads(p.dim)), 0, st, p)
   BLOCK_NORM_DISPATCH(CALL);
 #undef CALL
   const hipError_t e = hipGetLastError();
@@ -324,7 +408,8 @@ hipError_t launch_block_norm_fwd(DType dt, const BlockNormParams& p, hipStream_t
 
 static int block_norm_rows_per_block(int dim) { return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 512 ? 4 : dim <= 1024 ? 2 : 1; }
 int block_norm_bwd_blocks(long rows, int dim) {
-  const long want = dim <= 4096 ? 2 * kComputeUnits : kComputeUnits;
+  const int resident = (dim > 2048 && block_norm_single(dim) ? 768 : 512) / block_norm_threads(dim);   // workgroups resident on a compute unit
+  const long want = (resident < 1 ? 1 : resident) * kComputeUnits;
   const long most = (rows + block_norm_rows_per_block(dim) - 1) / block_norm_rows_per_block(dim);
   return (int)(most < want ? most : want);
 }
@@ -333,7 +418,7 @@ static hipError_t block_norm_bwd(const BlockNormParams& p, hipStream_t st) {
   if (p.blocks > 0) {
     timing_before("block_norm_bwd", st);
 #define CALL(TPR, NV) \
-  hipLaunchKernelGGL((k_block_norm_bwd<T, TPR, NV>), dim3((unsigned)p.blocks), dim3(TPR < 256 ? 256 : TPR), 0, st, p)
+  hipLaunchKernelGGL((k_block_norm_bwd<T, TPR, NV>), dim3((unsigned)p.blocks), dim3(block_norm_threads(p.dim)), 0, st, p)
     BLOCK_NORM_DISPATCH(CALL);
 #undef CALL
     const hipError_t e = hipGetLastError();

@@ -67,10 +67,10 @@ __device__ __forceinline__ GDR_GLOBAL char* lin_uniform(const void* p) {
   return (GDR_GLOBAL char*)(uintptr_t)((uint64_t)hi << 32 | lo);
 }
 
-// Channels of a lane: four from lin_base on.  A column's last lanes are moved
-// back onto the last four channels, which they share with the lane before:
+// Channels of a lane: two from lin_base on.  A column's last lanes are moved
+// back onto the last two channels, which they share with the lane before:
 // they compute and store the same values, and no access needs a mask.  Fewer
-// than four channels (NARROW) are all held by every lane.
+// than two channels (NARROW) are held by every lane.
 __device__ __forceinline__ int lin_base(int first, int D) { return max(0, min(first, D - kLinVec)); }
 template <bool NARROW, typename T>
 __device__ __forceinline__ typename VecIO<T, kLinVec>::raw lin_read(const void* row, int d, int D) {
@@ -604,7 +604,9 @@ __global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
   }
 }
 
-// One new token per row; a wave takes 128 channels of one row.
+// One new token per row; a wave takes 128 channels of one row.  Bound by the
+// launch: 256 x 4096 in bf16 6.3 us (16 MB, 3.2 at a copy's rate), one row 3 (7.8
+// a call).
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_step(LinParams p) {
   const long unit = (long)blockIdx.x * (blockDim.x >> 6) + wave_id();

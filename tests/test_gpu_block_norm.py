@@ -31,6 +31,13 @@ NORMS = [
     (5, 8191, F32, True, True, True),
     (3, 16384, F32, True, True, True),
     (300, 16381, BF, True, True, True),
+    (1300, 2049, BF, False, True, True),
+    (530, 4097, BF, True, False, True),
+    (600, 5120, BF, True, True, True),
+    (4, 6145, F32, False, False, False),
+    (270, 8193, BF, False, False, True),
+    (9, 12000, F32, True, False, False),
+    (520, 9000, BF, False, True, False),
 ]
 
 
