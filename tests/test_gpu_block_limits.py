@@ -100,6 +100,30 @@ def test_product_of_the_most_columns():
         check(y[:, at], *ref.matmul_i8(q, s, w[at], ws[at]))
 
 
+@pytest.mark.parametrize("T,cu", [(20, [0, 10, 5, 20]), (150, [0, 70, 30, 150]), (640, [640, 0, 640, 3, 500]),
+                                  (640, [-7, 900, 100, 2 ** 31 - 1, -2 ** 31, 640])])
+def test_recurrence_on_tables_that_decrease(T, cu):
+    g, D, N = gen(T), 200, len(cu) - 1
+    x, r, i, dy = (cuda(randn(g, 1, T, D, dtype=BF)) for _ in range(4))
+    A, h0, dht = cuda(-torch.rand(D, generator=g)), cuda(randn(g, N, D)), cuda(randn(g, N, D))
+    table, guard = torch.tensor(cu, dtype=torch.int32, device="cuda"), 1 << 20
+    spaces = []
+    for name in ("gdr_linear_scan_fwd_workspace_size", "gdr_linear_scan_bwd_workspace_size"):
+        n = layer._bytes(name, layer._LinearScanShape(1, T, D, N, 0, 0, 0, 0))
+        spaces.append(torch.full((n + 2 * guard,), 0x5a, dtype=torch.uint8, device="cuda"))
+    y, _ = gdr.gdr_linear_scan_fwd(x, r, i, A, h0, table, output_final_state=True, workspace=spaces[0][guard:-guard])
+    grads = gdr.gdr_linear_scan_bwd(x, r, i, A, dy, h0, dht, table, workspace=spaces[1][guard:-guard])
+    for w in spaces:
+        assert bool((w[:guard] == 0x5a).all() and (w[-guard:] == 0x5a).all())
+    assert all(bool(torch.isfinite(t).all()) for t in (y, *grads[:4]))
+    again, _ = gdr.gdr_linear_scan_fwd(x, r, i, A, h0, table)
+    assert torch.equal(again, y)
+    if T <= 150:   # the tokens from the first decrease on are a run of the last sequence that holds them
+        at = cu[1]
+        v = [t[:, at:].cpu() for t in (x, r, i)]
+        check(y[:, at:], *ref.linear_scan(*v, A.cpu(), h0[2:3].cpu())[:2], "the run behind the decrease")
+
+
 def test_h_takes_the_residuals_place():
     g = gen(6)
     for rows, dim in ((37, 100), (9, 4096), (300, 128)):
