@@ -142,7 +142,8 @@ __device__ __forceinline__ void i8_landed() {
 // at c ^ stage_swz<16>(r % 16).  Bound by the copies, of the weight from memory
 // and, from 100 rows on, of x from the cache: 4096 -> 8192, 1 row 8.9 us (floor
 // 6.5), 100 rows 12.3, 256 rows 17.4.  Operands read straight into registers
-// took 8.8, 19.4 and 41 (a lane's 16 bytes of 16 rows are 64 requests).
+// took 8.8, 19.4 and 41 (a lane's 16 bytes of 16 rows are 64 requests); more
+// steps ahead (9, 6 and 4 buffers for 6, 4 and 3) 9.2, 12.8 and 18.5.
 template <typename T, int MT, int NT, int ST>
 __global__ __launch_bounds__(256) void k_i8_some(I8Params p) {
   constexpr int NW = 4, KS = 64 * NW, R = 16 * (MT + NT), C = R / 4 / NW, TILES = MT * NT;   // C: 1 KB copies a wave and step
