@@ -375,7 +375,8 @@ hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t 
 // many waves as its vectors need.  The gradient holds its registers for two
 // (two vectors) or three (one) waves a SIMD; measured in bf16, 2^26 values, us:
 // rows of 2304 347 in two, 458 in one, 4096 175 and 214, 5120 268 and 234, 6144
-// 239 and 204 (a few waves of two vectors leave SIMDs idle), 8192 208 in two.
+// 239 and 204 (a few waves of two vectors leave SIMDs idle), 8192 208 in two; two
+// vectors within the registers of three waves a SIMD spill: 4096 336.
 static bool block_norm_single(int dim) { return dim <= 2048 || (dim > 4096 && dim <= 6144); }
 static int block_norm_threads(int dim) { return dim <= 2048 ? 256 : block_norm_single(dim) ? (dim + 511) / 512 * 64 : (dim + 1023) / 1024 * 64; }
 #define BLOCK_NORM_DISPATCH(CALL)              \
