@@ -11,7 +11,7 @@
 // unrounded h.
 //
 // 16384 x 4096 in bf16 with gate and scale: 121 us (5.5 TB/s; a copy moves 5.2),
-// the gradient 208 (5.2) with its sums of partial rows 9; 64 rows 8.5 a call.
+// the gradient 211 (5.1) with its sums of partial rows 7; 64 rows 8.5 a call.
 #include "gdr_layer.h"
 
 namespace gdr {
@@ -138,11 +138,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockN
 //   dw_pre = sum dy n,  dw_post = sum dp q,  dscale = sum dh q w_post c
 // Persistent workgroups keep the three vectors' sums in registers and leave one
 // partial row of each.
-// Values as they were loaded: what was made of them before is made again and not
-// held in registers.
-__device__ __forceinline__ void as_loaded(VecIO<bf16, 8>::raw& r) { asm volatile("" : "+v"(r)); }
-__device__ __forceinline__ void as_loaded(VecIO<float, 8>::raw& r) { asm volatile("" : "+v"(r.a), "+v"(r.b)); }
-
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockNormParams p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
@@ -237,10 +232,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
         asm volatile("" ::: "memory");   // a second read, and not registers that hold the first
         sums_of(v);
         others(v);
-      } else if constexpr (TPR > 256) {
-        as_loaded(xr[v]);
-        as_loaded(hr[v]);
-        as_loaded(yr[v]);
       }
       float h[8], g[8], w[8], q[8], wp[8], s[8], k[8], z[8];
       VecIO<T, 8>::up(hr[v], h);
@@ -279,12 +270,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
     }
     row_sums<TPR, 1>(s1, red1[buf]);
     const float mx = s1[0] * p.inv_dim;
-    if constexpr (TPR > 256)
+    if constexpr (BIG)
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if constexpr (BIG) xr[v] = vec_raw<T, 8>(values_at<const T>(x, (v * lanes + t) * 8), max(0, p.dim - (v * lanes + t) * 8));
-        else as_loaded(xr[v]);
-      }
+      for (int v = 0; v < NV; ++v) xr[v] = vec_raw<T, 8>(values_at<const T>(x, (v * lanes + t) * 8), max(0, p.dim - (v * lanes + t) * 8));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int d = (v * lanes + t) * 8, nd = min(8, p.dim - d);
@@ -333,7 +321,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
 }
 
 // Sums of partial rows, [rows][outputs][dim], in 64 strands of every 64th that
-// are then added in order; 32 columns a workgroup.  512 rows of 3 x 4096: 9 us (25
+// are then added in order; 32 columns a workgroup.  512 rows of 3 x 4096: 7 us (25
 // MB, from the last-level cache); bound by the few workgroups that so few columns
 // make, and by the launch.
 template <typename T>
@@ -374,8 +362,8 @@ hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t 
 // Lanes per row and vectors per lane by the row's length; from 2049 values on as
 // many waves as its vectors need.  The gradient holds its registers for two
 // (two vectors) or three (one) waves a SIMD; measured in bf16, 2^26 values, us:
-// rows of 2304 347 in two, 458 in one, 4096 175 and 214, 5120 268 and 234, 6144
-// 239 and 204 (a few waves of two vectors leave SIMDs idle), 8192 208 in two; two
+// rows of 2304 326 in two, 458 in one, 4096 173 and 214, 5120 268 and 225, 6144
+// 239 and 199 (a few waves of two vectors leave SIMDs idle), 8192 202 in two; two
 // vectors within the registers of three waves a SIMD spill: 4096 336.
 static bool block_norm_single(int dim) { return dim <= 2048 || (dim > 4096 && dim <= 6144); }
 static int block_norm_threads(int dim) { return dim <= 2048 ? 256 : block_norm_single(dim) ? (dim + 511) / 512 * 64 : (dim + 1023) / 1024 * 64; }

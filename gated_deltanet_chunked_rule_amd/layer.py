@@ -480,7 +480,8 @@ def _norm_shape(x):
         raise GdrError("x must be [..., dim] with at least two dimensions")
     shape = x.shape
     dim = shape[-1]
-    _fits(dim=dim)
+    if dim > _MOST:
+        _too_long(dim=dim)
     rows = x.numel() // dim if dim else 0
     return shape, rows, (shape[-2] if len(shape) > 2 and rows else 1), dim
 
@@ -551,11 +552,11 @@ def rms_norm(x, weight, residual: Optional[torch.Tensor] = None, gate: Optional[
     return _NormFunction.apply(x, weight, residual, gate, eps)
 
 
-def _fits(**sizes):
-    """The library's sizes are 32-bit integers, and ctypes cuts what is longer off without a word."""
-    for name, n in sizes.items():
-        if n > 0x7fffffff:
-            raise GdrError(f"{name} must be below 2^31")
+_MOST = 0x7fffffff   # the library's sizes are 32-bit integers, and ctypes cuts what is longer off without a word
+
+
+def _too_long(**sizes):
+    raise GdrError(f"{next(name for name, n in sizes.items() if n > _MOST)} must be below 2^31")
 
 
 # ------------------------------------------------------- linear recurrence --
@@ -564,7 +565,8 @@ def _linear_scan_args(x, r, i, A, cu_seqlens):
         raise GdrError("x must be [B, T, D]")
     shape = tuple(x.shape)
     B, T, D = shape
-    _fits(B=B, T=T, D=D)
+    if B > _MOST or T > _MOST or D > _MOST:
+        _too_long(B=B, T=T, D=D)
     code, dev, ty = _code(x), x.get_device(), x.dtype
     xp, xs = _rows_of(x, "x", shape, ty, dev, 2)
     rp, rs = _rows_of(r, "r", shape, ty, dev, 2)
@@ -613,7 +615,8 @@ def gdr_linear_scan_step(x, r, i, A, state, *, slots=None):
         _no_gradient("gdr_linear_scan_step")
     shape = x.shape
     rows, D = shape
-    _fits(rows=rows, D=D)
+    if rows > _MOST or D > _MOST:
+        _too_long(rows=rows, D=D)
     code, dev, ty = _code(x), x.get_device(), x.dtype
     xp, xs = _rows_of(x, "x", shape, ty, dev, 1)
     rp, rs = _rows_of(r, "r", shape, ty, dev, 1)
@@ -686,7 +689,8 @@ def _block_norm_args(x, post_weight, h, pre_weight, gate, scale, eps, h_name):
         raise GdrError("x must be [..., dim] with at least two dimensions")
     shape = x.shape
     dim = shape[-1]
-    _fits(dim=dim)
+    if dim > _MOST:
+        _too_long(dim=dim)
     rows = x.numel() // dim if dim else 0
     code, dev, ty = _code(x), x.get_device(), x.dtype
     xp, xs = _flat_rows(x, "x", shape, ty, dev)
@@ -765,7 +769,8 @@ def gdr_quantize_rows(x):
         _no_gradient("gdr_quantize_rows")
     shape = x.shape
     K = shape[-1]
-    _fits(K=K)
+    if K > _MOST:
+        _too_long(K=K)
     code, dev = _code(x), x.get_device()
     xp, xs = _flat_rows(x, "x", shape, x.dtype, dev)
     pad = -(-K // 16) * 16
@@ -806,7 +811,8 @@ def gdr_matmul_i8(q, scales, weight, weight_scales, bias=None, *, dtype=torch.bf
     if K < 1 or shape[-1] != K:
         raise GdrError(f"shape mismatch: q is {tuple(shape)}, weight {tuple(weight.shape)}")
     M = q.numel() // K
-    _fits(M=M, N=N, K=K)
+    if M > _MOST or N > _MOST or K > _MOST:
+        _too_long(M=M, N=N, K=K)
     code = GDR_BF16 if dtype is torch.bfloat16 else GDR_F32 if dtype is torch.float32 else None
     if code is None:
         raise GdrError(f"unsupported dtype {dtype} (bfloat16 or float32)")
