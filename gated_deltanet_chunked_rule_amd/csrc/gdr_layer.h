@@ -381,6 +381,25 @@ __host__ __device__ __forceinline__ TokenRuns token_runs(const SeqFinder& sf, in
   if (live < count) m.gap |= ~0u << live;
   return m;
 }
+// Linear recurrence: a column of kLinCh channels is a wave's, kLinVec a lane, from
+// lin_base on.  The last column's last lanes are moved back onto the last
+// channels, which they share with the lane before: they compute and store the
+// same values, and no access needs a mask.  Fewer than kLinVec channels are
+// held by every lane, in its first places.
+constexpr int kLinVec = 2, kLinCh = 64 * kLinVec;
+__host__ __device__ __forceinline__ int lin_base(int first, int D) {
+  const int last = D < kLinVec ? 0 : D - kLinVec;
+  return first < last ? first : last;
+}
+// Value c < kLinCh of a column is that of lane c / kLinVec in its place
+// lin_place, and of the channel lin_channel, which is there for every c.
+__host__ __device__ __forceinline__ int lin_place(int c, int D) {
+  const int k = c % kLinVec;
+  return k < D ? k : D - 1;
+}
+__host__ __device__ __forceinline__ int lin_channel(int col, int c, int D) {
+  return lin_base(col * kLinCh + c / kLinVec * kLinVec, D) + lin_place(c, D);
+}
 // Every thread of the workgroup calls this (barrier inside).
 template <int STAGE = kCuLds>
 __device__ __forceinline__ SeqFinder seq_finder(const SeqRanges& s, int32_t* lds) {

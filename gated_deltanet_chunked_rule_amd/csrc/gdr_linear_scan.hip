@@ -16,8 +16,6 @@
 namespace gdr {
 
 constexpr float kFresh = -1.f;   // in the place of a product of decays: the end does not depend on the start
-constexpr int kLinVec = 2;       // channels a lane
-constexpr int kLinCh = 64 * kLinVec;
 typedef float lin_v __attribute__((ext_vector_type(kLinVec)));
 constexpr int kLinJoinCh = 16;
 
@@ -67,11 +65,7 @@ __device__ __forceinline__ GDR_GLOBAL char* lin_uniform(const void* p) {
   return (GDR_GLOBAL char*)(uintptr_t)((uint64_t)hi << 32 | lo);
 }
 
-// Channels of a lane: two from lin_base on.  A column's last lanes are moved
-// back onto the last two channels, which they share with the lane before:
-// they compute and store the same values, and no access needs a mask.  Fewer
-// than two channels (NARROW) are held by every lane.
-__device__ __forceinline__ int lin_base(int first, int D) { return max(0, min(first, D - kLinVec)); }
+// A row's values of a lane's channels; NARROW: fewer than kLinVec are there.
 template <bool NARROW, typename T>
 __device__ __forceinline__ typename VecIO<T, kLinVec>::raw lin_read(const void* row, int d, int D) {
   GDR_GLOBAL char* at = lin_uniform(row) + (uint32_t)d * (uint32_t)sizeof(T);   // a scalar row address and one offset in a register
@@ -106,8 +100,6 @@ __device__ __forceinline__ void lin_empty(const SeqFinder& sf, const float* from
   for (int n = tile; n < sf.N; n += tiles)
     if (sf.at(n + 1) <= sf.at(n)) to[(long)n * D + d] = from ? from[(long)n * D + d] : 0.f;
 }
-// The channel that value c of a column's lanes stands for.
-__device__ __forceinline__ int lin_channel(int col, int c, int D) { return lin_base(col * kLinCh + (c & ~(kLinVec - 1)), D) + (c & (kLinVec - 1)); }
 
 // What the waves of a tile do to the state.
 struct LinAgg {
@@ -252,6 +244,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_one(LinParams p) {
   const int w = wave_id(), l = lane_id(), col = blockIdx.x % p.cols, d = lin_base(col * kLinCh + l * kLinVec, p.D);
   const int hf = w / (kLinCh / 64), c = 64 * (w - kLinCh / 64 * hf) + l;
   const uint32_t dc = lin_channel(col, c, p.D);
+  const int cl = c / kLinVec, cv = lin_place(c, p.D);
   int* tickets = p.ticket + col * kLinLine;
   if (threadIdx.x == 0) ticket = atomicAdd(tickets, 1);
   float A2[kLinVec];
@@ -281,7 +274,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_one(LinParams p) {
     float tp = 1.f, ts = 0.f;
     if (hf == 0) {
 #pragma unroll
-      for (int u = 0; u < NW; ++u) lin_join(tp, ts, agg.p[u][c / kLinVec][c % kLinVec], agg.s[u][c / kLinVec][c % kLinVec]);
+      for (int u = 0; u < NW; ++u) lin_join(tp, ts, agg.p[u][cl][cv], agg.s[u][cl][cv]);
       lin_put(p.words + (long)tile * p.D + dc, tp, ts);
     }
     const int grp = tile / kLinGroup, in = tile - grp * kLinGroup, n = max(0, min(EACH, in - EACH * hf));
@@ -523,13 +516,12 @@ __global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
   lds_barrier();
   if constexpr (!OUT) {
     for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) {
-      const int dc = lin_channel(col, c, p.D);
-      if (dc >= p.D) break;
+      const int dc = lin_channel(col, c, p.D), cl = c / kLinVec, cv = lin_place(c, p.D);
       float tp = 1.f, ts = 0.f, tq = 0.f;
 #pragma unroll
-      for (int v = 0; v < NW; ++v) lin_join(tp, ts, agg.p[v][c / kLinVec][c % kLinVec], agg.s[v][c / kLinVec][c % kLinVec]);
+      for (int v = 0; v < NW; ++v) lin_join(tp, ts, agg.p[v][cl][cv], agg.s[v][cl][cv]);
 #pragma unroll
-      for (int v = NW - 1; v >= 0; --v) tq = lin_after(tq, agg.p[v][c / kLinVec][c % kLinVec], back[v][c / kLinVec][c % kLinVec]);
+      for (int v = NW - 1; v >= 0; --v) tq = lin_after(tq, agg.p[v][cl][cv], back[v][cl][cv]);
       p.P[(long)tile * p.D + dc] = tp;
       p.S[(long)tile * p.D + dc] = ts;
       p.Q[(long)tile * p.D + dc] = tq;
@@ -595,12 +587,10 @@ __global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
   lds_barrier();
   for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) {
     lin_empty(sf, p.dht, p.dh0, tile, p.tiles, col * kLinCh + c, p.D);
-    const int dc = lin_channel(col, c, p.D);
-    if (dc >= p.D) break;
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < NW; ++v) s += back[v][c / kLinVec][c % kLinVec];
-    p.part[(long)tile * p.D + dc] = s;
+    for (int v = 0; v < NW; ++v) s += back[v][c / kLinVec][lin_place(c, p.D)];
+    p.part[(long)tile * p.D + lin_channel(col, c, p.D)] = s;
   }
 }
 
