@@ -366,7 +366,7 @@ hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t 
 // 239 and 199 (a few waves of two vectors leave SIMDs idle), 8192 202 in two; two
 // vectors within the registers of three waves a SIMD spill: 4096 336.
 static bool block_norm_single(int dim) { return dim <= 2048 || (dim > 4096 && dim <= 6144); }
-static int block_norm_threads(int dim) { return dim <= 2048 ? 256 : block_norm_single(dim) ? (dim + 511) / 512 * 64 : (dim + 1023) / 1024 * 64; }
+int block_norm_threads(int dim) { return dim <= 2048 ? 256 : block_norm_single(dim) ? (dim + 511) / 512 * 64 : (dim + 1023) / 1024 * 64; }
 #define BLOCK_NORM_DISPATCH(CALL)              \
   if (p.dim <= 128) { CALL(16, 1); }           \
   else if (p.dim <= 256) { CALL(32, 1); }      \
@@ -395,7 +395,7 @@ hipError_t launch_block_norm_fwd(DType dt, const BlockNormParams& p, hipStream_t
   return dt == DType::BF16 ? block_norm_fwd<bf16>(p, st) : block_norm_fwd<float>(p, st);
 }
 
-static int block_norm_rows_per_block(int dim) { return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 512 ? 4 : dim <= 1024 ? 2 : 1; }
+int block_norm_rows_per_block(int dim) { return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 512 ? 4 : dim <= 1024 ? 2 : 1; }
 int block_norm_bwd_blocks(long rows, int dim) {
   const int resident = (dim > 2048 && block_norm_single(dim) ? 768 : 512) / block_norm_threads(dim);   // workgroups resident on a compute unit
   const long want = (resident < 1 ? 1 : resident) * kComputeUnits;

@@ -147,6 +147,8 @@ hipError_t launch_lin_step(DType dt, const LinParams& p, hipStream_t st);
 hipError_t launch_block_norm_fwd(DType dt, const BlockNormParams& p, hipStream_t st);
 hipError_t launch_block_norm_bwd(DType dt, const BlockNormParams& p, hipStream_t st);
 int block_norm_bwd_blocks(long rows, int dim);
+int block_norm_threads(int dim);            // of a workgroup
+int block_norm_rows_per_block(int dim);
 hipError_t launch_quant_rows(DType dt, const QuantParams& p, hipStream_t st);
 hipError_t launch_i8_matmul(DType dt, const I8Params& p, hipStream_t st);
 hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t st);   // dt: of the outputs

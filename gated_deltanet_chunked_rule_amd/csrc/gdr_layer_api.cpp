@@ -45,7 +45,7 @@ gdr::SeqRanges ranges(int B, int T, int num_seqs, const int32_t* cu) {
   return s;
 }
 
-// Lanes that a row of dim values takes in the kernels that hold whole rows.
+// Lanes that a row of dim values takes in the norm's and the quantisation's kernels.
 long row_threads(int dim) {
   return dim <= 128 ? 16 : dim <= 256 ? 32 : dim <= 512 ? 64 : dim <= 1024 ? 128 : dim <= 4096 ? 256 : dim <= 8192 ? 512 : 1024;
 }
@@ -194,7 +194,7 @@ gdr_status block_norm_check(const gdr_block_norm_shape* sh) {
   const int64_t st[3] = {sh->x_stride, sh->residual_stride, sh->gate_stride};
   for (int64_t s : st)
     if (s != 0 && s < sh->dim) return invalid("a row stride is smaller than its row");
-  if (sh->rows > (kMaxThreads - 1024) / row_threads(sh->dim)) return unsupported("too many rows");
+  if (sh->rows > kMaxThreads / gdr::block_norm_threads(sh->dim) * gdr::block_norm_rows_per_block(sh->dim)) return unsupported("too many rows");
   return GDR_OK;
 }
 gdr::BlockNormParams block_norm_params(const gdr_block_norm_shape* sh, const void* x, const void* gate, const void* post,
