@@ -377,7 +377,8 @@ gdr_status gdr_rms_norm_bwd(const gdr_norm_shape* shape, const void* h, const vo
  *   e = sigmoid(r_t),  a = exp(A e),  b = sqrt(1 - a^2) sigmoid(i_t) x_t
  *   h_t = a h_{t-1} + b,  y_t = h_t
  * per channel; A <= 0 (a positive one gives NaN where a > 1).  States and sums
- * are fp32; y is h rounded once. */
+ * are fp32; y is h rounded once.  An infinite state stays infinite until its
+ * sequence ends (NaN behind a decay that is zero in fp32, e^-87 and less). */
 typedef struct {
   int32_t B, T;               /* as in gdr_shape */
   int32_t D;                  /* channels, at most 2^25 */
