@@ -275,13 +275,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
 #pragma unroll
     for (int j = 0; j < MT; ++j) fx[H][j] = *reinterpret_cast<const i32x4*>(&lds[buf][ax + j * 16 * KS + at]);
   };
-  // Products FROM .. TO of the NT x MT of a half step.
-  auto products = [&](auto half, auto from, auto to) __attribute__((always_inline)) {
+  auto products = [&](auto half) __attribute__((always_inline)) {
     constexpr int H = decltype(half)::value;
 #pragma unroll
-    for (int k = decltype(from)::value; k < decltype(to)::value; ++k) acc[k / MT][k % MT] = i8_mma(fw[H][k / MT], fx[H][k % MT], acc[k / MT][k % MT]);
+    for (int k = 0; k < NT * MT; ++k) acc[k / MT][k % MT] = i8_mma(fw[H][k / MT], fx[H][k % MT], acc[k / MT][k % MT]);
   };
-  constexpr int ALL = NT * MT, EARLY = ALL / 4;
   auto copy = [&](int s, int buf) __attribute__((always_inline)) {
     const uint32_t k0 = copy_at(s);
 #pragma unroll
@@ -295,13 +293,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
   int buf = 0;
   for (int s = 0; s + 1 < steps; ++s) {
     read(buf, ic<1>{});
-    products(ic<0>{}, ic<0>{}, ic<ALL>{});
+    products(ic<0>{});
     i8_landed<0>();    // of the next step, this wave's copies; and its reads of this one are done
     lds_barrier();     // and everybody's
     copy(s + 2, buf);
     buf ^= 1;
     read(buf, ic<0>{});
-    products(ic<1>{}, ic<0>{}, ic<ALL>{});
+    products(ic<1>{});
   }
   read(buf, ic<1>{});
   if (steps * KS > p.K) {
@@ -311,8 +309,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
       fw[1][i] = i8_head(fw[1][i], (steps - 1) * KS + 64 + 16 * g, p.K);
     }
   }
-  products(ic<0>{}, ic<0>{}, ic<ALL>{});
-  products(ic<1>{}, ic<0>{}, ic<ALL>{});
+  products(ic<0>{});
+  products(ic<1>{});
   i8_landed<0>();   // no copy outlives the wave
   // a lane's 4 NT values of a row one after another, so that cache lines fill at
   // once (in two turns of 16 bytes each was written twice: 267 MB for 134)
