@@ -162,6 +162,13 @@ def _code(t) -> int:
     raise GdrError(f"unsupported dtype {t.dtype} (bfloat16 or float32)")
 
 
+_MOST = 0x7fffffff   # the library's sizes are 32-bit integers, and ctypes cuts what is longer off without a word
+
+
+def _too_long(**sizes):
+    raise GdrError(f"{next(name for name, n in sizes.items() if n > _MOST)} must be below 2^31")
+
+
 # The checks below run on every call of a serving step: one test of what is
 # expected first, and what is wrong with the tensor only where that fails.
 def _refuse(t, name, shape, dtype, index, contiguous=True):
@@ -270,6 +277,8 @@ def _conv_args(x, weight, bias, cu_seqlens, activation):
         raise GdrError("x must be [B, T, D] and weight [D, W]")
     B, T, D = x.shape
     W = weight.shape[1]
+    if B > _MOST or T > _MOST or D > _MOST:
+        _too_long(B=B, T=T, D=D)
     act, code, dev, ty = _activation(activation), _code(x), x.get_device(), x.dtype
     xp, xs = _rows_of(x, "x", (B, T, D), ty, dev, 2)
     wp = _dense(weight, "weight", (D, W), ty, dev)
@@ -322,6 +331,8 @@ def gdr_causal_conv_step(x, state, weight, bias=None, *, slots=None, activation=
         _no_gradient("gdr_causal_conv_step")
     rows, D = x.shape
     W = weight.shape[1]
+    if rows > _MOST or D > _MOST:
+        _too_long(rows=rows, D=D)
     act, code, dev, ty = _activation(activation), _code(x), x.get_device(), x.dtype
     xp, xs = _rows_of(x, "x", (rows, D), ty, dev, 1)
     wp = _dense(weight, "weight", (D, W), ty, dev)
@@ -550,13 +561,6 @@ class _NormFunction(torch.autograd.Function):
 def rms_norm(x, weight, residual: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, eps=1e-6):
     """High-level call: returns (y, h or None) with h = x + residual; differentiable."""
     return _NormFunction.apply(x, weight, residual, gate, eps)
-
-
-_MOST = 0x7fffffff   # the library's sizes are 32-bit integers, and ctypes cuts what is longer off without a word
-
-
-def _too_long(**sizes):
-    raise GdrError(f"{next(name for name, n in sizes.items() if n > _MOST)} must be below 2^31")
 
 
 # ------------------------------------------------------- linear recurrence --
