@@ -162,13 +162,6 @@ def _code(t) -> int:
     raise GdrError(f"unsupported dtype {t.dtype} (bfloat16 or float32)")
 
 
-_MOST = 0x7fffffff   # the library's sizes are 32-bit integers, and ctypes cuts what is longer off without a word
-
-
-def _too_long(**sizes):
-    raise GdrError(f"{next(name for name, n in sizes.items() if n > _MOST)} must be below 2^31")
-
-
 # The checks below run on every call of a serving step: one test of what is
 # expected first, and what is wrong with the tensor only where that fails.
 def _refuse(t, name, shape, dtype, index, contiguous=True):
@@ -218,6 +211,13 @@ def _rows_of(t, name, shape, dtype, index, lead):
     return t.data_ptr(), token
 
 
+_MOST = 0x7fffffff   # the library's sizes are 32-bit integers, and ctypes cuts what is longer off without a word
+
+
+def _too_long(**sizes):
+    raise GdrError(f"{next(name for name, n in sizes.items() if n > _MOST)} must be below 2^31")
+
+
 def _offsets(cu_seqlens, B, T, dev):
     """(device int32 tensor or None, number of sequences)."""
     if cu_seqlens is None:
@@ -227,6 +227,8 @@ def _offsets(cu_seqlens, B, T, dev):
     cu = cu_seqlens if isinstance(cu_seqlens, torch.Tensor) else torch.as_tensor(cu_seqlens)
     if cu.dim() != 1 or cu.numel() < 2 or cu.dtype not in (torch.int32, torch.int64):
         raise GdrError("cu_seqlens must be a 1-D int32 or int64 tensor of at least two offsets")
+    if cu.numel() > _MOST:
+        _too_long(offsets=cu.numel())
     if cu.is_cuda:
         if cu.device != dev:
             raise GdrError(f"cu_seqlens is on {cu.device}, expected {dev}")
@@ -259,7 +261,8 @@ def _pool(state, name, tail, dtype, index, rows, slots):
     ptr = state.data_ptr()
     if n < 1 or (slots is None and n < rows):
         raise GdrError(f"{name} holds {n} slots for {rows} rows")
-    return ptr, n, _dense(slots, "slots", (rows,), torch.int32, index)
+    # int32 slots name none behind the 2^31 - 1st, and ctypes would cut a longer pool's size off
+    return ptr, n if n < _MOST else _MOST, _dense(slots, "slots", (rows,), torch.int32, index)
 
 
 _ACT = {None: 0, "none": 0, "silu": 1}
