@@ -333,7 +333,7 @@ struct SeqFinder {
     }
     int lo = 0, hi = N - 1;
     while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
+      const int mid = lo + ((hi - lo + 1) >> 1);   // their sum may leave an int
       if (at(mid) <= t) lo = mid; else hi = mid - 1;
     }
     const int e = at(lo + 1);
@@ -350,6 +350,14 @@ struct SeqFinder {
   // at the piece's own first token, and never at token 0, whatever the table.
   static __host__ __device__ __forceinline__ bool goes_on(int t, int piece, int start) { return t == piece && start < t; }
 };
+// f(n) of the sequences without a token among first, first + step, ...  (Their
+// numbers plus a step may leave an int.)
+template <typename F>
+__host__ __device__ __forceinline__ void empty_sequences(const SeqFinder& sf, long first, long step, F f) {
+  if (!sf.packed && sf.T > 0) return;
+  for (long n = first; n < sf.N; n += step)
+    if (sf.at((int)n + 1) <= sf.at((int)n)) f(n);
+}
 // What happens at the `count` (below 32) tokens from t0 on, as bits: first: the
 // token starts a run that does not go on from the tokens before t0; last: it
 // ends its sequence; gap: it belongs to none, or lies behind the last token.

@@ -97,12 +97,14 @@ __device__ __forceinline__ void lin_load(const void* base, long stride, int t0, 
 }
 
 // Sequences without a token: their final state is their initial state (the
-// gradient of that one the gradient of the final state).  Each tile of tokens
-// takes its share of the sequences.
-__device__ __forceinline__ void lin_empty(const SeqFinder& sf, const float* from, float* to, int tile, int tiles, int d, int D) {
-  if (!to || d >= D) return;
-  for (int n = tile; n < sf.N; n += tiles)
-    if (sf.at(n + 1) <= sf.at(n)) to[(long)n * D + d] = from ? from[(long)n * D + d] : 0.f;
+// gradient of that one the gradient of the final state).  Each wave of each tile
+// of tokens takes its share of the sequences.
+template <int NW>
+__device__ __forceinline__ void lin_empty(const SeqFinder& sf, const float* from, float* to, int tile, int tiles, int col, int D) {
+  if (!to) return;
+  empty_sequences(sf, tile + (long)tiles * wave_id(), (long)tiles * NW, [&](long n) {
+    for (int d = col * kLinCh + lane_id(); d < min(D, (col + 1) * kLinCh); d += 64) to[n * D + d] = from ? from[n * D + d] : 0.f;
+  });
 }
 
 // What the waves of a tile do to the state.
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_one(LinParams p) {
       for (int e = 0; e < kLinVec; ++e) h[e] = lin_after(h[e], pu[e], su[e]);
     }
     lin_leave<NARROW, T, TT>(p, agg.seq[w], run, t0, d, a, b, h);
-    if (hf == 0) lin_empty(sf, p.h0, p.ht, done, p.tiles, col * kLinCh + c, p.D);
+    lin_empty<NW>(sf, p.h0, p.ht, done, p.tiles, col, p.D);
   }
 }
 
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_lin_tile(LinParams p) {
     for (int c = 0; c < kLinVec; ++c) h[c] = lin_after(h[c], pu[c], su[c]);
   }
   lin_leave<NARROW, T, TT>(p, agg.seq[w], run, t0, d, a, b, h);
-  for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) lin_empty(sf, p.h0, p.ht, 0, 1, col * kLinCh + c, p.D);
+  lin_empty<NW>(sf, p.h0, p.ht, 0, 1, col, p.D);
 }
 
 // The tiles' (P, S) turned into the states at their ends, and Q into what the
@@ -610,8 +612,8 @@ __global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
   lds_barrier();   // every wave has read the others' runs
   back[w][l] = dA;
   lds_barrier();
+  lin_empty<NW>(sf, p.dht, p.dh0, tile, p.tiles, col, p.D);
   for (int c = threadIdx.x; c < kLinCh; c += 64 * NW) {
-    lin_empty(sf, p.dht, p.dh0, tile, p.tiles, col * kLinCh + c, p.D);
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < NW; ++v) s += back[v][c / kLinVec][lin_place(c, p.D)];
