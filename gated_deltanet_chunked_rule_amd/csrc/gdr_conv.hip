@@ -136,7 +136,7 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
   const T* dy = static_cast<const T*>(p.dy) + d;
   T* dx = static_cast<T*>(p.dx) + d;
   const T* dht = static_cast<const T*>(p.dht);
-  if (tile >= p.tiles + (p.dh0 ? p.s.N : 0)) return;
+  if (tile >= (long)p.tiles + (p.dh0 ? p.s.N : 0)) return;
   float w[W][VEC], b[VEC];
   load_taps<T, VEC, W>(p, d, nd, w, b);
   auto dact = [&](const float (&win)[W][VEC], const float (&g)[VEC], float (&dz)[VEC]) {
@@ -368,7 +368,7 @@ static hipError_t conv_fwd(ConvParams p, hipStream_t st) {
   const long ncg = (p.D + 7) / 8;
   p.tile = tile_for(ncg, p.s.Ttot, 1L << 18, 4, 32);
   p.tiles = (p.s.Ttot + p.tile - 1) / p.tile;
-  const long items = ncg * (p.tiles + (p.ht ? p.s.N : 0));
+  const long items = ncg * ((long)p.tiles + (p.ht ? p.s.N : 0));
   if (items == 0) return hipSuccess;
   timing_before("conv_fwd", st);
   hipLaunchKernelGGL((k_conv_fwd<T, W>), dim3((unsigned)((items + 255) / 256)), dim3(256), 0, st, p);
@@ -379,7 +379,7 @@ static hipError_t conv_fwd(ConvParams p, hipStream_t st) {
 template <typename T, int W>
 static hipError_t conv_bwd(const ConvParams& p, hipStream_t st) {
   const long ncg = (p.D + 3) / 4;
-  const long items = ncg * (p.tiles + (p.dh0 ? p.s.N : 0));
+  const long items = ncg * ((long)p.tiles + (p.dh0 ? p.s.N : 0));
   hipError_t e = hipSuccess;
   if (items > 0) {
     timing_before("conv_bwd", st);
