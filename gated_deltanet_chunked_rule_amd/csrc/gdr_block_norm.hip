@@ -10,8 +10,9 @@
 // nothing from memory.  Sums are fp32 over unrounded values; y is made from the
 // unrounded h.
 //
-// 16384 x 4096 in bf16 with gate and scale: 121 us (5.5 TB/s; a copy moves 5.2),
-// the gradient 211 (5.1) with its sums of partial rows 7; 64 rows 8.5 a call.
+// 16384 x 4096 in bf16 with gate and scale: 121 us (5.5 TB/s; plain streams, four
+// read to two written, move 5.7), the gradient 211 (5.1; four to three 5.4) with
+// its sums of partial rows 7; 64 rows 8.8 a call.
 #include "gdr_layer.h"
 
 namespace gdr {
@@ -147,8 +148,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
   __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NV * 8 : 1];
   // From 8193 values on a lane has 128 registers.  LDS holds the sums of two of
   // the vectors, and row and vectors are read again (from L2) where they are used
-  // a second time: 4096 x 16384 in bf16 411 us, 1516 with all of it in registers
-  // (736 bytes a lane spilled), 2048 x 16384 in fp32 336 and 805.
+  // a second time: 4096 x 16384 in bf16 464 us, 2048 x 16384 in fp32 370.  With x
+  // for the gate and h for d_res 411 and 336, where all of it in registers (736
+  // bytes a lane spilled) took 1516 and 805.
   constexpr bool BIG = TPR == 1024;
   __shared__ f32x4 far[BIG ? 2 * NV : 1][2][BIG ? TPR : 1];   // [sum and vector][half][lane]
   const int t = row_lane<TPR>(), sub = row_sub<TPR>(), lanes = row_lanes<TPR>();
@@ -361,10 +363,15 @@ hipError_t launch_rows_sum(DType dt, int outputs, const RowsSum& p, hipStream_t 
 
 // Lanes per row and vectors per lane by the row's length; from 2049 values on as
 // many waves as its vectors need.  The gradient holds its registers for two
-// (two vectors) or three (one) waves a SIMD; measured in bf16, 2^26 values, us:
-// rows of 2304 326 in two, 458 in one, 4096 173 and 214, 5120 268 and 225, 6144
-// 239 and 199 (a few waves of two vectors leave SIMDs idle), 8192 202 in two; two
-// vectors within the registers of three waves a SIMD spill: 4096 336.
+// (two vectors) or three (one) waves a SIMD.  It in bf16, 2^26 values, us: rows of
+// 2304 370 in two, 522 in one, 3000 306 and 447, 4096 211 and 246, 5120 269 and
+// 237, 6144 248 and 225 (a few waves of two vectors leave SIMDs idle).  In fp32,
+// 2^25 values: 246 and 341, 228 and 311, 217 and 209, 214 and 212, 216 and 216:
+// the same choice.  The forward's differ less, and both types share the plan: bf16
+// 137 and 155, 128 and 144, 117 and 113, 116 and 120, 116 and 116, fp32 157 and
+// 129, 146 and 124, 133 and 120, 149 and 136, 142 and 130.  Two vectors within the
+// registers of three waves a SIMD spill: 4096 336, where these took 173 (x for the
+// gate, h for d_res).
 static bool block_norm_single(int dim) { return dim <= 2048 || (dim > 4096 && dim <= 6144); }
 int block_norm_threads(int dim) { return dim <= 2048 ? 256 : block_norm_single(dim) ? (dim + 511) / 512 * 64 : (dim + 1023) / 1024 * 64; }
 #define BLOCK_NORM_DISPATCH(CALL)              \

@@ -139,11 +139,15 @@ __device__ __forceinline__ void i8_landed() {
 // bytes of k of which each of the four waves multiplies 64.  Direct copies of
 // whole rows bring the steps into LDS, ST - 1 ahead; nothing in LDS is read
 // twice, and the waves' sums meet at the end.  Row r's 16-byte piece c stands
-// at c ^ stage_swz<16>(r % 16).  Bound by the copies, of the weight from memory
-// and, from 100 rows on, of x from the cache: 4096 -> 8192, 1 row 8.9 us (floor
-// 6.5), 100 rows 12.3, 256 rows 17.4.  Operands read straight into registers
-// took 8.8, 19.4 and 41 (a lane's 16 bytes of 16 rows are 64 requests); more
-// steps ahead (9, 6 and 4 buffers for 6, 4 and 3) 9.2, 12.8 and 18.5.
+// at c ^ stage_swz<16>(r % 16).  4096 -> 8192, 1 row 8.9 us (bound by the weight:
+// 5.1 at the rate of reads alone, and the launch), 100 rows 12.3, 256 rows 17.4.
+// Operands read straight into registers took 8.8, 19.4 and 41 (a lane's 16 bytes of
+// 16 rows are 64 requests); more steps ahead (9, 6 and 4 buffers for 6, 4 and 3)
+// 9.2, 12.8 and 18.5.  What bounds 100 rows is not shown: the 655 KB that a compute
+// unit copies are 4.3 us at 64 bytes a clock, its round takes 8; 1.08 million
+// requests of 128 bytes to L2 (a quarter of them on to memory) return after 490
+// clocks each, which the two steps of 40 KB ahead would cover, and waves wait to
+// issue for 45 % of their time.
 template <typename T, int MT, int NT, int ST>
 __global__ __launch_bounds__(256) void k_i8_some(I8Params p) {
   constexpr int NW = 4, KS = 64 * NW, R = 16 * (MT + NT), C = R / 4 / NW, TILES = MT * NT;   // C: 1 KB copies a wave and step
@@ -219,9 +223,11 @@ __global__ __launch_bounds__(256) void k_i8_some(I8Params p) {
 // ((r % 16) / 4) + 4 (r / 16) + r % 4, so that a lane's values of one m over its
 // NT tiles are 4 NT consecutive n.
 //
-// 8192 x 4096 -> 8192: 235 us (2.35e15 operations a second), 8192^3 420 (2.6e15);
-// a tile's first copies and its outputs are the rest.  Of its variants, where
-// this loop took 249: operands read where they are used 304; steps of 64 k in
+// 8192 x 4096 -> 8192: 223 to 251 us by the data and the run (2.2e15 to 2.5e15
+// operations a second; outputs in fp32 282), 8192^3 410 (2.7e15).  The matrix unit
+// is busy 54 % of that; products alone, from registers, reach 3.9e15 with 16 or
+// more accumulators a wave (2.2e15 to 2.6e15 with 8 and fewer), and so do those of
+// 32 x 32 x 32.  Of its variants, where this loop took 249: operands read where they are used 304; steps of 64 k in
 // four buffers 346 (rows of 64 bytes are read at half the rate); copies between
 // the products, or behind an earlier second barrier, 273 and 265; persistent
 // workgroups with the next tile's first copies ahead of the outputs 272; waves of
@@ -392,6 +398,10 @@ static void i8_many(I8Params p, hipStream_t st) {
 // some 3 for all):
 //   x rows by weight rows    32 x 32   64 x 32   128 x 32   128 x 64   128 x 128   256 x 256
 //   a round                     6         7         8         12.5        20           57
+// The order of the rounds is that of other k too: of 56 cases (k of 512, 1024,
+// 4096 and 16384, 1 to 2048 rows, 2048 and 8192 columns) this choice was within 0.8
+// us or 4 % of the fastest in all but one (1024 rows, 512 -> 2048: 10.5 us, 8.0 in
+// 128 x 128).
 // Measured, us a call, 4096 -> 8192: 17 rows 9.3 (64 x 32: 9.8), 40 rows 10.0 (32
 // x 32: 14, 128 x 32: 11.3), 100 rows 12.5 (64 x 32: 17.4, 128 x 64: 16.5), 256
 // rows 18.1 (128 x 32: 26, 128 x 128: 24.9), 512 rows 27.8 (128 x 64: 33.5, 256 x

@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256) void k_lin_clear(LinParams p) {
 // tiles taken and not yet finished the one taken first waits for finished ones
 // only (none is taken by a workgroup that does not run).
 //
-// 8192 x 4096 in bf16: 80 us (3.3 TB/s), 65536 x 2560 362 (3.7); without the
+// 8192 x 4096 in bf16: 80 us (3.3 TB/s), 65536 x 2560 360 (3.7); without the
 // waits 65 and 288.  Two passes (the tiles' words, a join, the outputs) took 111
 // and 477, as the values are made twice; tiles of 64 tokens 88 and 447, which
 // wait more often; one counter for all columns 93 and 383 (512 workgroups that
@@ -455,7 +455,8 @@ __global__ __launch_bounds__(1024) void k_lin_join(LinParams p) {
 // OUT false: what each tile does to the state (P, S) and to its gradient (P, Q:
 // what it hands on to the tile before it, from zero).  Both directions cannot
 // be had in one pass, as tiles would wait for each other.  32768 x 4096 in bf16:
-// 236 us (4.5 TB/s), the join 21, this pass 380 (4.9 TB/s), dA 11.  With eight
+// 236 us (4.5 TB/s), the join 21 to 23, this pass 380 to 408 by the run (4.6 to 4.9
+// TB/s), dA 9 to 11.  With eight
 // tokens a wave one workgroup of 152 registers is resident and not two (475); in
 // workgroups of four waves 355, and the shorter tiles' joins take that again.
 // Values made again for the walk backwards instead of held took 643.
@@ -622,7 +623,7 @@ __global__ __launch_bounds__(64 * NW, OUT ? 4 : 6) void k_lin_bwd(LinParams p) {
 }
 
 // One new token per row; a wave takes 128 channels of one row.  Bound by the
-// launch: 256 x 4096 in bf16 6.3 us (16 MB, 3.2 at a copy's rate), one row 3 (7.8
+// launch: 256 x 4096 in bf16 6.3 us (17 MB, 3.0 at the rate of such streams), one row 3 (7.8
 // a call).
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_step(LinParams p) {

@@ -389,7 +389,9 @@ typedef struct {
 
 /* Bytes of device workspace the forward needs (0 on invalid arguments).  Calls
  * that overlap in time need workspaces of their own, as everywhere: tiles of one
- * prompt tell each other through it how far they are. */
+ * prompt tell each other through it how far they are.  Calls that share one all
+ * the same end (the waits between tiles are bounded) and report nothing: their
+ * values mean nothing, NaN among them. */
 size_t gdr_linear_scan_fwd_workspace_size(const gdr_linear_scan_shape* shape);
 
 /*   x, r, i                      [B, T, D], strided;  A [D] fp32
