@@ -227,11 +227,11 @@ __global__ __launch_bounds__(256) void k_i8_some(I8Params p) {
 // operations a second; outputs in fp32 282), 8192^3 410 (2.7e15).  The matrix unit
 // is busy 54 % of that; products alone, from registers, reach 3.9e15 with 16 or
 // more accumulators a wave (2.2e15 to 2.6e15 with 8 and fewer), and so do those of
-// 32 x 32 x 32.  Of its variants, where this loop took 249: operands read where they are used 304; steps of 64 k in
-// four buffers 346 (rows of 64 bytes are read at half the rate); copies between
-// the products, or behind an earlier second barrier, 273 and 265; persistent
-// workgroups with the next tile's first copies ahead of the outputs 272; waves of
-// 64 x 128 288.
+// 32 x 32 x 32.  Of its variants, where this loop took 249: operands read where
+// they are used 304; steps of 64 k in four buffers 346 (rows of 64 bytes are read
+// at half the rate); copies between the products, or behind an earlier second
+// barrier, 273 and 265; persistent workgroups with the next tile's first copies
+// ahead of the outputs 272; waves of 64 x 128 288.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_i8_many(I8Params p) {
   constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16, KS = 128;

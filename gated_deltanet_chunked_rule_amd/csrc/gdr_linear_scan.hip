@@ -11,9 +11,9 @@
 // run that starts or ends a sequence does not depend on what is before it:
 // its P is kFresh, and S stands alone (a product with zero would carry a NaN
 // of another sequence over).  A product of positive decays stays positive: one
-// that falls below fp32's smallest value, 2^-149, counts as that, so that
-// an infinite state stays infinite across runs as it does token by token, and only
-// a decay that is zero makes it NaN (a finite state adds 2^-149 of itself at most,
+// that falls below fp32's smallest value, 2^-149, counts as that, so that an
+// infinite state stays infinite across runs as it does token by token, and only a
+// decay that is zero makes it NaN (a finite state adds 2^-149 of itself at most,
 // as the rounding of a product next to that size does).
 #include "gdr_layer.h"
 
@@ -178,7 +178,7 @@ template <int N, typename F> __device__ __forceinline__ LinRun lin_joined(int n,
       P *= r.P;
       low = min(low, __builtin_bit_cast(int, r.P));
     }
-  return {low < 0 ? kFresh : lin_product(P, low), S};   // kFresh is the only one below zero
+  return {low < 0 ? kFresh : lin_product(P, low), S};   // below zero is kFresh alone, or a NaN with a sign, whose S is NaN and stands alone too
 }
 __device__ __forceinline__ float lin_after(float h, float P, float S) { return P == kFresh ? S : fmaf(P, h, S); }
 

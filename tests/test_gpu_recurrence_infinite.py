@@ -67,3 +67,26 @@ def test_a_decay_of_zero_makes_an_infinite_state_nan():
     A = torch.full((D,), -200.0)
     y, _ = gdr.gdr_linear_scan_fwd(*(cuda(t) for t in (x, r, i, A)))
     assert bool((y[0, :1500] == INF).all()) and bool(torch.isnan(y[0, 1500:]).all())
+
+
+def test_nan_of_either_sign_stays_to_the_end_of_its_sequence():
+    g = gen(31)
+    T, D, cu = 5000, 12, [0, 4000, 4980]
+    x, r, i, dy = (randn(g, 1, T, D) for _ in range(4))
+    A, h0 = torch.full((D,), -0.5), randn(g, 2, D)
+    want, behind = torch.zeros(T, D, dtype=torch.bool), torch.zeros(T, D, dtype=torch.bool)
+    for t, channel, bits in ((100, 3, 0x7fc00000), (100, 4, -0x400000), (3999, 5, -0x400000), (4000, 6, -1), (4979, 7, 0x7fffffff)):
+        end = 4000 if t < 4000 else 4980
+        r.view(torch.int32)[0, t, channel] = bits             # the decay is NaN
+        want[t:end, channel] = True
+        behind[(0 if t < 4000 else 4000):end, channel] = True
+    table = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    y, ht = gdr.gdr_linear_scan_fwd(*(cuda(t) for t in (x, r, i, A)), cuda(h0), table, output_final_state=True)
+    assert torch.equal(torch.isnan(y[0]).cpu(), want)
+    assert torch.equal(torch.isnan(ht).cpu(), torch.stack([want[3999], want[4979]]))
+    grads = gdr.gdr_linear_scan_bwd(*(cuda(t) for t in (x, r, i, A, dy)), cuda(h0), None, table)
+    first = torch.stack([behind[3999], behind[4979]])
+    assert torch.equal(torch.isnan(grads[4]).cpu(), first)     # every gradient in front goes through that decay
+    for t in grads[:3]:
+        assert not torch.isnan(t[0].cpu()[~behind]).any()
+    assert torch.equal(torch.isnan(grads[3]).cpu(), first.any(0))
