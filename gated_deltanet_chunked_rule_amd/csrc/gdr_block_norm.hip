@@ -90,7 +90,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockN
     for (int c = 0; c < 8; ++c) ss[0] = fmaf(h[v][c], h[v][c], ss[0]);
   }
   row_sums<TPR, 1>(ss, red[0]);
-  const float rx = __builtin_amdgcn_rsqf(fmaf(ss[0], p.inv_dim, p.eps));   // an ulp
+  const float rx = rsqrt_f(fmaf(ss[0], p.inv_dim, p.eps));
   ss[0] = 0.f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_fwd(BlockN
     for (int c = 0; c < 8; ++c) ss[0] = fmaf(h[v][c], h[v][c], ss[0]);
   }
   row_sums<TPR, 1>(ss, red[1]);
-  const float rh = __builtin_amdgcn_rsqf(fmaf(ss[0], p.inv_dim, p.eps));
+  const float rh = rsqrt_f(fmaf(ss[0], p.inv_dim, p.eps));
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int d = (v * lanes + t) * 8, nd = min(8, p.dim - d);
@@ -223,8 +223,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm_bwd(BlockN
       }
     }
     row_sums<TPR, 3>(s3, red3[buf]);   // two buffers: the next row's sums do not meet this one's readers
-    const float rh = __builtin_amdgcn_rsqf(fmaf(s3[0], p.inv_dim, p.eps)), mh = s3[1] * rh * p.inv_dim;
-    const float rx = __builtin_amdgcn_rsqf(fmaf(s3[2], p.inv_dim, p.eps));
+    const float rh = rsqrt_f(fmaf(s3[0], p.inv_dim, p.eps)), mh = s3[1] * rh * p.inv_dim;
+    const float rx = rsqrt_f(fmaf(s3[2], p.inv_dim, p.eps));
     float dh[NV][8], s1[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

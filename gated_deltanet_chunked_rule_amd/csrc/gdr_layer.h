@@ -293,6 +293,13 @@ __device__ __forceinline__ void vec_store(T* p, int n, const float (&f)[VEC]) {
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 // 1 / (1 + e^-x), with the hardware's exp2 and reciprocal (one ulp each)
 __device__ __forceinline__ float sigmoid_f(float x) { return __builtin_amdgcn_rcpf(1.f + exp_f(-x)); }
+// 1 / sqrt(v) for v >= 0, an ulp.  The instruction takes what lies below the normal
+// numbers as zero, so small v are scaled by 2^64 and the root's 2^32 taken back.
+__device__ __forceinline__ float rsqrt_f(float v) {
+  const bool small = v < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v);
+  return small ? r * 0x1p32f : r;
+}
 // log(1 + e^x); above 20 it equals x in fp32.  With u = e^x and w = 1 + u
 // rounded, log(w) u / (w - 1) takes back the rounding of w (the correction of
 // Goldberg's "What every computer scientist should know about floating-point

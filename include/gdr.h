@@ -429,7 +429,7 @@ typedef struct {
   int64_t rows;
   int32_t dim;
   gdr_dtype dtype;            /* of all tensors and gradients */
-  float eps;                  /* >= 0 */
+  float eps;                  /* >= 0 (rows whose squares fp32 holds with few bits, from 1e-19 on down, are as exact as those) */
   int64_t x_stride, residual_stride, gate_stride;  /* elements between rows (0: dim) */
 } gdr_block_norm_shape;
 
