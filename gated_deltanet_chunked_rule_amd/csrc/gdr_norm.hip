@@ -167,7 +167,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(NormParams p
     } else {
       row_sum2<TPR>(ss, unused, red);
     }
-    const float r = __builtin_amdgcn_rsqf(fmaf(ss, p.inv_dim, p.eps));   // an ulp
+    const float r = rsqrt_f(fmaf(ss, p.inv_dim, p.eps));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int d = (v * TPR + t) * 8, nd = min(8, p.dim - d);
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(NormParams p
     }
     if (AHEAD && base + step < p.rows) fetch(row + step);
     row_sum2<TPR>(ss, su, red[buf]);   // two buffers: the next step's sums do not meet this step's readers
-    const float r = __builtin_amdgcn_rsqf(fmaf(ss, inv, p.eps));   // an ulp
+    const float r = rsqrt_f(fmaf(ss, inv, p.eps));
     const float m = su * r * inv;      // mean(u n)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

@@ -347,7 +347,7 @@ typedef struct {
   int32_t inner;              /* rows per outer step (heads), >= 1; rows % inner == 0 */
   int32_t dim;
   gdr_dtype dtype;            /* of x, residual, gate, weight, 16- or 32-bit outputs and gradients */
-  float eps;                  /* >= 0 */
+  float eps;                  /* >= 0 (rows whose squares fp32 holds with few bits, from 1e-19 on down, are as exact as those) */
   int32_t quant;              /* 1: y in 8 bits (e4m3) with an fp32 scale for each 128 values of a row */
   gdr_row_stride x_stride, residual_stride, gate_stride;
 } gdr_norm_shape;
